@@ -27,7 +27,9 @@ __all__ = [
     "FD_FLAG_CUDA_CORES", "FD_FLAG_NO_4D_BOXES", "FD_FLAG_NO_HEAD_FUSION", "FD_FLAG_NO_GATHER",
     "FD_FLAG_FUSE_HEADS", "FD_FLAG_NO_PREFETCH", "FD_FLAG_TMEM_SCORES", "FD_FLAG_NO_TMEM_SCORES", "FD_KV_AS_Q", "FD_KV_FP8_E4M3", "FD_KV_FP8_E5M2",
     "fd_decode_noalloc", "fd_decode_partial", "fd_decode_paged_partial", "fd_merge_partials",
-    "KV_END",
+    "KV_END", "fd_build_tables", "fd_cache_write", "fd_cache_compact", "fd_tree_workspace_size",
+    "make_tree_workspace", "fd_tree_decode", "fd_tree_decode_paged", "Tables", "FD_DEVICE_STATUS_BAD_LENGTH",
+    "FD_DEVICE_STATUS_NO_PAGES", "FD_DEVICE_STATUS_BAD_SLOT",
 ]
 
 FD_OK, FD_ERR_INVALID_ARG, FD_ERR_UNSUPPORTED, FD_ERR_WORKSPACE_TOO_SMALL = 0, 1, 2, 3
@@ -45,6 +47,7 @@ FD_KV_AS_Q, FD_KV_FP8_E4M3, FD_KV_FP8_E5M2 = 0, 1, 2
 KV_END = 2 ** 31 - 1   # kv_end of a range that runs to the end of every request
 
 _P, _I, _F, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_LL = ctypes.c_longlong
 
 
 class FdOptions(ctypes.Structure):
@@ -87,6 +90,21 @@ def _load():
     lib.fd_merge_partials.restype = _I
     lib.fd_decode_noalloc.argtypes = [_P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P, _P, _P, _P]
     lib.fd_decode_noalloc.restype = _I
+    lib.fd_build_tables.argtypes = [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P]
+    lib.fd_build_tables.restype = _I
+    lib.fd_cache_write.argtypes = [_P, _P, _LL, _LL, _P, _I, _I, _I, _P, _P, _LL, ctypes.POINTER(FdOptions), _P, _P]
+    lib.fd_cache_write.restype = _I
+    lib.fd_cache_compact.argtypes = [_P, _P, _P, _I, _I, _I, _P, _P, _I, _P, _P, _I, _I, _I, _I, _P,
+                                     ctypes.POINTER(FdOptions), _P, _P]
+    lib.fd_cache_compact.restype = _I
+    lib.fd_tree_workspace_size.argtypes = [_I, _I, _I, _I, _I]
+    lib.fd_tree_workspace_size.restype = _SZ
+    lib.fd_tree_decode.argtypes = [_P, _P, _P, _P, _LL, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _SZ,
+                                   ctypes.POINTER(FdOptions), _P]
+    lib.fd_tree_decode.restype = _I
+    lib.fd_tree_decode_paged.argtypes = [_P, _P, _P, _P, _I, _P, _LL, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F,
+                                         _P, _P, _P, _SZ, ctypes.POINTER(FdOptions), _P]
+    lib.fd_tree_decode_paged.restype = _I
     lib.fd_get_device_error.argtypes = [_P, _P]
     lib.fd_get_device_error.restype = _I
     lib.fd_status_string.argtypes = [_I]
@@ -427,3 +445,8 @@ def fd_decode_noalloc(q, k, v, seq_lens, o, lse=None, device_status=None, scale=
 def fd_get_device_error(workspace, stream=None) -> int:
     """Read and clear the workspace's sticky device-error word (synchronises the stream)."""
     return int(_lib.fd_get_device_error(_ptr(workspace), _stream_ptr(stream, workspace.device)))
+
+
+from .speculative import (FD_DEVICE_STATUS_BAD_LENGTH, FD_DEVICE_STATUS_BAD_SLOT,  # noqa: E402
+                          FD_DEVICE_STATUS_NO_PAGES, Tables, fd_build_tables, fd_cache_compact, fd_cache_write,
+                          fd_tree_decode, fd_tree_decode_paged, fd_tree_workspace_size, make_tree_workspace)

@@ -419,6 +419,185 @@ fd_status fd_decode_noalloc(const void *q, const void *k, const void *v,
                             int num_kv_heads, int head_dim, int s_max, float scale, float *o,
                             float *lse, unsigned int *device_status, fd_stream_t stream);
 
+/* More bits of a device status word (fd_build_tables, fd_cache_write,
+ * fd_cache_compact OR them into *device_status). */
+#define FD_DEVICE_STATUS_NO_PAGES 0x4u    /* the free pages ran out */
+#define FD_DEVICE_STATUS_BAD_SLOT 0x8u    /* a slot, page or path entry was out of range */
+
+/*
+ * ---- A step of speculative decoding over a cache ----
+ *
+ * Four calls around the attention: fd_build_tables gives the new tokens their
+ * pages and slots, fd_cache_write fills the slots, fd_tree_decode (or the
+ * paged form) attends the drafted tokens to the cache and to one another, and
+ * fd_cache_compact keeps the accepted path.  The sources this library follows
+ * have no counterpart to them; the arithmetic of fd_tree_decode is fd_decode's.
+ *
+ * They follow the conventions at the top of this file, and:
+ *   - device_status: NULL, or a device uint32 into which a call ORs its
+ *     FD_DEVICE_STATUS_* bits, stream-ordered (the caller zeroes it).
+ *   - The stream must belong to the current device, as for every call here.
+ *   - Inputs and outputs of one call must not overlap unless an argument says so.
+ */
+
+/*
+ * Block tables and slot maps from request lengths, on the device.
+ *
+ * Request b holds seq_lens[b] tokens in its first held_pages[b] pages and gets
+ * new_lens[b] more.  It needs
+ *     n_b = max(0, ceil((seq_lens[b] + new_lens[b]) / page_size) - held_pages[b])
+ * new pages; they come from the end of the stack free_pages[0 .. *free_count),
+ * request by request and page by page:
+ *     block_table[b][held_pages[b] + j] = free_pages[*free_count - 1 - (n_0 + .. + n_{b-1}) - j],  j < n_b.
+ * Its new tokens i = 0 .. new_lens[b] - 1 (positions seq_lens[b] + i) get the slots
+ *     slot_map[cu_new_lens[b] + i] = block_table[b][pos / page_size] * page_size + pos % page_size.
+ *
+ *   seq_lens, new_lens [batch] int32, device.
+ *   held_pages   [batch] int32, device, or NULL: ceil(seq_lens[b] / page_size).
+ *                More than that is usual after drafted tokens were rejected.
+ *   free_pages   [max_free] int32, device; free_count int32 [1], device.  The
+ *                count is clamped to [0, max_free].
+ *   block_table  [batch, max_blocks_per_seq] int32, device: the entries of held
+ *                pages are read, those of new pages written, the others left.
+ *   slot_map     [max_tokens] int64, device, written: entries behind the last
+ *                token are -1 (so a captured call of fixed size can follow).
+ *   cu_new_lens  [batch + 1] int32, written: prefix sums of new_lens.
+ *   seq_lens_out, held_pages_out [batch] and free_count_out [1] int32, written:
+ *                the state after the call.  They must not overlap the inputs.
+ * When the free pages run out, requests are served in order; a page that none
+ * is left for becomes -1 in the table, the slots in it -1, seq_lens_out[b]
+ * counts the tokens before the first missing page, held_pages_out[b] the pages
+ * that b has, and FD_DEVICE_STATUS_NO_PAGES is reported.  A negative length, or
+ * one that passes the table (max_blocks_per_seq * page_size) or, summed,
+ * max_tokens is clamped and reported as FD_DEVICE_STATUS_BAD_LENGTH, and so is
+ * a held_pages[b] outside [ceil(seq_lens[b] / page_size), max_blocks_per_seq].
+ * A page outside [0, num_pages) gives slots of -1 and FD_DEVICE_STATUS_BAD_SLOT.
+ * batch <= 4096; page_size >= 1; num_pages * page_size may pass 2^31.  batch = 0
+ * fills slot_map with -1 and copies the free count.
+ */
+fd_status fd_build_tables(const int32_t *seq_lens, const int32_t *new_lens, const int32_t *held_pages,
+                          const int32_t *free_pages, const int32_t *free_count, int max_free,
+                          int batch, int page_size, int num_pages, int max_blocks_per_seq,
+                          int max_tokens, int32_t *block_table, int64_t *slot_map,
+                          int32_t *cu_new_lens, int32_t *seq_lens_out, int32_t *held_pages_out,
+                          int32_t *free_count_out, unsigned int *device_status, fd_stream_t stream);
+
+/*
+ * Write num_tokens new K and V rows into a cache of num_slots slots: a
+ * contiguous cache [batch, s_max, Hkv, D] (slot b * s_max + t) or pages
+ * [num_pages, P, Hkv, D] (slot page * P + t), as fd_build_tables numbers them.
+ *   k_new, v_new [num_tokens, Hkv, D] of type opts->dtype, device; token rows of
+ *                Hkv * D elements are k_stride and v_stride elements apart (e.g.
+ *                slices of a fused projection's output).  Strides are
+ *                multiples of 8 elements, at least Hkv * D (any when num_tokens <= 1).
+ *   slot_map     [num_tokens] int64, device.  A negative slot skips its token; one
+ *                >= num_slots too, and is reported as FD_DEVICE_STATUS_BAD_SLOT.
+ *                Slots >= 0 must differ: the row of a slot given twice is a mix
+ *                of both tokens' 16-byte pieces.
+ *   k_cache, v_cache [num_slots, Hkv, D], device: of the type of k_new, or FP8
+ *                codes (opts->kv_dtype), code = round(x / scale) with the call's
+ *                k_scale or v_scale: an fp32 division, nearest even, values past
+ *                the largest finite code (infinities too) become that code, NaN
+ *                stays NaN.  Slots that are not named keep their bytes.
+ *   opts         NULL or options; dtype, kv_dtype, k_scale and v_scale are used.
+ * head_dim 64, 128 or 256.
+ */
+fd_status fd_cache_write(const void *k_new, const void *v_new, long long k_stride, long long v_stride,
+                         const int64_t *slot_map, int num_tokens, int num_kv_heads, int head_dim,
+                         void *k_cache, void *v_cache, long long num_slots, const fd_options *opts,
+                         unsigned int *device_status, fd_stream_t stream);
+
+/*
+ * Keep the accepted path of a drafted tree: the rows of the accepted nodes move
+ * to the front of the drafted tail, in place, in K and in V.  Request b holds
+ * L_b = seq_lens[b] tokens, the last t_b of them drafted (base = L_b - t_b):
+ *     row base + j  <-  row base + accepted[b][j],   j < accept_lens[b]
+ *     seq_lens_out[b] = base + accept_lens[b]
+ *   k_cache, v_cache the cache: block_table NULL: [batch, s_max, Hkv, D] with
+ *                page_size = s_max (max_blocks_per_seq and num_pages are ignored);
+ *                else pages [num_pages, page_size, Hkv, D] behind
+ *                block_table [batch, max_blocks_per_seq] int32.
+ *   seq_lens     [batch] int32, device; tree_lens [batch] int32, device, or NULL:
+ *                every request drafted tree_len tokens.
+ *   accepted     [batch, max_accept] int32, device: node indices in [0, t_b),
+ *                strictly ascending; entries behind accept_lens[b] are not read.
+ *   accept_lens  [batch] int32, device, in [0, min(max_accept, t_b)].
+ *   seq_lens_out [batch] int32, written; must not overlap seq_lens.
+ *   opts         dtype and kv_dtype give the cache's element type.
+ * A length outside its range (t_b > L_b and accept_lens[b] > t_b too) is clamped
+ * and reported as FD_DEVICE_STATUS_BAD_LENGTH.  A path ends before its first
+ * entry that is out of range or not ascending, and before the first whose page
+ * (its own, or the one it moves to) is outside [0, num_pages); seq_lens_out counts
+ * what was kept and FD_DEVICE_STATUS_BAD_SLOT is reported.  Requests must not
+ * share the pages of their drafted tokens.
+ */
+fd_status fd_cache_compact(void *k_cache, void *v_cache, const int32_t *block_table,
+                           int max_blocks_per_seq, int page_size, int num_pages,
+                           const int32_t *seq_lens, const int32_t *tree_lens, int tree_len,
+                           const int32_t *accepted, const int32_t *accept_lens, int max_accept,
+                           int batch, int num_kv_heads, int head_dim, int32_t *seq_lens_out,
+                           const fd_options *opts, unsigned int *device_status, fd_stream_t stream);
+
+/* Bytes of workspace that fd_tree_decode / fd_tree_decode_paged need for a
+ * shape; initialise it once with fd_workspace_init.  Pure host function; 0 for
+ * shapes that no call accepts. */
+size_t fd_tree_workspace_size(int batch, int tree_len, int num_q_heads, int num_kv_heads, int head_dim);
+
+/*
+ * Attention of a tree of drafted tokens over a contiguous cache.  The cache of
+ * length L_b already holds the request's t_b drafted tokens ("nodes") as its
+ * last positions: node i sits at L_b - t_b + i.  Node i of query head h attends
+ * to every position before the nodes, and to node j when bit j of its mask row
+ * is set:
+ *     s_p = scale * q[b,i,h] . K_b[p, g],  p < L_b - t_b, or p = L_b - t_b + j with the bit set
+ *     O = softmax(s) V,  LSE = ln sum exp(s)                      (fp32)
+ * For any mask (a tree's: a node's ancestors and itself); no bit is implied.
+ *   q            [batch, tree_len, num_q_heads, head_dim] bf16 or fp16, device.
+ *   tree_mask    [batch, tree_len, W] uint64, device, W = ceil(tree_len / 64): bit
+ *                j % 64 of word j / 64 of row i says whether node i sees node j.
+ *                Bits j >= t_b are ignored.  NULL: the causal chain (j <= i), as
+ *                fd_decode with q_len = tree_len, for more query columns.
+ *   mask_stride  words between two requests' masks: tree_len * W, or 0 when all
+ *                requests share one mask [tree_len, W]; other strides >= tree_len * W
+ *                are accepted.
+ *   tree_lens_dev [batch] int32, device: t_b in [0, tree_len] (clamped and reported
+ *                as FD_ERR_DEVICE_INPUT otherwise); NULL: t_b = tree_len.
+ *   o            [batch, tree_len, num_q_heads, head_dim] fp32; lse [batch, tree_len,
+ *                num_q_heads] fp32, natural log, or NULL.  Written whole: a row that
+ *                sees nothing (i >= t_b, a node before the cache's start when
+ *                L_b < t_b, an empty mask row without context) gets O = 0 and
+ *                LSE = -inf.
+ *   workspace    at least fd_tree_workspace_size(...) bytes, as for fd_decode (its
+ *                error word is read with fd_get_device_error).
+ *   opts         as for fd_decode; q_len must be 0 or 1 (tree_len replaces it).
+ *                No user flag changes the call.
+ *   The other arguments are fd_decode's.
+ * Any whole group Hq/Hkv; tree_len 1 .. 256; tree_len * Hq/Hkv <= 4096; batch
+ * <= 4096; head_dim 64, 128 or 256; bf16, fp16 or FP8 caches.  What the cache
+ * holds at positions that no row sees (behind L_b, nodes without a set bit in
+ * any row) does not matter, and what a node holds does not reach the rows that
+ * do not see it, not-a-numbers included.
+ */
+fd_status fd_tree_decode(const void *q, const void *k, const void *v, const uint64_t *tree_mask,
+                         long long mask_stride, const int32_t *tree_lens_dev,
+                         const int32_t *seq_lens_dev, const int32_t *seq_lens_host, int batch,
+                         int tree_len, int num_q_heads, int num_kv_heads, int head_dim, int s_max,
+                         float scale, float *o, float *lse, void *workspace, size_t workspace_bytes,
+                         const fd_options *opts, fd_stream_t stream);
+
+/* fd_tree_decode over a paged cache: k_pages, v_pages, block_table,
+ * max_blocks_per_seq, page_size and num_pages as for fd_decode_paged (an entry
+ * outside [0, num_pages) is replaced by page 0 and reported as
+ * FD_ERR_DEVICE_INPUT), except that any of its page sizes goes with any cache. */
+fd_status fd_tree_decode_paged(const void *q, const void *k_pages, const void *v_pages,
+                               const int32_t *block_table, int max_blocks_per_seq,
+                               const uint64_t *tree_mask, long long mask_stride,
+                               const int32_t *tree_lens_dev, const int32_t *seq_lens_dev,
+                               const int32_t *seq_lens_host, int batch, int tree_len, int num_q_heads,
+                               int num_kv_heads, int head_dim, int page_size, int num_pages,
+                               float scale, float *o, float *lse, void *workspace,
+                               size_t workspace_bytes, const fd_options *opts, fd_stream_t stream);
+
 /*
  * Read and clear the sticky device-error word of a workspace: FD_OK,
  * FD_ERR_TIMEOUT or FD_ERR_DEVICE_INPUT (timeout wins if both happened).
