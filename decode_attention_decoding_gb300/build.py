@@ -3,8 +3,9 @@
 Usage: ``python -m decode_attention_decoding_gb300.build`` or call :func:`build`.
 Each translation unit is compiled by its own nvcc process, in parallel, then
 linked into ``decode_attention_decoding_gb300/libfd.so``.  ``fd_split_inst.cu``
-is compiled once per split-kernel variant (layout x K/V element type x head_dim),
-each with its own defines.  Objects go to ``decode_attention_decoding_gb300/_build/``.
+is compiled once per split-kernel variant (layout x K/V element type x head_dim)
+and ``fd_tree_inst.cu`` once per tree-kernel variant (how the cache is loaded x
+head_dim), each with its own defines.  Objects go to ``decode_attention_decoding_gb300/_build/``.
 """
 from __future__ import annotations
 
@@ -36,6 +37,9 @@ def _nvcc() -> str:
 
 SPLIT_INST = "fd_split_inst.cu"
 KV_NAMES = ("bf16", "f16", "e4m3", "e5m2")
+TREE_INST = "fd_tree_inst.cu"
+TREE_LOADS = ("tma", "pages", "e4m3", "e5m2")   # 16-bit by TMA, 16-bit by loader threads, FP8 codes
+TREE_VARIANTS = [(load, d) for load in range(4) for d in (64, 128, 256)]
 SPLIT_VARIANTS = [(paged, kv, d) for paged in (0, 1) for kv in range(4) for d in (64, 128, 256)]
 
 
@@ -53,6 +57,10 @@ def _units():
                 defs = [f"-DFD_INST_PAGED={'true' if paged else 'false'}", f"-DFD_INST_KV={kv}",
                         f"-DFD_INST_D={d}"]
                 units.append((src, f"{stem}_{'paged' if paged else 'contig'}_{KV_NAMES[kv]}_d{d}", defs))
+        elif os.path.basename(src) == TREE_INST:
+            for load, d in TREE_VARIANTS:
+                units.append((src, f"{stem}_{TREE_LOADS[load]}_d{d}",
+                              [f"-DFD_TREE_LOAD={load}", f"-DFD_TREE_D={d}"]))
         else:
             units.append((src, stem, []))
     return units

@@ -50,7 +50,7 @@ static int kv_elem_bytes(int kv) { return kv_is_fp8(kv) ? 1 : 2; }
 // (token, kv head) pairs of head_dim elements; each load is a box of
 // box_rows tokens of one kv head: the whole row, or (swizzled) one 128-byte
 // part of it with the 128-byte swizzle that the tensor-core consumers read.
-static fd_status encode_kv_map(CUtensorMap *map, const void *base, int hkv, long long rows, int box_rows,
+fd_status encode_kv_map(CUtensorMap *map, const void *base, int hkv, long long rows, int box_rows,
                         bool swizzled, int kv, int d)
 {
     EncodeTiledFn fn = encode_fn();
@@ -224,19 +224,10 @@ fd_status plan_smem(const DeviceInfo &dev, int cons, int group, int d, int elem_
     return launch->smem_bytes <= avail ? FD_OK : FD_ERR_UNSUPPORTED;
 }
 
-}  // namespace fd
-
-namespace {
-
-using namespace fd;
-
-constexpr int kVersion = 10400;   // 1.4.0
-constexpr unsigned long long kDefaultTimeoutNs = 2000000000ull;
-
 // The one piece of state kept across calls: a cache of device properties.
-std::mutex g_dev_mu;
-DeviceInfo g_dev[64];
-bool g_dev_ok[64] = {};
+static std::mutex g_dev_mu;
+static DeviceInfo g_dev[64];
+static bool g_dev_ok[64] = {};
 
 fd_status device_info(DeviceInfo *out)
 {
@@ -256,6 +247,29 @@ fd_status device_info(DeviceInfo *out)
     *out = g_dev[dev];
     return FD_OK;
 }
+
+// Record a caller's timing event on `stream`.  Inside a stream capture the
+// record becomes an event node of the graph (cudaEventRecordExternal), so
+// every replay of the graph records it.
+bool record_event(cudaEvent_t ev, cudaStream_t stream)
+{
+    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(stream, &cs) != cudaSuccess)
+        return false;
+    const cudaError_t e = cs == cudaStreamCaptureStatusActive
+                              ? cudaEventRecordWithFlags(ev, stream, cudaEventRecordExternal)
+                              : cudaEventRecord(ev, stream);
+    return e == cudaSuccess;
+}
+
+}  // namespace fd
+
+namespace {
+
+using namespace fd;
+
+constexpr int kVersion = 10400;   // 1.4.0
+constexpr unsigned long long kDefaultTimeoutNs = 2000000000ull;
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -585,20 +599,6 @@ fd_status fill_plan(CallPlan *cp, const DeviceInfo &dev, const void *q, const in
     mp.kv_begin = sp.kv_begin;
     mp.kv_end = sp.kv_end;
     return FD_OK;
-}
-
-// Record a caller's timing event on `stream`.  Inside a stream capture the
-// record becomes an event node of the graph (cudaEventRecordExternal), so
-// every replay of the graph records it.
-bool record_event(cudaEvent_t ev, cudaStream_t stream)
-{
-    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(stream, &cs) != cudaSuccess)
-        return false;
-    const cudaError_t e = cs == cudaStreamCaptureStatusActive
-                              ? cudaEventRecordWithFlags(ev, stream, cudaEventRecordExternal)
-                              : cudaEventRecord(ev, stream);
-    return e == cudaSuccess;
 }
 
 fd_status run(CallPlan cp, bool paged, const CUtensorMap &tmk, const CUtensorMap &tmv, const fd_options *opts)

@@ -28,6 +28,19 @@ struct DeviceInfo {
     int smem_optin = 0;
 };
 
+// Properties of the current device, cached (fd_api.cu).
+fd_status device_info(DeviceInfo *out);
+
+// Record a caller's timing event on `stream`; inside a stream capture as a
+// node of the graph (fd_api.cu).
+bool record_event(cudaEvent_t ev, cudaStream_t stream);
+
+// Tensor map of one K or V tensor: a rank-3 view {d, hkv, rows} with boxes of
+// box_rows rows of one kv head, whole rows or (swizzled) 128-byte parts
+// (fd_api.cu).
+fd_status encode_kv_map(CUtensorMap *map, const void *base, int hkv, long long rows, int box_rows, bool swizzled,
+                        int kv, int d);
+
 // Calls with fewer (estimated) KV tiles per split CTA than this count as
 // short: they keep less K/V in flight per CTA and kv heads are not fused for
 // them (fd_api.cu).

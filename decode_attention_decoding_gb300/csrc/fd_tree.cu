@@ -6,9 +6,9 @@
 #include <cuda_runtime.h>
 
 #include "fd.h"
-#include "fd_device.cuh"
-#include "fd_sched.h"
+#include "fd_launch.h"
 #include "fd_tree.cuh"
+#include "fd_tree_kernel.cuh"
 
 namespace fd {
 namespace {
@@ -33,7 +33,7 @@ fd_status check_tree(const void *q, const void *k, const void *v, const void *ma
     const long long words = (tree_len + 63) / 64;
     if (mask && mask_stride != 0 && mask_stride < words * tree_len)
         return FD_ERR_INVALID_ARG;
-    if (opts && (opts->num_ctas < 0 || opts->num_ctas > kMaxCtas || opts->dtype < 0 || opts->dtype > 1 ||
+    if (opts && (opts->num_ctas < 0 || opts->num_ctas > kTreeMaxCtas || opts->dtype < 0 || opts->dtype > 1 ||
                  opts->kv_dtype < FD_KV_AS_Q || opts->kv_dtype > FD_KV_FP8_E5M2 || !scale_ok(opts->k_scale) ||
                  !scale_ok(opts->v_scale) || opts->q_len < 0 || opts->q_len > 1))
         return FD_ERR_INVALID_ARG;
@@ -53,20 +53,117 @@ bool host_lens_ok(const int32_t *lens, int batch, long long cap)
     return true;
 }
 
-fd_status launch(TreeParams p, const fd_options *opts, void *workspace, fd_stream_t stream)
+// Shared memory of the split kernel: the query rows, then rings of K and V
+// tiles in what is left, then the barriers.  The odd slot goes to K, whose
+// tiles are wanted a step earlier.
+template <int D>
+void plan_tree_smem(TreeParams *p, TreeLaunch *c)
 {
+    using C = TreeCfg<D, true>;   // the sizes used here do not depend on the loader
+    const size_t q = (size_t)(p->rows / 128) * C::kQBytes, misc = align_up(sizeof(TreeMisc), 16);
+    int slots = (int)((c->smem_optin - q - misc) / C::kSlotBytes);
+    slots = slots < 2 * kTreeMaxSlots ? slots : 2 * kTreeMaxSlots;
+    p->k_slots = (slots + 1) / 2;
+    p->v_slots = slots / 2;
+    p->off_k = (uint32_t)q;
+    p->off_v = (uint32_t)(p->off_k + p->k_slots * C::kSlotBytes);
+    p->off_misc = (uint32_t)(p->off_v + p->v_slots * C::kSlotBytes);
+    c->smem_bytes = p->off_misc + misc;
+}
+
+int slot_rows_of(int rows, int tree_rows) { return tree_rows < rows ? tree_rows : rows; }
+
+// Query rows of a segment: both softmax groups get rows of their own when there are more than 128.
+int segment_rows(int tree_rows, int d) { return d != 256 && tree_rows > 128 ? 256 : 128; }
+
+struct TreeWorkspace {
+    size_t cost, lse, o, sums, total;
+};
+TreeWorkspace tree_workspace(int batch, int tree_rows, int d)
+{
+    const size_t rows = (size_t)slot_rows_of(segment_rows(tree_rows, d), tree_rows) * 2 * kTreeMaxCtas;
+    TreeWorkspace w;
+    w.cost = 256;
+    w.lse = align_up(w.cost + sizeof(long long) * ((size_t)batch + 1), 256);
+    w.o = align_up(w.lse + sizeof(float) * rows, 256);
+    w.sums = align_up(w.o + sizeof(float) * rows * d, 256);
+    w.total = align_up(w.sums + sizeof(float) * kTreeMaxCtas * tree_groups(d) * slot_rows_of(128, tree_rows) * d, 256);
+    return w;
+}
+
+fd_status launch(TreeParams p, int head_dim, float scale, const fd_options *opts, void *workspace, fd_stream_t stream)
+{
+    DeviceInfo dev;
+    fd_status st = device_info(&dev);
+    if (st != FD_OK)
+        return st;
     const bool f16 = opts && opts->dtype == FD_DTYPE_F16;
     const int kv_dtype = opts ? opts->kv_dtype : FD_KV_AS_Q;
     const int kv = kv_dtype == FD_KV_FP8_E4M3 ? kKvE4m3
                    : kv_dtype == FD_KV_FP8_E5M2 ? kKvE5m2 : (f16 ? kKvF16 : kKvBf16);
     const bool fp8 = kv_is_fp8(kv);
-    p.scale *= fp8 && opts->k_scale != 0.f ? opts->k_scale : 1.f;
+    // an FP8 cache's k_scale multiplies every score; a negative scale changes q's sign
+    scale *= fp8 && opts->k_scale != 0.f ? opts->k_scale : 1.f;
+    p.negate_q = scale < 0.f;
+    p.scale_log2 = (p.negate_q ? -scale : scale) * 1.4426950408889634f;
     p.v_scale = fp8 && opts->v_scale != 0.f ? opts->v_scale : 1.f;
-    p.q_f16 = f16;
     p.words = (p.tree_len + 63) / 64;
     p.group = p.hq / p.hkv;
-    p.ws_err = static_cast<unsigned int *>(workspace);
-    return launch_tree_simple(kv, p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? FD_OK : FD_ERR_CUDA;
+    p.timeout_ns = opts && opts->wait_timeout_ns ? opts->wait_timeout_ns : 2000000000ull;
+    p.starve = opts && (opts->flags & FD_FLAG_TEST_STARVE_FIRST_TILE) ? 1 : 0;
+    p.rows = segment_rows(p.tree_len * p.group, head_dim);
+    p.slot_rows = slot_rows_of(p.rows, p.tree_len * p.group);
+    const TreeWorkspace w = tree_workspace(p.batch, p.tree_len * p.group, head_dim);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    p.ws_err = reinterpret_cast<unsigned int *>(ws);
+    p.ws_cost = reinterpret_cast<long long *>(ws + w.cost);
+    p.ws_lse = reinterpret_cast<float *>(ws + w.lse);
+    p.ws_o = reinterpret_cast<float *>(ws + w.o);
+    p.ws_sums = reinterpret_cast<float *>(ws + w.sums);
+    p.sum_rows = slot_rows_of(128, p.tree_len * p.group);
+
+    TreeLaunch c;
+    c.grid = opts && opts->num_ctas > 0 ? opts->num_ctas : dev.sms < kTreeMaxCtas ? dev.sms : kTreeMaxCtas;
+    c.smem_optin = (size_t)dev.smem_optin;
+    c.stream = reinterpret_cast<cudaStream_t>(stream);
+    if (head_dim == 64)
+        plan_tree_smem<64>(&p, &c);
+    else if (head_dim == 128)
+        plan_tree_smem<128>(&p, &c);
+    else
+        plan_tree_smem<256>(&p, &c);
+    if (p.v_slots < 2)
+        return FD_ERR_UNSUPPORTED;
+
+    // FP8 codes and pages under 8 tokens (a box's rows would not reach the
+    // swizzle's 1 KB) come through loader threads, the rest by TMA
+    const bool tma = !fp8 && (!p.block_table || p.page_size >= 8);
+    p.box_rows = p.block_table && p.page_size < kTileTokens ? p.page_size : kTileTokens;
+    alignas(64) CUtensorMap tmk, tmv;
+    std::memset(&tmk, 0, sizeof tmk);
+    std::memset(&tmv, 0, sizeof tmv);
+    if (tma) {
+        long long rows = p.block_table ? (long long)p.num_pages * p.page_size : (long long)p.batch * p.page_size;
+        rows = rows > 0 ? rows : 1;
+        if ((st = encode_kv_map(&tmk, p.k, p.hkv, rows, p.box_rows, true, kv, head_dim)) != FD_OK ||
+            (st = encode_kv_map(&tmv, p.v, p.hkv, rows, p.box_rows, true, kv, head_dim)) != FD_OK)
+            return st;
+    }
+    cudaEvent_t ev0 = opts ? static_cast<cudaEvent_t>(opts->split_start_event) : nullptr;
+    cudaEvent_t ev1 = opts ? static_cast<cudaEvent_t>(opts->split_end_event) : nullptr;
+    if (ev0 && !record_event(ev0, c.stream))
+        return FD_ERR_CUDA;
+    cudaError_t e = cudaErrorInvalidValue;
+#define FD_PICK_TREE(D, F16, KV, TMA)                              \
+    if (head_dim == D && f16 == F16 && kv == KV && tma == TMA)      \
+        e = launch_tree_variant<D, F16, KV, TMA>(p, tmk, tmv, c);
+    FD_TREE_VARIANTS(FD_PICK_TREE)
+#undef FD_PICK_TREE
+    if (e != cudaSuccess)
+        return FD_ERR_CUDA;
+    if (ev1 && !record_event(ev1, c.stream))
+        return FD_ERR_CUDA;
+    return launch_tree_merge(head_dim, p, c.grid, c.stream) == cudaSuccess ? FD_OK : FD_ERR_CUDA;
 }
 
 }  // namespace
@@ -83,7 +180,7 @@ size_t fd_tree_workspace_size(int batch, int tree_len, int num_q_heads, int num_
         (head_dim != 64 && head_dim != 128 && head_dim != 256) ||
         (long long)(num_q_heads / num_kv_heads) * tree_len > kMaxTreeRows)
         return 0;
-    return 256;
+    return tree_workspace(batch, num_q_heads / num_kv_heads * tree_len, head_dim).total;
 }
 
 fd_status fd_tree_decode(const void *q, const void *k, const void *v, const uint64_t *tree_mask,
@@ -115,13 +212,11 @@ fd_status fd_tree_decode(const void *q, const void *k, const void *v, const uint
     p.tree_len = tree_len;
     p.hq = num_q_heads;
     p.hkv = num_kv_heads;
-    p.head_dim = head_dim;
     p.cap = s_max;
     p.page_size = s_max;
-    p.scale = scale;
     p.o = o;
     p.lse = lse;
-    return launch(p, opts, workspace, stream);
+    return launch(p, head_dim, scale, opts, workspace, stream);
 }
 
 fd_status fd_tree_decode_paged(const void *q, const void *k_pages, const void *v_pages, const int32_t *block_table,
@@ -163,12 +258,10 @@ fd_status fd_tree_decode_paged(const void *q, const void *k_pages, const void *v
     p.tree_len = tree_len;
     p.hq = num_q_heads;
     p.hkv = num_kv_heads;
-    p.head_dim = head_dim;
     p.cap = (int)cap;
-    p.scale = scale;
     p.o = o;
     p.lse = lse;
-    return launch(p, opts, workspace, stream);
+    return launch(p, head_dim, scale, opts, workspace, stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,1117 @@
+// fd_tree_kernel.cuh -- the split kernel of the tree attention (sm_103a).
+//
+// One persistent CTA per SM takes a run of tiles (fd_tree.cuh).  Per tile of N
+// positions and 128 query rows:
+//
+//     S = Q K^T        128 x N,  tcgen05, Q and K in shared memory, S in tensor memory
+//     P = exp2(S scale log2(e) - m)   a thread per row: a running maximum m and sum l
+//     O = O + P V      128 x D,  tcgen05, P in tensor memory, V in shared memory
+//
+//   * two loaders bring K and V tiles into rings of shared-memory slots, in the
+//     128-byte swizzled layout that the MMAs read: parts of 64 dims, a part
+//     being N rows of 128 bytes;
+//   * one thread issues the MMAs; their completion releases the slots;
+//   * two groups of 128 threads (one for D = 256, whose accumulator fills half
+//     the tensor memory) hold one query row a thread and turn S into P in
+//     place.  With up to 128 rows both groups have the same rows and take
+//     alternate tiles, each with an accumulator of its own (they are added at
+//     the end of the segment); with more, each group has 128 rows of its own
+//     and both take every tile.  Either way one group's exponentials run
+//     beside the other's MMAs.
+//
+// P is taken as a 16-bit part and its 16-bit remainder (two MMAs): outputs are
+// fp32, and one bf16 part alone would leave an error of 2^-9.  The two parts
+// of 32 positions, 16 + 16 columns, overwrite those positions' 32 columns of S.
+//
+// The accumulator is rescaled only when a row's maximum grew by more than
+// 2^kSlack; until then the weights may exceed 1.
+//
+// The tensor cores cut an accumulator's low bits off at every MMA, towards
+// zero: measured, 1.7e-8 of it a step, 2.9e-5 after 108 tiles of 16 MMAs.  So
+// after kTreeFlush units an accumulator is added to fp32 sums that the CTA
+// keeps in the workspace (in L2: a thread's row is its own, 128 D bytes of
+// every 32 kB x kTreeFlush of cache), and starts again.
+//
+// What a row must not see must not reach it: a score outside the row's mask is
+// dropped before the maximum, and V rows behind the last position are zeroed
+// in shared memory.  Among the nodes, a V element that is not finite is zeroed
+// too and added afterwards, to the rows that see its node (fix_up).
+#pragma once
+
+#include <atomic>
+
+#include "fd_tree.cuh"
+
+namespace fd {
+
+// ---------------------------------------------------------------- PTX
+
+__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// 32 consecutive 32-bit columns of this thread's tensor-memory lane.  The
+// registers are valid after tmem_wait_ld32, which takes them so that no use
+// moves ahead of it.
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+                   "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+                   "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+                   "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld32(uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                   "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+                 "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+                 "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+                 "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+                 "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+                 "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Instruction descriptor of a dense kind::f16 MMA (A and B both fp16, or both
+// bf16), fp32 accumulator: D format 1 = F32 (bits 4-5), A and B formats
+// (7-9, 10-12; 0 = fp16, 1 = bf16), B major (16; 1 = N contiguous), N >> 3
+// (17-22), M >> 4 (24-28).
+__host__ __device__ constexpr uint32_t umma_idesc_f16(int m, int n, bool f16, bool b_n_major)
+{
+    return (1u << 4) | ((f16 ? 0u : 1u) << 7) | ((f16 ? 0u : 1u) << 10) | ((b_n_major ? 1u : 0u) << 16) |
+           ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+// Descriptor of an operand whose N (not K) is contiguous, in the 128-byte
+// swizzled layout: a part holds 64 elements of N a row, one row a K index;
+// groups of 8 rows are 1024 bytes apart (stride offset), parts part_bytes apart
+// (leading offset).  Other fields as in umma_desc_sw128.
+__device__ __forceinline__ uint64_t umma_desc_sw128_n_major(uint32_t addr, uint32_t part_bytes)
+{
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(part_bytes >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+// D[tmem] (+)= A B^T for one K step of 16 elements, A in shared or in tensor memory.
+__device__ __forceinline__ void umma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+                 : "memory");
+}
+__device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+                 : "memory");
+}
+
+__device__ __forceinline__ uint64_t l2_policy_evict_normal()
+{
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint4 v)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+
+// ---------------------------------------------------------------- layout
+
+constexpr int kTreeMaxSlots = 6;
+
+template <int D, bool TMA>
+struct TreeCfg {
+    static constexpr int kN = tree_tile(D);
+    static constexpr int kGroups = tree_groups(D);
+    static constexpr int kSoftWarps = 4 * kGroups;
+    static constexpr int kSoftThreads = 32 * kSoftWarps;
+    static constexpr int kLoadWarps = TMA ? 1 : 4;                // of K, and as many of V
+    static constexpr int kMmaWarp = kSoftWarps + 2 * kLoadWarps;
+    static constexpr int kThreads = 32 * (kMmaWarp + 1);
+    static constexpr int kParts = D / 64;
+    static constexpr int kPartBytes = kN * 128;                   // of a K or V tile
+    static constexpr int kSlotBytes = kParts * kPartBytes;
+    static constexpr int kQBytes = 128 * D * 2;                   // 128 query rows
+    static constexpr int kFlush = kTreeFlush * 128 / kN;          // units between flushes
+    // tensor memory: two score buffers, then the accumulators
+    static constexpr uint32_t kTmemO = 256;
+    static constexpr uint32_t kTmemCols = 512;
+};
+
+struct TreeMisc {
+    uint64_t kfull[kTreeMaxSlots], kempty[kTreeMaxSlots], vfull[kTreeMaxSlots], vempty[kTreeMaxSlots];
+    uint64_t sfull[2], pfull[2], pvdone[2], qfull, pair, drain;
+    long long scan[18];
+    long long segpos, x1;
+    int b, seg, j, abort;
+    uint32_t tmem;
+    unsigned int bad[kMaxTree / 32];   // nodes whose V row is not finite
+    float2 ml[2][128];
+};
+
+// A CTA's walk over its tiles, segment by segment; every role makes its own.
+template <int D>
+struct TreeWalk {
+    int b, seg, j0, n;      // request, segment of it, its tiles [j0, j0 + n) are this CTA's
+    long long segpos, x1;   // position of the segment's first tile, end of the CTA's positions
+    TreeReq r;
+    TreeSeg s;
+
+    __device__ __forceinline__ void load(const TreeParams &p)
+    {
+        r = tree_req(p, b, nullptr);
+        s = tree_seg<D>(p, r);
+    }
+    __device__ __forceinline__ void count()
+    {
+        const long long left = x1 - segpos;
+        n = (int)(left < s.nb ? (left < 0 ? 0 : left) : s.nb) - j0;
+    }
+    __device__ __forceinline__ void start(const TreeParams &p, const TreeMisc &m)
+    {
+        b = m.b;
+        seg = m.seg;
+        j0 = m.j;
+        segpos = m.segpos;
+        x1 = m.x1;
+        n = 0;
+        if (b < p.batch) {
+            load(p);
+            count();
+        }
+    }
+    __device__ __forceinline__ void next(const TreeParams &p)
+    {
+        segpos += s.nb + kTreeSegCost;
+        j0 = 0;
+        ++seg;
+        while (seg >= s.segs) {
+            seg = 0;
+            if (++b >= p.batch) {
+                n = 0;
+                return;
+            }
+            load(p);
+        }
+        count();
+    }
+};
+
+// Pool row of position pos of request b (contiguous or paged); a page out of range is page 0.
+__device__ __forceinline__ int tree_page(const TreeParams &p, int b, int blk, bool report)
+{
+    int page = p.block_table[(long long)b * p.max_blocks + blk];
+    if ((unsigned)page >= (unsigned)p.num_pages) {
+        if (report)
+            atomicOr(p.ws_err, kErrPage);
+        page = 0;
+    }
+    return page;
+}
+__device__ __forceinline__ int tree_row(const TreeParams &p, int b, int pos, bool report)
+{
+    if (!p.block_table)
+        return b * p.page_size + pos;
+    const unsigned blk = (unsigned)pos / (unsigned)p.page_size;
+    return tree_page(p, b, (int)blk, report) * p.page_size + (int)((unsigned)pos - blk * (unsigned)p.page_size);
+}
+
+// Which of the nodes n0 .. n0 + 31 row i sees, as bits; n0 < 0 are positions of
+// the context, seen by every row.  Nodes from t on do not exist.
+__device__ __forceinline__ uint32_t tree_bits(const TreeParams &p, const uint64_t *mask_row, int i, int n0, int t)
+{
+    if (n0 <= -32)
+        return 0xffffffffu;
+    const int s = max(n0, 0);
+    uint32_t w = 0;
+    if (s < t) {
+        if (mask_row) {
+            const int k = s >> 6, sh = s & 63;
+            uint64_t x = mask_row[k] >> sh;
+            if (sh > 32 && k + 1 < p.words)
+                x |= mask_row[k + 1] << (64 - sh);
+            w = (uint32_t)x;
+        } else {
+            const int seen = i - s + 1;   // nodes s .. i
+            w = seen >= 32 ? 0xffffffffu : seen <= 0 ? 0u : (1u << seen) - 1u;
+        }
+        if (t - s < 32)
+            w &= (1u << (t - s)) - 1u;
+    }
+    return n0 < 0 ? (w << -n0) | ((1u << -n0) - 1u) : w;
+}
+
+// ---------------------------------------------------------------- roles
+
+// K or V tiles by TMA: lane = (box, part).
+template <int D, bool IS_K>
+__device__ __forceinline__ void tree_load_tma(const TreeParams &p, TreeMisc &m, const CUtensorMap *map, uint32_t ring,
+                                              int slots, int lane)
+{
+    using C = TreeCfg<D, true>;
+    const uint32_t full0 = smem_addr(IS_K ? m.kfull : m.vfull), empty0 = smem_addr(IS_K ? m.kempty : m.vempty);
+    volatile int *abort_flag = &m.abort;
+    const int box = lane / C::kParts, part = lane % C::kParts;
+    int slot = 0, issued = 0;
+    uint32_t ph = 0;
+    TreeWalk<D> w;
+    bool ok = true;
+    for (w.start(p, m); ok && w.n > 0; w.next(p)) {
+        const int g = w.seg / w.s.groups;
+        // row groups read the same tiles: those stay in L2
+        const uint64_t policy = w.s.groups > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
+        for (int j = w.j0; j < w.j0 + w.n; ++j) {
+            const int t0 = j * C::kN;
+            const int boxes = (min(C::kN, w.r.L - t0) + p.box_rows - 1) / p.box_rows;
+            int row = 0;
+            if (box < boxes)
+                row = tree_row(p, w.b, t0 + box * p.box_rows, IS_K);
+            ok = mbar_wait_bounded(empty0 + 8 * slot, ph ^ 1u, p.timeout_ns, abort_flag);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok)
+                break;
+            const uint32_t full = full0 + 8 * slot;
+            if (lane == 0)
+                mbar_arrive_expect_tx(full, (uint32_t)(boxes * C::kParts * p.box_rows * 128) +
+                                                (IS_K && p.starve && issued == 0 && blockIdx.x == 0 ? 16u : 0u));
+            __syncwarp();
+            if (box < boxes)
+                tma_load_3d(ring + slot * C::kSlotBytes + part * C::kPartBytes + box * p.box_rows * 128, map, full,
+                            part * 64, g, row, policy);
+            ++issued;
+            if (++slot == slots) {
+                slot = 0;
+                ph ^= 1u;
+            }
+        }
+    }
+    if (!ok) {
+        // gave up: wait (bounded) for the copies in flight before the CTA ends
+        if (lane == 0) {
+            atomicOr(p.ws_err, kErrTimeout);
+            *abort_flag = 1;
+            for (int k = 0; k < min(issued, slots); ++k) {
+                if (slot == 0) {
+                    slot = slots;
+                    ph ^= 1u;
+                }
+                --slot;
+                mbar_wait_bounded(full0 + 8 * slot, ph, p.timeout_ns, nullptr);
+            }
+        }
+    } else if (lane == 0) {
+        // every release has arrived: nothing signals this CTA's barriers any more
+        for (int k = 0; k < slots; ++k) {
+            if (!mbar_wait_bounded(empty0 + 8 * slot, ph ^ 1u, p.timeout_ns, abort_flag)) {
+                atomicOr(p.ws_err, kErrTimeout);
+                *abort_flag = 1;
+                break;
+            }
+            if (++slot == slots) {
+                slot = 0;
+                ph ^= 1u;
+            }
+        }
+    }
+    __syncwarp();
+}
+
+// K or V tiles by 128 threads: 16 (8) bytes of the cache, converted from FP8
+// codes if it holds those, to the swizzled 16-bit tile.
+template <int D, bool F16, int KV, bool IS_K>
+__device__ __forceinline__ void tree_load_threads(const TreeParams &p, TreeMisc &m, uint32_t ring, int slots, int tid)
+{
+    using C = TreeCfg<D, false>;
+    constexpr int kThreads = 32 * C::kLoadWarps;
+    constexpr bool kFp8 = kv_is_fp8(KV);
+    constexpr int kPer = 16;                              // elements a thread handles at once
+    constexpr int kRowUnits = D / kPer;
+    constexpr int kRounds = C::kN * kRowUnits / kThreads;   // units a thread has of a tile
+    constexpr int kBatch = kRounds < 4 ? kRounds : 4;
+    static_assert(C::kN * kRowUnits % kThreads == 0 && kRounds % kBatch == 0 && kThreads % kRowUnits == 0, "whole rounds");
+    const uint32_t full0 = smem_addr(IS_K ? m.kfull : m.vfull), empty0 = smem_addr(IS_K ? m.kempty : m.vempty);
+    volatile int *abort_flag = &m.abort;
+    const uint8_t *cache = IS_K ? p.k : p.v;
+    const int unit = tid % kRowUnits, row0 = tid / kRowUnits;
+    constexpr int kRowStep = kThreads / kRowUnits;
+    int slot = 0;
+    bool first = true;
+    uint32_t ph = 0;
+    TreeWalk<D> w;
+    bool ok = true;
+    for (w.start(p, m); ok && w.n > 0; w.next(p)) {
+        const int g = w.seg / w.s.groups;
+        for (int j = w.j0; j < w.j0 + w.n; ++j) {
+            const int t0 = j * C::kN, valid = min(C::kN, w.r.L - t0);
+            ok = mbar_wait_bounded(empty0 + 8 * slot, ph ^ 1u, p.timeout_ns, abort_flag);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok)
+                break;
+            const uint32_t tile = ring + slot * C::kSlotBytes;
+#pragma unroll
+            for (int r0 = 0; r0 < kRounds; r0 += kBatch) {
+                uint4 x[kBatch][kFp8 ? 1 : 2];
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const int row = row0 + (r0 + k) * kRowStep;
+                    x[k][0] = make_uint4(0, 0, 0, 0);
+                    if (!kFp8)
+                        x[k][kFp8 ? 0 : 1] = make_uint4(0, 0, 0, 0);
+                    if (row < valid) {
+                        const long long at = ((long long)tree_row(p, w.b, t0 + row, IS_K && unit == 0) * p.hkv + g) * D + unit * kPer;
+                        const uint8_t *src = cache + (kFp8 ? at : 2 * at);
+                        x[k][0] = ldg128_nc(src);
+                        if (!kFp8)
+                            x[k][kFp8 ? 0 : 1] = ldg128_nc(src + 16);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const int row = row0 + (r0 + k) * kRowStep;
+                    const int c = (2 * unit) & 7;   // the unit's first 16-byte chunk in its part
+                    const uint32_t at = tile + (2 * unit / 8) * C::kPartBytes + row * 128;
+                    if constexpr (kFp8) {
+                        const uint32_t in[4] = {x[k][0].x, x[k][0].y, x[k][0].z, x[k][0].w};
+                        uint32_t out[8];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t a = fp8x2_to_f16x2<KV>(lo16(in[e])), b = fp8x2_to_f16x2<KV>(hi16(in[e]));
+                            if constexpr (F16) {
+                                out[2 * e] = a;
+                                out[2 * e + 1] = b;
+                            } else {   // exact: an FP8 value has at most 4 significant bits
+                                const float2 fa = f16x2_to_float2(a), fb = f16x2_to_float2(b);
+                                out[2 * e] = pack_bf16x2(fa.x, fa.y);
+                                out[2 * e + 1] = pack_bf16x2(fb.x, fb.y);
+                            }
+                        }
+                        sts128(at + ((c ^ (row & 7)) << 4), make_uint4(out[0], out[1], out[2], out[3]));
+                        sts128(at + (((c + 1) ^ (row & 7)) << 4), make_uint4(out[4], out[5], out[6], out[7]));
+                    } else {
+                        sts128(at + ((c ^ (row & 7)) << 4), x[k][0]);
+                        sts128(at + (((c + 1) ^ (row & 7)) << 4), x[k][kFp8 ? 0 : 1]);
+                    }
+                }
+            }
+            fence_async_shared();
+            // the test hook leaves out one arrival, so that the tile never becomes full
+            if (!(IS_K && p.starve && first && blockIdx.x == 0 && tid == 0))
+                mbar_arrive(full0 + 8 * slot);
+            first = false;
+            if (++slot == slots) {
+                slot = 0;
+                ph ^= 1u;
+            }
+        }
+    }
+    // every release has arrived: nothing signals this CTA's barriers any more
+    for (int k = 0; ok && k < slots; ++k) {
+        ok = mbar_wait_bounded(empty0 + 8 * slot, ph ^ 1u, p.timeout_ns, abort_flag);
+        if (++slot == slots) {
+            slot = 0;
+            ph ^= 1u;
+        }
+    }
+    if (!ok) {
+        atomicOr(p.ws_err, kErrTimeout);
+        *abort_flag = 1;
+    }
+    __syncwarp();
+}
+
+// How the MMAs of a segment follow one another.  With the same rows in both
+// groups (or one group) unit u is tile u, in score buffer u & 1; with rows of
+// their own, tile u / active for group u % active.
+struct TreeUnits {
+    int active;   // groups with rows of their own: 0 = one set of rows
+    int units;
+    __device__ __forceinline__ int tile(int u) const { return active == 2 ? u >> 1 : u; }
+    __device__ __forceinline__ int buf(int u) const { return active == 1 ? 0 : u & 1; }
+    __device__ __forceinline__ int ahead() const { return active == 1 ? 1 : 2; }
+    __device__ __forceinline__ bool last_of_tile(int u) const { return active != 2 || (u & 1); }
+    __device__ __forceinline__ bool first_of_tile(int u) const { return active != 2 || !(u & 1); }
+};
+template <int D>
+__device__ __forceinline__ TreeUnits tree_units(const TreeParams &p, const TreeWalk<D> &w)
+{
+    TreeUnits u;
+    u.active = 0;
+    if (p.rows == 256)
+        u.active = (w.seg % w.s.groups) * 256 + 128 < w.r.t * p.group ? 2 : 1;
+    u.units = u.active == 2 ? 2 * w.n : w.n;
+    return u;
+}
+
+// The MMA issuer: one thread.
+template <int D, bool F16, bool TMA>
+__device__ __forceinline__ void tree_mma(const TreeParams &p, TreeMisc &m, uint32_t q_smem, uint32_t k_ring,
+                                         uint32_t v_ring, uint32_t tmem)
+{
+    using C = TreeCfg<D, TMA>;
+    constexpr uint32_t kIdescS = umma_idesc_f16(128, C::kN, F16, false);
+    constexpr uint32_t kIdescO = umma_idesc_f16(128, D, F16, true);
+    volatile int *abort_flag = &m.abort;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        return mbar_wait_bounded(smem_addr(bar), parity, p.timeout_ns, abort_flag);
+    };
+    int ks = 0, vs = 0, segs = 0;   // the slot of the newest S's tile, and of the next P V's
+    uint32_t kph = 0, vph = 0, pph = 0;
+    TreeWalk<D> w;
+    bool ok = true;
+    for (w.start(p, m); ok && w.n > 0; w.next(p), ++segs) {
+        const TreeUnits un = tree_units<D>(p, w);
+        if (!(ok = wait(&m.qfull, segs & 1)))
+            break;
+        tc_fence_after();
+        auto scores = [&](int u) {
+            if (un.first_of_tile(u) && !wait(&m.kfull[ks], kph))
+                return false;
+            tc_fence_after();
+            const int buf = un.buf(u);
+            const uint32_t a = q_smem + (un.active == 2 ? buf * C::kQBytes : 0), b = k_ring + ks * C::kSlotBytes;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+                umma_f16_ss(tmem + buf * C::kN, umma_desc_sw128(a + (k / 4) * (128 * 128) + (k % 4) * 32),
+                            umma_desc_sw128(b + (k / 4) * C::kPartBytes + (k % 4) * 32), kIdescS, k > 0);
+            umma_commit(smem_addr(&m.sfull[buf]));
+            if (un.last_of_tile(u)) {
+                umma_commit(smem_addr(&m.kempty[ks]));
+                if (++ks == p.k_slots) {
+                    ks = 0;
+                    kph ^= 1u;
+                }
+            }
+            return true;
+        };
+        for (int u = 0; ok && u < un.ahead() && u < un.units; ++u)
+            ok = scores(u);
+        for (int u = 0; ok && u < un.units; ++u) {
+            const int buf = un.buf(u), acc = C::kGroups == 1 ? 0 : buf;
+            if (!(ok = wait(&m.pfull[buf], (pph >> buf) & 1u)))
+                break;
+            pph ^= 1u << buf;
+            if (un.first_of_tile(u) && !(ok = wait(&m.vfull[vs], vph)))
+                break;
+            tc_fence_after();
+            // the first unit of an accumulator in this segment, and after a flush, overwrites it
+            const int nth = C::kGroups == 1 ? u : u / un.ahead();
+            const bool fresh = nth % C::kFlush == 0;
+            const uint32_t d = tmem + C::kTmemO + acc * D, b = v_ring + vs * C::kSlotBytes;
+#pragma unroll
+            for (int k = 0; k < C::kN / 16; ++k) {
+                const uint32_t a = tmem + buf * C::kN + (k / 2) * 32 + (k % 2) * 8;
+                const uint64_t bd = umma_desc_sw128_n_major(b + k * 16 * 128, C::kPartBytes);
+                umma_f16_ts(d, a, bd, kIdescO, !(fresh && k == 0));
+                umma_f16_ts(d, a + 16, bd, kIdescO, true);
+            }
+            umma_commit(smem_addr(&m.pvdone[acc]));
+            if (un.last_of_tile(u)) {
+                umma_commit(smem_addr(&m.vempty[vs]));
+                if (++vs == p.v_slots) {
+                    vs = 0;
+                    vph ^= 1u;
+                }
+            }
+            if (u + un.ahead() < un.units)
+                ok = scores(u + un.ahead());
+        }
+    }
+    if (!ok) {
+        atomicOr(p.ws_err, kErrTimeout);
+        *abort_flag = 1;
+        // gave up: the MMAs in flight end before the tensor memory is freed
+        umma_commit(smem_addr(&m.drain));
+        mbar_wait_bounded(smem_addr(&m.drain), 0, p.timeout_ns, nullptr);
+    }
+}
+
+// Copies this CTA's query rows of a segment into the swizzled operand: rows
+// [0, 128) of one 128-row tile, by `threads` threads.  Rows without a node are zero.
+template <int D>
+__device__ __forceinline__ void tree_load_q(const TreeParams &p, const TreeWalk<D> &w, uint32_t q_smem, int first_row,
+                                            int tid, int threads)
+{
+    constexpr int kChunks = D / 8;
+    const int g = w.seg / w.s.groups;
+    const uint32_t flip = p.negate_q ? 0x80008000u : 0u;
+    const int chunk = tid % kChunks;
+    for (int r = tid / kChunks; r < 128; r += threads / kChunks) {
+        const int row = first_row + r, i = row / p.group, h = row - i * p.group;
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (i < w.r.t) {
+            x = __ldg(reinterpret_cast<const uint4 *>(
+                    p.q + (((long long)w.b * p.tree_len + i) * p.hq + g * p.group + h) * D) + chunk);
+            x.x ^= flip;
+            x.y ^= flip;
+            x.z ^= flip;
+            x.w ^= flip;
+        }
+        sts128(q_smem + (chunk / 8) * (128 * 128) + r * 128 + (((chunk & 7) ^ (r & 7)) << 4), x);
+    }
+}
+
+// V tile rows from `from` on: those at or past `valid` become zero, and in the
+// others (tree nodes) elements that are not finite do, their node marked in bad.
+template <int D, bool F16, bool TMA>
+__device__ __forceinline__ void tree_clean_v(uint32_t tile, int from, int valid, int node0, unsigned int *bad, int tid)
+{
+    using C = TreeCfg<D, TMA>;
+    constexpr int kChunks = D / 8;
+    constexpr uint32_t kExp = F16 ? 0x7c00u : 0x7f80u;
+    for (int e = from * kChunks + tid; e < C::kN * kChunks; e += 128) {
+        const int row = e / kChunks, chunk = e % kChunks;
+        const uint32_t at = tile + (chunk / 8) * C::kPartBytes + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+        if (row >= valid) {
+            sts128(at, make_uint4(0, 0, 0, 0));
+            continue;
+        }
+        const uint4 v = lds128(at);
+        uint32_t x[4] = {v.x, v.y, v.z, v.w};
+        bool hit = false;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if ((x[k] & kExp) == kExp) {
+                x[k] &= 0xffff0000u;
+                hit = true;
+            }
+            if ((x[k] & (kExp << 16)) == kExp << 16) {
+                x[k] &= 0x0000ffffu;
+                hit = true;
+            }
+        }
+        if (hit) {
+            sts128(at, make_uint4(x[0], x[1], x[2], x[3]));
+            const int node = node0 + row;
+            atomicOr(&bad[node >> 5], 1u << (node & 31));
+        }
+    }
+}
+
+// Element e of a K or V row as fp32, for values that are not finite.
+template <bool F16, int KV>
+__device__ __forceinline__ float tree_element(const uint8_t *cache, long long e)
+{
+    if constexpr (kv_is_fp8(KV))
+        return fp8x2_to_float2<KV>(cache[e]).x;
+    else
+        return x2_to_float2<F16>(reinterpret_cast<const uint16_t *>(cache)[e]).x;
+}
+
+// A group of 128 threads, one query row each.
+template <int D, bool F16, int KV, bool TMA>
+__device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, uint32_t q_smem, uint32_t v_ring,
+                                             uint32_t tmem)
+{
+    using C = TreeCfg<D, TMA>;
+    // fp16 weights: 2^8 more keeps weights down to 2^-33 of the largest among
+    // the 16-bit parts (fp16 ends at 2^-25), and 2^7 of slack ends at 2^15.
+    constexpr float kShift = F16 ? 8.f : 0.f, kSlack = F16 ? 7.f : 8.f;
+    constexpr float kNegInf = -__builtin_huge_valf();
+    const int tid = threadIdx.x & 127, group = threadIdx.x >> 7, lane_base = (threadIdx.x >> 5 & 3) << 5;
+    volatile int *abort_flag = &m.abort;
+    const bool own_rows = p.rows == 256;             // each group has its own 128 rows
+    const bool shared_rows = C::kGroups == 2 && !own_rows;
+    const uint32_t t_lane = tmem + ((uint32_t)lane_base << 16);
+    const uint32_t t_o = t_lane + C::kTmemO + (C::kGroups == 2 ? group * D : 0);
+    const float sl = p.scale_log2;
+    uint32_t sph = 0, pvph = 0, pairph = 0;
+    int vcount = 0;                                  // tiles before the current segment
+    bool ok = true;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        // all lanes take part; a lane that gives up takes its warp with it
+        const bool r = mbar_wait_bounded(smem_addr(bar), parity, p.timeout_ns, abort_flag);
+        return __all_sync(0xffffffffu, r) != 0;
+    };
+    auto pair_sync = [&]() {
+        mbar_arrive(smem_addr(&m.pair));
+        const bool r = wait(&m.pair, pairph);
+        pairph ^= 1u;
+        return r;
+    };
+    // this thread's sums of the units before the last flush, relative to the maximum then
+    float *sums = p.ws_sums + ((long long)(blockIdx.x * C::kGroups + group) * (D / 4) * p.sum_rows + tid) * 4;
+    const bool has_sums = tid < p.sum_rows;
+    float flushed_at = kNegInf;
+    // sums = sums * 2^((their maximum - mx) scale) + the accumulator, `fresh`: = the accumulator
+    auto flush_sums = [&](bool fresh, float now) {
+        const float corr = fresh || flushed_at == kNegInf ? 0.f : exp2_approx((flushed_at - now) * sl);
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(t_o + 32 * c, o);
+            float4 old[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                old[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (!fresh && has_sums)
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    old[k] = *reinterpret_cast<const float4 *>(sums + (long long)(8 * c + k) * p.sum_rows * 4);
+            tmem_wait_ld32(o);
+            if (has_sums)
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    *reinterpret_cast<float4 *>(sums + (long long)(8 * c + k) * p.sum_rows * 4) =
+                        make_float4(fmaf(old[k].x, corr, __uint_as_float(o[4 * k])),
+                                    fmaf(old[k].y, corr, __uint_as_float(o[4 * k + 1])),
+                                    fmaf(old[k].z, corr, __uint_as_float(o[4 * k + 2])),
+                                    fmaf(old[k].w, corr, __uint_as_float(o[4 * k + 3])));
+        }
+        tc_fence_before();
+    };
+    TreeWalk<D> w;
+    w.start(p, m);
+    auto load_q = [&]() {
+        const int first = (w.seg % w.s.groups) * p.rows;
+        if (shared_rows)
+            tree_load_q<D>(p, w, q_smem, first, threadIdx.x, C::kSoftThreads);
+        else
+            tree_load_q<D>(p, w, q_smem + group * C::kQBytes, first + group * 128, tid, 128);
+        fence_async_shared();
+        tc_fence_before();
+        mbar_arrive(smem_addr(&m.qfull));
+    };
+    if (w.n > 0)
+        load_q();
+    while (w.n > 0) {
+        const TreeUnits un = tree_units<D>(p, w);
+        const int L = w.r.L, t = w.r.t, base = L - t;
+        const int row = (w.seg % w.s.groups) * p.rows + (own_rows ? group * 128 : 0) + tid;
+        const int i = row / p.group, h = row - i * p.group;
+        const bool in_call = i < p.tree_len, live = i < t && base + i >= 0;
+        const bool warp_live = __any_sync(0xffffffffu, live);
+        const uint64_t *mask_row = p.mask && in_call ? p.mask + w.b * p.mask_stride + (long long)i * p.words : nullptr;
+        float mx = kNegInf, l = 0.f;
+        int mine = 0;                                // units of this group so far in the segment
+        // own rows: unit 2 j + group (or j); shared: units group, group + 2, ..
+        const int u0 = C::kGroups == 1 || un.active == 1 ? 0 : group;
+        const int step = C::kGroups == 1 || un.active == 1 ? 1 : 2;
+        const int end = un.active == 1 && group == 1 ? 0 : un.units;
+        for (int u = u0; u < end; u += step, ++mine) {
+            const int tile = un.tile(u), buf = un.buf(u);
+            const int t0 = (w.j0 + tile) * C::kN;
+            const uint32_t t_s = t_lane + buf * C::kN;
+            const bool tail = t0 + C::kN > base;
+            if (!(ok = wait(&m.sfull[buf], (sph >> buf) & 1u)))
+                break;
+            sph ^= 1u << buf;
+            tc_fence_after();
+            const bool flush = mine > 0 && mine % C::kFlush == 0;
+            if (C::kGroups == 1 && flush && !(ok = wait(&m.pvdone[0], pvph ^ 1u)))
+                break;
+            if (flush && warp_live) {
+                tc_fence_after();
+                flush_sums(mine == C::kFlush, mx);
+                flushed_at = mx;
+            }
+            if (warp_live) {
+                float tm = kNegInf;
+#pragma unroll
+                for (int c = 0; c < C::kN / 32; ++c) {
+                    uint32_t s[32];
+                    tmem_ld32(t_s + 32 * c, s);
+                    tmem_wait_ld32(s);
+                    if (tail) {
+                        const uint32_t bits = live ? tree_bits(p, mask_row, i, t0 + 32 * c - base, t) : 0u;
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            tm = fmaxf(tm, bits >> k & 1u ? __uint_as_float(s[k]) : kNegInf);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            tm = fmaxf(tm, __uint_as_float(s[k]));
+                    }
+                }
+                const bool grow = tm > mx && (mx == kNegInf || (tm - mx) * sl > kSlack);
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float corr = grow ? (mx == kNegInf ? 0.f : exp2_approx((mx - tm) * sl)) : 1.f;
+                    if (grow)
+                        mx = tm;
+                    l *= corr;
+                    if (mine > 0 && !flush) {   // after a flush there is nothing to rescale
+                        // with two groups the score that was waited for follows this
+                        // accumulator's last MMAs; with one, the last unit's may still run
+                        if (C::kGroups == 1 && !(ok = wait(&m.pvdone[0], pvph ^ 1u)))
+                            break;
+                        if (C::kGroups == 1)
+                            tc_fence_after();
+#pragma unroll
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t o[32];
+                            tmem_ld32(t_o + 32 * c, o);
+                            tmem_wait_ld32(o);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                o[k] = __float_as_uint(__uint_as_float(o[k]) * corr);
+                            tmem_st32(t_o + 32 * c, o);
+                        }
+                    }
+                }
+                const float off = kShift - (mx == kNegInf ? 0.f : mx * sl);
+                const float2 sl2 = make_float2(sl, sl), off2 = make_float2(off, off), one2 = make_float2(1.f, 1.f),
+                             neg2 = make_float2(-1.f, -1.f);
+                float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int c = 0; c < C::kN / 32; ++c) {
+                    uint32_t s[32];
+                    tmem_ld32(t_s + 32 * c, s);
+                    uint32_t bits = 0xffffffffu;
+                    if (tail)
+                        bits = live ? tree_bits(p, mask_row, i, t0 + 32 * c - base, t) : 0u;
+                    tmem_wait_ld32(s);
+                    uint32_t out[32];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        float2 x = fma2(make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), sl2, off2);
+                        x.x = exp2_approx(x.x);
+                        x.y = exp2_approx(x.y);
+                        if (tail) {
+                            x.x = bits >> (2 * k) & 1u ? x.x : 0.f;
+                            x.y = bits >> (2 * k + 1) & 1u ? x.y : 0.f;
+                        }
+                        sum = fma2(x, one2, sum);
+                        out[k] = pack_x2<F16>(x.x, x.y);
+                        const float2 rest = fma2(x2_to_float2<F16>(out[k]), neg2, x);
+                        out[16 + k] = pack_x2<F16>(rest.x, rest.y);
+                    }
+                    tmem_st32(t_s + 32 * c, out);
+                }
+                l += sum.x + sum.y;
+                tmem_wait_st();
+            }
+            if (tail) {
+                // this group's tile (with rows of their own: the first group cleans for both)
+                const int vs = (vcount + tile) % p.v_slots;
+                if (!own_rows || group == 0) {
+                    if (!(ok = wait(&m.vfull[vs], ((vcount + tile) / p.v_slots) & 1)))
+                        break;
+                    tree_clean_v<D, F16, TMA>(v_ring + vs * C::kSlotBytes, max(0, base - t0), L - t0, t0 - base, m.bad, tid);
+                    fence_async_shared();
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(smem_addr(&m.pfull[buf]));
+            pvph ^= 1u;
+        }
+        if (!ok)
+            break;
+        if (mine > 0 && !(ok = wait(&m.pvdone[C::kGroups == 2 ? group : 0], pvph ^ 1u)))
+            break;
+        tc_fence_after();
+        vcount += w.n;
+
+        // the segment's result: O / l and the log-sum-exp (base 2), final or partial
+        if (mine > C::kFlush && warp_live) {
+            flush_sums(false, mx);   // the segment's whole sum, relative to the final maximum
+            __threadfence_block();   // with shared rows the other group reads half of it
+        }
+        if (!live) {
+            mx = kNegInf;
+            l = 0.f;
+        }
+        if (shared_rows)
+            m.ml[group][tid] = make_float2(mx, l);
+        if (!(ok = pair_sync()))
+            break;
+        float a0 = 1.f, a1 = 0.f;
+        const bool two = shared_rows && w.n > 1;     // the second group had a tile
+        if (shared_rows) {
+            const float2 x = m.ml[0][tid], y = m.ml[1][tid];
+            mx = fmaxf(x.x, y.x);
+            a0 = x.x == kNegInf ? 0.f : exp2_approx((x.x - mx) * sl);
+            a1 = y.x == kNegInf ? 0.f : exp2_approx((y.x - mx) * sl);
+            // scores of NaN leave no maximum, but a sum of NaN
+            l = x.y * (x.x == kNegInf ? 1.f : a0) + y.y * (y.x == kNegInf ? 1.f : a1);
+        }
+        const bool any = live && l != 0.f;           // true for NaN
+        const float inv = any ? p.v_scale / l : 0.f;
+        const float lse2 = any ? (mx == kNegInf ? 0.f : mx * sl) + log2f(l) - kShift : kNegInf;
+        const int g = w.seg / w.s.groups;
+        const long long o_row = ((long long)w.b * p.tree_len + i) * p.hq + g * p.group + h;
+        const bool whole = w.j0 == 0 && w.n == w.s.nb;
+        const int slot = 2 * (int)blockIdx.x + (w.j0 > 0 ? 0 : 1);
+        const int srow = (own_rows ? group * 128 : 0) + tid;   // row of the partial
+        const int c0 = shared_rows ? group * (D / 2) : 0, c1 = shared_rows ? c0 + D / 2 : D;
+        const bool computed = mine > 0 || (shared_rows && w.n > 0);
+        for (int c = c0; c < c1; c += 32) {
+            float v[32];
+            [[maybe_unused]] uint32_t x[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+                v[k] = 0.f;
+            if (computed && warp_live) {
+                // columns c .. c + 31 of a group's sum: in the workspace once it was flushed
+                auto add = [&](int of, bool flushed, float weight) {
+                    if (flushed) {
+                        if (!has_sums)
+                            return;
+                        const float *src = p.ws_sums + (((long long)(blockIdx.x * C::kGroups + of) * (D / 4) + c / 4) * p.sum_rows + tid) * 4;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float4 o = *reinterpret_cast<const float4 *>(src + (long long)k * p.sum_rows * 4);
+                            v[4 * k] = fmaf(o.x, weight, v[4 * k]);
+                            v[4 * k + 1] = fmaf(o.y, weight, v[4 * k + 1]);
+                            v[4 * k + 2] = fmaf(o.z, weight, v[4 * k + 2]);
+                            v[4 * k + 3] = fmaf(o.w, weight, v[4 * k + 3]);
+                        }
+                    } else {
+                        tmem_ld32(t_lane + C::kTmemO + of * D + c, x);
+                        tmem_wait_ld32(x);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            v[k] = fmaf(__uint_as_float(x[k]), weight, v[k]);
+                    }
+                };
+                if (shared_rows) {
+                    add(0, (w.n + 1) / 2 > C::kFlush, a0);
+                    if (two)
+                        add(1, w.n / 2 > C::kFlush, a1);
+                } else
+                    add(C::kGroups == 1 ? 0 : group, mine > C::kFlush, 1.f);
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                    v[k] = any ? v[k] * inv : 0.f;
+            }
+            if (in_call && (whole || any)) {
+                float *dst = whole ? p.o + o_row * D + c
+                                   : p.ws_o + (((long long)slot * (D / 4) + c / 4) * p.slot_rows + srow) * 4;
+                const int stride = whole ? 4 : p.slot_rows * 4;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    *reinterpret_cast<float4 *>(dst + k * stride) = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+            }
+        }
+        if (in_call && (!shared_rows || group == 0)) {
+            if (!whole)
+                p.ws_lse[slot * p.slot_rows + srow] = lse2;
+            else if (p.lse)
+                p.lse[o_row] = any ? lse2 * 0.6931471805599453f : kNegInf;
+        }
+        // values that are not finite, of nodes in this CTA's tiles
+        for (int wd = 0; wd < kMaxTree / 32; ++wd) {
+            uint32_t nodes = m.bad[wd];
+            for (; nodes; nodes &= nodes - 1) {
+                const int node = 32 * wd + __ffs(nodes) - 1;
+                if (!any || !(tree_bits(p, mask_row, i, node, t) & 1u))
+                    continue;
+                const long long at = ((long long)tree_row(p, w.b, base + node, false) * p.hkv + g) * D;
+                float s = 0.f;
+                for (int d = 0; d < D; ++d)
+                    s = fmaf(x2_to_float2<F16>(p.q[o_row * D + d]).x, tree_element<F16, KV>(p.k, at + d), s);
+                const float weight = exp2_approx((p.negate_q ? -s : s) * sl - lse2);
+                for (int d = c0; d < c1; ++d) {
+                    const float x = tree_element<F16, KV>(p.v, at + d);
+                    if (fabsf(x) <= 3.4028235e38f)
+                        continue;
+                    float *dst = whole ? p.o + o_row * D + d
+                                       : p.ws_o + (((long long)slot * (D / 4) + d / 4) * p.slot_rows + srow) * 4 + d % 4;
+                    *dst = fmaf(weight, x, *dst);
+                }
+            }
+        }
+        tc_fence_before();
+        if (!(ok = pair_sync()))
+            break;
+        if (threadIdx.x < kMaxTree / 32)
+            m.bad[threadIdx.x] = 0;
+        w.next(p);
+        if (w.n > 0)
+            load_q();
+    }
+    if (!ok) {
+        atomicOr(p.ws_err, kErrTimeout);
+        *abort_flag = 1;
+    }
+    __syncwarp();
+}
+
+// ---------------------------------------------------------------- kernel
+
+template <int D, bool F16, int KV, bool TMA>
+__global__ void __launch_bounds__(TreeCfg<D, TMA>::kThreads, 1)
+tree_split_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUtensorMap tmk,
+                  const __grid_constant__ CUtensorMap tmv)
+{
+    using C = TreeCfg<D, TMA>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    TreeMisc &m = *reinterpret_cast<TreeMisc *>(smem + p.off_misc);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (smem_addr(smem) & 1023u) {   // the swizzled layout and its descriptors count on it
+        if (tid == 0)
+            atomicOr(p.ws_err, kErrTimeout);
+        return;
+    }
+    if (warp == C::kMmaWarp)
+        tmem_alloc(smem_addr(&m.tmem), C::kTmemCols);
+    if (tid == 0) {
+        for (int s = 0; s < kTreeMaxSlots; ++s) {
+            mbar_init(smem_addr(&m.kfull[s]), TMA ? 1 : 32 * C::kLoadWarps);
+            mbar_init(smem_addr(&m.vfull[s]), TMA ? 1 : 32 * C::kLoadWarps);
+            mbar_init(smem_addr(&m.kempty[s]), 1);
+            mbar_init(smem_addr(&m.vempty[s]), 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(smem_addr(&m.sfull[s]), 1);
+            mbar_init(smem_addr(&m.pfull[s]), 128);
+            mbar_init(smem_addr(&m.pvdone[s]), 1);
+        }
+        mbar_init(smem_addr(&m.qfull), C::kSoftThreads);
+        mbar_init(smem_addr(&m.pair), C::kSoftThreads);
+        mbar_init(smem_addr(&m.drain), 1);
+        mbar_init_fence();
+        m.abort = 0;
+        m.b = p.batch;
+        if (TMA) {
+            tma_prefetch_desc(&tmk);
+            tma_prefetch_desc(&tmv);
+        }
+    }
+    if (tid < kMaxTree / 32)
+        m.bad[tid] = 0;
+    pdl_wait_prior_grid();
+    pdl_launch_dependents();
+
+    // This CTA's run: a scan of the requests' costs, and the thread whose
+    // requests hold the run's first position looks it up.
+    const int per = (p.batch + C::kThreads - 1) / C::kThreads;
+    const int b0 = min(tid * per, p.batch), b1 = min(b0 + per, p.batch);
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b)
+        mine += tree_cost(tree_seg<D>(p, tree_req(p, b, blockIdx.x == 0 ? p.ws_err : nullptr)));
+    long long x = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, off);
+        if (lane >= off)
+            x += y;
+    }
+    if (lane == 31)
+        m.scan[warp] = x;
+    __syncthreads();
+    long long before = x - mine, total = 0;
+    for (int k = 0; k <= C::kMmaWarp; ++k) {
+        before += k < warp ? m.scan[k] : 0;
+        total += m.scan[k];
+    }
+    const TreeSplit split = tree_split(total, gridDim.x);
+    const int cta = blockIdx.x;
+    const bool works = cta < split.ctas;
+    const long long x0 = works ? split.begin(cta) : 0;
+    if (tid == 0)
+        m.x1 = works ? split.begin(cta + 1) : 0;
+    long long at = before;
+    for (int b = b0; b < b1 && (cta == 0 || works); ++b) {
+        const TreeSeg s = tree_seg<D>(p, tree_req(p, b, nullptr));
+        if (cta == 0)
+            p.ws_cost[b] = at;
+        const long long cost = tree_cost(s);
+        if (works && at <= x0 && x0 < at + cost) {
+            const long long rel = x0 - at - kTreeSegCost;
+            long long seg = rel < 0 ? 0 : rel / (s.nb + kTreeSegCost);
+            long long j = rel < 0 ? 0 : rel - seg * (s.nb + kTreeSegCost);
+            if (j >= s.nb) {   // the gap before the next segment (there is one: the last ends with its tiles)
+                ++seg;
+                j = 0;
+            }
+            m.b = b;
+            m.seg = (int)seg;
+            m.j = (int)j;
+            m.segpos = at + seg * (s.nb + kTreeSegCost) + kTreeSegCost;
+        }
+        at += cost;
+    }
+    if (cta == 0 && tid == 0)
+        p.ws_cost[p.batch] = total;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = m.tmem;
+    const uint32_t q_smem = smem_addr(smem), k_ring = smem_addr(smem + p.off_k), v_ring = smem_addr(smem + p.off_v);
+    if (warp < C::kSoftWarps)
+        tree_softmax<D, F16, KV, TMA>(p, m, q_smem, v_ring, tmem);
+    else if (warp == C::kMmaWarp) {
+        if (lane == 0)
+            tree_mma<D, F16, TMA>(p, m, q_smem, k_ring, v_ring, tmem);
+        __syncwarp();
+    } else if constexpr (TMA) {
+        if (warp == C::kSoftWarps)
+            tree_load_tma<D, true>(p, m, &tmk, k_ring, p.k_slots, lane);
+        else
+            tree_load_tma<D, false>(p, m, &tmv, v_ring, p.v_slots, lane);
+    } else {
+        if (warp < C::kSoftWarps + C::kLoadWarps)
+            tree_load_threads<D, F16, KV, true>(p, m, k_ring, p.k_slots, tid - 32 * C::kSoftWarps);
+        else
+            tree_load_threads<D, F16, KV, false>(p, m, v_ring, p.v_slots, tid - 32 * (C::kSoftWarps + C::kLoadWarps));
+    }
+    // every role returns, its waits being bounded
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == C::kMmaWarp)
+        tmem_dealloc(tmem, C::kTmemCols);
+}
+
+template <int D, bool F16, int KV, bool TMA>
+cudaError_t launch_tree_variant(const TreeParams &p, const CUtensorMap &tmk, const CUtensorMap &tmv, const TreeLaunch &c)
+{
+    // the shared-memory limit is raised once per device, so that later calls
+    // may be captured; again if a launch is refused (the context was reset)
+    static std::atomic<unsigned long long> configured{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    auto configure = [&]() -> cudaError_t {
+        const cudaError_t r = cudaFuncSetAttribute(tree_split_kernel<D, F16, KV, TMA>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)c.smem_optin);
+        if (r == cudaSuccess)
+            configured.fetch_or(bit, std::memory_order_release);
+        return r;
+    };
+    if (!(configured.load(std::memory_order_acquire) & bit) && (e = configure()) != cudaSuccess)
+        return e;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)c.grid);
+    cfg.blockDim = dim3(TreeCfg<D, TMA>::kThreads);
+    cfg.dynamicSmemBytes = c.smem_bytes;
+    cfg.stream = c.stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, tree_split_kernel<D, F16, KV, TMA>, p, tmk, tmv);
+    if (e == cudaErrorInvalidValue) {
+        (void)cudaGetLastError();
+        if ((e = configure()) != cudaSuccess)
+            return e;
+        e = cudaLaunchKernelEx(&cfg, tree_split_kernel<D, F16, KV, TMA>, p, tmk, tmv);
+    }
+    return e;
+}
+
+}  // namespace fd

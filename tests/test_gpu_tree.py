@@ -220,3 +220,16 @@ def test_python_refusals(fd):
         fd.fd_tree_decode(q, k, v, lens, mask, workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ValueError):
         fd.fd_tree_decode_paged(q, k, v, None, lens, mask)
+
+
+@pytest.mark.parametrize("page,kv,T,D", [(0, "same", 8, 128), (16, "same", 50, 128), (4, "same", 8, 64), (0, "e4m3", 40, 128),
+                                         (64, "same", 8, 256)])
+def test_a_starved_wait_times_out_and_the_context_survives(fd, page, kv, T, D):
+    """A first tile that never arrives: every role gives up, the tensor memory is freed, the host
+    reads FD_ERR_TIMEOUT, and the same workspace serves the next call."""
+    c = make_tree_case(21, 2, T, 8, 2, D, [700, 300], page=page, kv=kv)
+    ws = fd.make_tree_workspace(2, T, 8, 2, D)
+    run(fd, c, 0.1, workspace=ws, num_ctas=4, flags=fd.FD_FLAG_TEST_STARVE_FIRST_TILE, wait_timeout_ns=50_000_000)
+    assert fd.fd_get_device_error(ws) == fd.FD_ERR_TIMEOUT
+    check_tree(*run(fd, c, 0.1, workspace=ws, num_ctas=4), want(c, 0.1))
+    assert fd.fd_get_device_error(ws) == fd.FD_OK
