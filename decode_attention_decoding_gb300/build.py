@@ -38,7 +38,7 @@ def _nvcc() -> str:
 SPLIT_INST = "fd_split_inst.cu"
 KV_NAMES = ("bf16", "f16", "e4m3", "e5m2")
 TREE_INST = "fd_tree_inst.cu"
-TREE_LOADS = ("tma", "pages", "e4m3", "e5m2")   # 16-bit by TMA, 16-bit by loader threads, FP8 codes
+TREE_LOADS = ("tma", "convert", "copy", "copy_fp8")   # fd_tree_inst.cu's FD_TREE_LOAD
 TREE_VARIANTS = [(load, d) for load in range(4) for d in (64, 128, 256)]
 SPLIT_VARIANTS = [(paged, kv, d) for paged in (0, 1) for kv in range(4) for d in (64, 128, 256)]
 

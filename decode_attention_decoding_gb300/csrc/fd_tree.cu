@@ -54,20 +54,30 @@ bool host_lens_ok(const int32_t *lens, int batch, long long cap)
 }
 
 // Shared memory of the split kernel: the query rows, then rings of K and V
-// tiles in what is left, then the barriers.  The odd slot goes to K, whose
-// tiles are wanted a step earlier.
+// tiles in what is left, then the barriers.  An odd slot goes to K, whose tiles
+// are wanted a step earlier.  FP8 codes wait in rings of their own; two
+// converted tiles of each are enough, the rest holds codes.
 template <int D>
-void plan_tree_smem(TreeParams *p, TreeLaunch *c)
+void plan_tree_smem(TreeParams *p, TreeLaunch *c, int load)
 {
-    using C = TreeCfg<D, true>;   // the sizes used here do not depend on the loader
+    using C = TreeCfg<D, kTreeTma>;   // the sizes used here are the same for every loader
     const size_t q = (size_t)(p->rows / 128) * C::kQBytes, misc = align_up(sizeof(TreeMisc), 16);
-    int slots = (int)((c->smem_optin - q - misc) / C::kSlotBytes);
+    size_t left = c->smem_optin - q - misc;
+    p->raw_slots = 0;
+    int slots = 4;
+    if (load == kTreeConvert) {
+        const int raw = (int)((left - 4 * C::kSlotBytes) / (2 * C::kRawBytes));
+        p->raw_slots = raw < kTreeMaxRaw ? raw : kTreeMaxRaw;
+        left -= 2 * (size_t)p->raw_slots * C::kRawBytes;
+    }
+    slots = (int)(left / C::kSlotBytes);
     slots = slots < 2 * kTreeMaxSlots ? slots : 2 * kTreeMaxSlots;
     p->k_slots = (slots + 1) / 2;
     p->v_slots = slots / 2;
     p->off_k = (uint32_t)q;
     p->off_v = (uint32_t)(p->off_k + p->k_slots * C::kSlotBytes);
-    p->off_misc = (uint32_t)(p->off_v + p->v_slots * C::kSlotBytes);
+    p->off_raw = (uint32_t)(p->off_v + p->v_slots * C::kSlotBytes);
+    p->off_misc = (uint32_t)(p->off_raw + 2 * p->raw_slots * C::kRawBytes);
     c->smem_bytes = p->off_misc + misc;
 }
 
@@ -104,6 +114,7 @@ fd_status launch(TreeParams p, int head_dim, float scale, const fd_options *opts
     const bool fp8 = kv_is_fp8(kv);
     // an FP8 cache's k_scale multiplies every score; a negative scale changes q's sign
     scale *= fp8 && opts->k_scale != 0.f ? opts->k_scale : 1.f;
+    p.q_f16 = f16;
     p.negate_q = scale < 0.f;
     p.scale_log2 = (p.negate_q ? -scale : scale) * 1.4426950408889634f;
     p.v_scale = fp8 && opts->v_scale != 0.f ? opts->v_scale : 1.f;
@@ -126,27 +137,24 @@ fd_status launch(TreeParams p, int head_dim, float scale, const fd_options *opts
     c.grid = opts && opts->num_ctas > 0 ? opts->num_ctas : dev.sms < kTreeMaxCtas ? dev.sms : kTreeMaxCtas;
     c.smem_optin = (size_t)dev.smem_optin;
     c.stream = reinterpret_cast<cudaStream_t>(stream);
+    const int load = p.block_table && p.page_size < 8 ? kTreeCopy : fp8 ? kTreeConvert : kTreeTma;
     if (head_dim == 64)
-        plan_tree_smem<64>(&p, &c);
+        plan_tree_smem<64>(&p, &c, load);
     else if (head_dim == 128)
-        plan_tree_smem<128>(&p, &c);
+        plan_tree_smem<128>(&p, &c, load);
     else
-        plan_tree_smem<256>(&p, &c);
-    if (p.v_slots < 2)
+        plan_tree_smem<256>(&p, &c, load);
+    if (p.v_slots < 2 || (load == kTreeConvert && p.raw_slots < 1))
         return FD_ERR_UNSUPPORTED;
-
-    // FP8 codes and pages under 8 tokens (a box's rows would not reach the
-    // swizzle's 1 KB) come through loader threads, the rest by TMA
-    const bool tma = !fp8 && (!p.block_table || p.page_size >= 8);
     p.box_rows = p.block_table && p.page_size < kTileTokens ? p.page_size : kTileTokens;
     alignas(64) CUtensorMap tmk, tmv;
     std::memset(&tmk, 0, sizeof tmk);
     std::memset(&tmv, 0, sizeof tmv);
-    if (tma) {
+    if (load != kTreeCopy) {
         long long rows = p.block_table ? (long long)p.num_pages * p.page_size : (long long)p.batch * p.page_size;
         rows = rows > 0 ? rows : 1;
-        if ((st = encode_kv_map(&tmk, p.k, p.hkv, rows, p.box_rows, true, kv, head_dim)) != FD_OK ||
-            (st = encode_kv_map(&tmv, p.v, p.hkv, rows, p.box_rows, true, kv, head_dim)) != FD_OK)
+        if ((st = encode_kv_map(&tmk, p.k, p.hkv, rows, p.box_rows, !fp8, kv, head_dim)) != FD_OK ||
+            (st = encode_kv_map(&tmv, p.v, p.hkv, rows, p.box_rows, !fp8, kv, head_dim)) != FD_OK)
             return st;
     }
     cudaEvent_t ev0 = opts ? static_cast<cudaEvent_t>(opts->split_start_event) : nullptr;
@@ -154,9 +162,9 @@ fd_status launch(TreeParams p, int head_dim, float scale, const fd_options *opts
     if (ev0 && !record_event(ev0, c.stream))
         return FD_ERR_CUDA;
     cudaError_t e = cudaErrorInvalidValue;
-#define FD_PICK_TREE(D, F16, KV, TMA)                              \
-    if (head_dim == D && f16 == F16 && kv == KV && tma == TMA)      \
-        e = launch_tree_variant<D, F16, KV, TMA>(p, tmk, tmv, c);
+#define FD_PICK_TREE(D, F16, KV, LOAD)                              \
+    if (head_dim == D && kv == KV && load == LOAD)                  \
+        e = launch_tree_variant<D, F16, KV, LOAD>(p, tmk, tmv, c);
     FD_TREE_VARIANTS(FD_PICK_TREE)
 #undef FD_PICK_TREE
     if (e != cudaSuccess)

@@ -61,9 +61,10 @@ struct TreeParams {
     int sum_rows;                  // rows of a group's flushed accumulator: min(128, tree_len * group)
     int box_rows;                  // positions of one TMA box
     int k_slots, v_slots;          // K and V tiles in shared memory
-    uint32_t off_k, off_v, off_misc;
+    int raw_slots;                 // tiles of FP8 codes, of K and of V each
+    uint32_t off_k, off_v, off_raw, off_misc;
     float scale_log2, v_scale;     // scale_log2 >= 0 (a negative scale's sign goes to q)
-    int negate_q, starve;
+    int q_f16, negate_q, starve;
 };
 
 // Request b's cache length and node count; a value out of range is clamped,
@@ -126,20 +127,25 @@ struct TreeLaunch {
     size_t smem_bytes, smem_optin;
     cudaStream_t stream;
 };
-// How the cache reaches shared memory: TMA boxes of 8 positions or more, or
-// loader threads (pages under 8 tokens, and FP8 codes, which they convert).
-template <int D, bool F16, int KV, bool TMA>
+// How the cache reaches shared memory: 16-bit tiles by TMA; FP8 codes by TMA,
+// converted by four warps; or copied by four warps (pages under 8 tokens: a TMA
+// box's rows would not reach the swizzle's 1 KB).
+enum : int { kTreeTma = 0, kTreeConvert = 1, kTreeCopy = 2 };
+
+// F16: the MMAs' type, fp16 or bf16: the query's, and fp16 for FP8 caches.
+template <int D, bool F16, int KV, int LOAD>
 cudaError_t launch_tree_variant(const TreeParams &p, const CUtensorMap &tmk, const CUtensorMap &tmv,
                                 const TreeLaunch &c);
 
 #define FD_TREE_VARIANTS_D(X, D)                                                              \
-    X(D, false, kKvBf16, true) X(D, true, kKvF16, true) X(D, false, kKvBf16, false)            \
-    X(D, true, kKvF16, false) X(D, false, kKvE4m3, false) X(D, true, kKvE4m3, false)           \
-    X(D, false, kKvE5m2, false) X(D, true, kKvE5m2, false)
+    X(D, false, kKvBf16, kTreeTma) X(D, true, kKvF16, kTreeTma)                               \
+    X(D, true, kKvE4m3, kTreeConvert) X(D, true, kKvE5m2, kTreeConvert)                       \
+    X(D, false, kKvBf16, kTreeCopy) X(D, true, kKvF16, kTreeCopy)                             \
+    X(D, true, kKvE4m3, kTreeCopy) X(D, true, kKvE5m2, kTreeCopy)
 #define FD_TREE_VARIANTS(X) FD_TREE_VARIANTS_D(X, 64) FD_TREE_VARIANTS_D(X, 128) FD_TREE_VARIANTS_D(X, 256)
-#define FD_EXTERN_TREE(D, F16, KV, TMA)                                                                           \
-    extern template cudaError_t launch_tree_variant<D, F16, KV, TMA>(const TreeParams &, const CUtensorMap &,     \
-                                                                      const CUtensorMap &, const TreeLaunch &);
+#define FD_EXTERN_TREE(D, F16, KV, LOAD)                                                                          \
+    extern template cudaError_t launch_tree_variant<D, F16, KV, LOAD>(const TreeParams &, const CUtensorMap &,    \
+                                                                       const CUtensorMap &, const TreeLaunch &);
 FD_TREE_VARIANTS(FD_EXTERN_TREE)
 #undef FD_EXTERN_TREE
 

@@ -7,9 +7,14 @@
 //     P = exp2(S scale log2(e) - m)   a thread per row: a running maximum m and sum l
 //     O = O + P V      128 x D,  tcgen05, P in tensor memory, V in shared memory
 //
-//   * two loaders bring K and V tiles into rings of shared-memory slots, in the
-//     128-byte swizzled layout that the MMAs read: parts of 64 dims, a part
-//     being N rows of 128 bytes;
+//   * K and V tiles come into rings of shared-memory slots, in the 128-byte
+//     swizzled layout that the MMAs read: parts of 64 dims, a part being N rows
+//     of 128 bytes.  A warp for K and one for V load 16-bit caches by TMA.  FP8
+//     codes come by TMA into rings of their own, and four warps convert them to
+//     fp16 (every FP8 value is one), the type of that call's MMAs; a bf16 query
+//     is then scaled by a power of two a row, so that fp16 holds it: an element
+//     of less than 2^-29 of its row's largest loses bits, by at most 2^-40 of
+//     that largest.  Pages under 8 tokens are copied by the four warps;
 //   * one thread issues the MMAs; their completion releases the slots;
 //   * two groups of 128 threads (one for D = 256, whose accumulator fills half
 //     the tensor memory) hold one query row a thread and turn S into P in
@@ -86,6 +91,33 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]
                  "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
                  : "memory");
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+                   "=r"(r[15])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+                 "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+                 "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+                 : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Instruction descriptor of a dense kind::f16 MMA (A and B both fp16, or both
@@ -124,6 +156,26 @@ __device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint64_t b, 
                  : "memory");
 }
 
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until at most N of this thread's groups of copies are in flight.
+template <int N>
+__device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A thread's register limit; all warps of a warpgroup execute it.
+template <int N>
+__device__ __forceinline__ void regs_more()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_fewer()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 __device__ __forceinline__ uint64_t l2_policy_evict_normal()
 {
     uint64_t p;
@@ -140,21 +192,36 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint4 v)
 // ---------------------------------------------------------------- layout
 
 constexpr int kTreeMaxSlots = 6;
+constexpr int kTreeMaxRaw = 4;
 
-template <int D, bool TMA>
+template <int D, int LOAD>
 struct TreeCfg {
     static constexpr int kN = tree_tile(D);
     static constexpr int kGroups = tree_groups(D);
     static constexpr int kSoftWarps = 4 * kGroups;
     static constexpr int kSoftThreads = 32 * kSoftWarps;
-    static constexpr int kLoadWarps = TMA ? 1 : 4;                // of K, and as many of V
-    static constexpr int kMmaWarp = kSoftWarps + 2 * kLoadWarps;
-    static constexpr int kThreads = 32 * (kMmaWarp + 1);
+    static constexpr int kCopyWarps = LOAD == kTreeTma ? 0 : 4;   // they convert, or copy small pages
+    static constexpr int kCopyThreads = 32 * kCopyWarps;
+    static constexpr int kLoadWarp = kSoftWarps + kCopyWarps;     // K by TMA; the next one V
+    static constexpr int kMmaWarp = kLoadWarp + 2;
+    static constexpr int kWarps = kLoadWarp + 4;                  // whole warpgroups
+    static constexpr int kThreads = 32 * kWarps;
     static constexpr int kParts = D / 64;
     static constexpr int kPartBytes = kN * 128;                   // of a K or V tile
     static constexpr int kSlotBytes = kParts * kPartBytes;
+    static constexpr int kRawBytes = kN * D;                      // of a tile of FP8 codes
     static constexpr int kQBytes = 128 * D * 2;                   // 128 query rows
     static constexpr int kFlush = kTreeFlush * 128 / kN;          // units between flushes
+    // Registers.  A softmax thread holds a row's 128 scores and some 70 more;
+    // two groups of them need more than a block's even share, so the other
+    // warps give some of theirs up (setmaxnreg): 216 x 256 + 72 x 128 =
+    // 168 x 384, and 200 x 256 + 56 x 256 = 128 x 512 registers.
+    static constexpr bool kSplitRegs = kGroups == 2;
+    static constexpr int kLaunchRegs = LOAD == kTreeTma ? 168 : 128;
+    static constexpr int kSoftRegs = LOAD == kTreeTma ? 216 : 200;
+    static constexpr int kOtherRegs = LOAD == kTreeTma ? 72 : 56;
+    static_assert(!kSplitRegs || kSoftRegs * kSoftThreads + kOtherRegs * (kThreads - kSoftThreads) <= kLaunchRegs * kThreads,
+                  "the shares come out of what the block was launched with");
     // tensor memory: two score buffers, then the accumulators
     static constexpr uint32_t kTmemO = 256;
     static constexpr uint32_t kTmemCols = 512;
@@ -162,12 +229,15 @@ struct TreeCfg {
 
 struct TreeMisc {
     uint64_t kfull[kTreeMaxSlots], kempty[kTreeMaxSlots], vfull[kTreeMaxSlots], vempty[kTreeMaxSlots];
+    uint64_t rkfull[kTreeMaxRaw], rkempty[kTreeMaxRaw], rvfull[kTreeMaxRaw], rvempty[kTreeMaxRaw];
     uint64_t sfull[2], pfull[2], pvdone[2], qfull, pair, drain;
     long long scan[18];
     long long segpos, x1;
     int b, seg, j, abort;
     uint32_t tmem;
     unsigned int bad[kMaxTree / 32];   // nodes whose V row is not finite
+    // a softmax thread's running maximum and sum at the end of a segment; at its
+    // start (FP8) the power of two that the row was divided by
     float2 ml[2][128];
 };
 
@@ -265,17 +335,34 @@ __device__ __forceinline__ uint32_t tree_bits(const TreeParams &p, const uint64_
 
 // ---------------------------------------------------------------- roles
 
-// K or V tiles by TMA: lane = (box, part).
-template <int D, bool IS_K>
+// A ring of slots as one of its sides sees it.
+struct TreeRing {
+    int slot;
+    uint32_t ph;
+    __device__ __forceinline__ void next(int slots)
+    {
+        if (++slot == slots) {
+            slot = 0;
+            ph ^= 1u;
+        }
+    }
+};
+
+// K or V tiles by TMA, 16-bit ones as (box, part) pairs, FP8 codes as whole
+// rows; a lane issues one copy.
+template <int D, int LOAD, bool IS_K>
 __device__ __forceinline__ void tree_load_tma(const TreeParams &p, TreeMisc &m, const CUtensorMap *map, uint32_t ring,
                                               int slots, int lane)
 {
-    using C = TreeCfg<D, true>;
-    const uint32_t full0 = smem_addr(IS_K ? m.kfull : m.vfull), empty0 = smem_addr(IS_K ? m.kempty : m.vempty);
+    using C = TreeCfg<D, LOAD>;
+    constexpr bool kRaw = LOAD == kTreeConvert;
+    constexpr int kParts = kRaw ? 1 : C::kParts, kRowBytes = kRaw ? D : 128;
+    uint64_t *full = kRaw ? (IS_K ? m.rkfull : m.rvfull) : (IS_K ? m.kfull : m.vfull);
+    uint64_t *empty = kRaw ? (IS_K ? m.rkempty : m.rvempty) : (IS_K ? m.kempty : m.vempty);
     volatile int *abort_flag = &m.abort;
-    const int box = lane / C::kParts, part = lane % C::kParts;
-    int slot = 0, issued = 0;
-    uint32_t ph = 0;
+    const int box = lane / kParts, part = lane % kParts;
+    TreeRing r = {0, 0};
+    int issued = 0;
     TreeWalk<D> w;
     bool ok = true;
     for (w.start(p, m); ok && w.n > 0; w.next(p)) {
@@ -288,152 +375,179 @@ __device__ __forceinline__ void tree_load_tma(const TreeParams &p, TreeMisc &m, 
             int row = 0;
             if (box < boxes)
                 row = tree_row(p, w.b, t0 + box * p.box_rows, IS_K);
-            ok = mbar_wait_bounded(empty0 + 8 * slot, ph ^ 1u, p.timeout_ns, abort_flag);
+            ok = mbar_wait_bounded(smem_addr(&empty[r.slot]), r.ph ^ 1u, p.timeout_ns, abort_flag);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok)
                 break;
-            const uint32_t full = full0 + 8 * slot;
+            const uint32_t bar = smem_addr(&full[r.slot]);
             if (lane == 0)
-                mbar_arrive_expect_tx(full, (uint32_t)(boxes * C::kParts * p.box_rows * 128) +
-                                                (IS_K && p.starve && issued == 0 && blockIdx.x == 0 ? 16u : 0u));
+                mbar_arrive_expect_tx(bar, (uint32_t)(boxes * kParts * p.box_rows * kRowBytes) +
+                                               (IS_K && p.starve && issued == 0 && blockIdx.x == 0 ? 16u : 0u));
             __syncwarp();
             if (box < boxes)
-                tma_load_3d(ring + slot * C::kSlotBytes + part * C::kPartBytes + box * p.box_rows * 128, map, full,
-                            part * 64, g, row, policy);
+                tma_load_3d(ring + r.slot * (kRaw ? C::kRawBytes : C::kSlotBytes) + part * C::kPartBytes +
+                                box * p.box_rows * kRowBytes,
+                            map, bar, part * 64, g, row, policy);
             ++issued;
-            if (++slot == slots) {
-                slot = 0;
-                ph ^= 1u;
-            }
+            r.next(slots);
         }
     }
-    if (!ok) {
-        // gave up: wait (bounded) for the copies in flight before the CTA ends
-        if (lane == 0) {
+    if (lane == 0) {
+        // Every release has arrived: nothing signals this CTA's barriers any
+        // more.  Having given up, wait (bounded) for the copies in flight instead.
+        for (int k = 0; ok && k < slots; ++k, r.next(slots))
+            ok = mbar_wait_bounded(smem_addr(&empty[r.slot]), r.ph ^ 1u, p.timeout_ns, abort_flag);
+        if (!ok) {
             atomicOr(p.ws_err, kErrTimeout);
             *abort_flag = 1;
-            for (int k = 0; k < min(issued, slots); ++k) {
-                if (slot == 0) {
-                    slot = slots;
-                    ph ^= 1u;
-                }
-                --slot;
-                mbar_wait_bounded(full0 + 8 * slot, ph, p.timeout_ns, nullptr);
-            }
-        }
-    } else if (lane == 0) {
-        // every release has arrived: nothing signals this CTA's barriers any more
-        for (int k = 0; k < slots; ++k) {
-            if (!mbar_wait_bounded(empty0 + 8 * slot, ph ^ 1u, p.timeout_ns, abort_flag)) {
-                atomicOr(p.ws_err, kErrTimeout);
-                *abort_flag = 1;
-                break;
-            }
-            if (++slot == slots) {
-                slot = 0;
-                ph ^= 1u;
-            }
+            for (int k = max(0, issued - slots); k < issued; ++k)
+                mbar_wait_bounded(smem_addr(&full[k % slots]), (uint32_t)(k / slots) & 1u, p.timeout_ns, nullptr);
         }
     }
     __syncwarp();
 }
 
-// K or V tiles by 128 threads: 16 (8) bytes of the cache, converted from FP8
-// codes if it holds those, to the swizzled 16-bit tile.
-template <int D, bool F16, int KV, bool IS_K>
-__device__ __forceinline__ void tree_load_threads(const TreeParams &p, TreeMisc &m, uint32_t ring, int slots, int tid)
+// One tile of FP8 codes (rows of D bytes) to the swizzled fp16 tile.  A unit is
+// 16 codes; eight lanes that store together take 4 units of 2 rows, whose
+// chunks fall into different banks.
+template <int D, int KV>
+__device__ __forceinline__ void tree_convert(uint32_t raw, uint32_t tile, int tid)
 {
-    using C = TreeCfg<D, false>;
-    constexpr int kThreads = 32 * C::kLoadWarps;
-    constexpr bool kFp8 = kv_is_fp8(KV);
-    constexpr int kPer = 16;                              // elements a thread handles at once
-    constexpr int kRowUnits = D / kPer;
-    constexpr int kRounds = C::kN * kRowUnits / kThreads;   // units a thread has of a tile
-    constexpr int kBatch = kRounds < 4 ? kRounds : 4;
-    static_assert(C::kN * kRowUnits % kThreads == 0 && kRounds % kBatch == 0 && kThreads % kRowUnits == 0, "whole rounds");
-    const uint32_t full0 = smem_addr(IS_K ? m.kfull : m.vfull), empty0 = smem_addr(IS_K ? m.kempty : m.vempty);
-    volatile int *abort_flag = &m.abort;
-    const uint8_t *cache = IS_K ? p.k : p.v;
-    const int unit = tid % kRowUnits, row0 = tid / kRowUnits;
-    constexpr int kRowStep = kThreads / kRowUnits;
-    int slot = 0;
-    bool first = true;
-    uint32_t ph = 0;
-    TreeWalk<D> w;
-    bool ok = true;
-    for (w.start(p, m); ok && w.n > 0; w.next(p)) {
-        const int g = w.seg / w.s.groups;
-        for (int j = w.j0; j < w.j0 + w.n; ++j) {
-            const int t0 = j * C::kN, valid = min(C::kN, w.r.L - t0);
-            ok = mbar_wait_bounded(empty0 + 8 * slot, ph ^ 1u, p.timeout_ns, abort_flag);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok)
-                break;
-            const uint32_t tile = ring + slot * C::kSlotBytes;
+    using C = TreeCfg<D, kTreeConvert>;
+    constexpr int kRowUnits = D / 16, kUnits = C::kN * kRowUnits;
+    static_assert(kUnits % C::kCopyThreads == 0, "whole rounds");
+#pragma unroll 4
+    for (int e = tid; e < kUnits; e += C::kCopyThreads) {
+        const int quad = e / 8, in = e & 7;                     // 8 lanes: units 4 n .. 4 n + 3 of rows 2 k, 2 k + 1
+        const int row = 2 * (quad / (kRowUnits / 4)) + (in >> 2), unit = 4 * (quad % (kRowUnits / 4)) + (in & 3);
+        const uint4 x = lds128(raw + row * D + unit * 16);
+        const uint32_t at = tile + (unit / 4) * C::kPartBytes + row * 128;
+        const int c = 2 * (unit & 3);
+        sts128(at + ((c ^ (row & 7)) << 4), make_uint4(fp8x2_to_f16x2<KV>(lo16(x.x)), fp8x2_to_f16x2<KV>(hi16(x.x)),
+                                                       fp8x2_to_f16x2<KV>(lo16(x.y)), fp8x2_to_f16x2<KV>(hi16(x.y))));
+        sts128(at + (((c + 1) ^ (row & 7)) << 4),
+               make_uint4(fp8x2_to_f16x2<KV>(lo16(x.z)), fp8x2_to_f16x2<KV>(hi16(x.z)), fp8x2_to_f16x2<KV>(lo16(x.w)),
+                          fp8x2_to_f16x2<KV>(hi16(x.w))));
+    }
+}
+
+// Small pages: one tile's rows by 128 threads, converted on the way if they
+// are FP8 codes; 16-bit rows by asynchronous copies, complete after
+// cp_async_wait.  Rows from `valid` on are left as they are.
+template <int D, int KV>
+__device__ __forceinline__ void tree_copy_rows(const TreeParams &p, const uint8_t *cache, const TreeWalk<D> &w, int t0,
+                                               int valid, uint32_t tile, int tid, bool report)
+{
+    using C = TreeCfg<D, kTreeCopy>;
+    const int g = w.seg / w.s.groups;
+    if constexpr (kv_is_fp8(KV)) {
+        constexpr int kRowUnits = D / 16, kStep = C::kCopyThreads / kRowUnits, kBatch = 4;
+        const int unit = tid % kRowUnits, c = 2 * (unit & 3);
+        for (int r0 = tid / kRowUnits; r0 < valid; r0 += kStep * kBatch) {
+            uint4 x[kBatch];
 #pragma unroll
-            for (int r0 = 0; r0 < kRounds; r0 += kBatch) {
-                uint4 x[kBatch][kFp8 ? 1 : 2];
+            for (int k = 0; k < kBatch; ++k)
+                if (r0 + k * kStep < valid)
+                    x[k] = ldg128_nc(cache + ((long long)tree_row(p, w.b, t0 + r0 + k * kStep, report && unit == 0) * p.hkv + g) * D + unit * 16);
 #pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    const int row = row0 + (r0 + k) * kRowStep;
-                    x[k][0] = make_uint4(0, 0, 0, 0);
-                    if (!kFp8)
-                        x[k][kFp8 ? 0 : 1] = make_uint4(0, 0, 0, 0);
-                    if (row < valid) {
-                        const long long at = ((long long)tree_row(p, w.b, t0 + row, IS_K && unit == 0) * p.hkv + g) * D + unit * kPer;
-                        const uint8_t *src = cache + (kFp8 ? at : 2 * at);
-                        x[k][0] = ldg128_nc(src);
-                        if (!kFp8)
-                            x[k][kFp8 ? 0 : 1] = ldg128_nc(src + 16);
-                    }
-                }
-#pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    const int row = row0 + (r0 + k) * kRowStep;
-                    const int c = (2 * unit) & 7;   // the unit's first 16-byte chunk in its part
-                    const uint32_t at = tile + (2 * unit / 8) * C::kPartBytes + row * 128;
-                    if constexpr (kFp8) {
-                        const uint32_t in[4] = {x[k][0].x, x[k][0].y, x[k][0].z, x[k][0].w};
-                        uint32_t out[8];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const uint32_t a = fp8x2_to_f16x2<KV>(lo16(in[e])), b = fp8x2_to_f16x2<KV>(hi16(in[e]));
-                            if constexpr (F16) {
-                                out[2 * e] = a;
-                                out[2 * e + 1] = b;
-                            } else {   // exact: an FP8 value has at most 4 significant bits
-                                const float2 fa = f16x2_to_float2(a), fb = f16x2_to_float2(b);
-                                out[2 * e] = pack_bf16x2(fa.x, fa.y);
-                                out[2 * e + 1] = pack_bf16x2(fb.x, fb.y);
-                            }
-                        }
-                        sts128(at + ((c ^ (row & 7)) << 4), make_uint4(out[0], out[1], out[2], out[3]));
-                        sts128(at + (((c + 1) ^ (row & 7)) << 4), make_uint4(out[4], out[5], out[6], out[7]));
-                    } else {
-                        sts128(at + ((c ^ (row & 7)) << 4), x[k][0]);
-                        sts128(at + (((c + 1) ^ (row & 7)) << 4), x[k][kFp8 ? 0 : 1]);
-                    }
-                }
-            }
-            fence_async_shared();
-            // the test hook leaves out one arrival, so that the tile never becomes full
-            if (!(IS_K && p.starve && first && blockIdx.x == 0 && tid == 0))
-                mbar_arrive(full0 + 8 * slot);
-            first = false;
-            if (++slot == slots) {
-                slot = 0;
-                ph ^= 1u;
+            for (int k = 0; k < kBatch; ++k) {
+                const int row = r0 + k * kStep;
+                if (row >= valid)
+                    break;
+                const uint32_t at = tile + (unit / 4) * C::kPartBytes + row * 128;
+                sts128(at + ((c ^ (row & 7)) << 4),
+                       make_uint4(fp8x2_to_f16x2<KV>(lo16(x[k].x)), fp8x2_to_f16x2<KV>(hi16(x[k].x)),
+                                  fp8x2_to_f16x2<KV>(lo16(x[k].y)), fp8x2_to_f16x2<KV>(hi16(x[k].y))));
+                sts128(at + (((c + 1) ^ (row & 7)) << 4),
+                       make_uint4(fp8x2_to_f16x2<KV>(lo16(x[k].z)), fp8x2_to_f16x2<KV>(hi16(x[k].z)),
+                                  fp8x2_to_f16x2<KV>(lo16(x[k].w)), fp8x2_to_f16x2<KV>(hi16(x[k].w))));
             }
         }
+    } else {
+        constexpr int kChunks = D / 8, kStep = C::kCopyThreads / kChunks;
+        const int chunk = tid % kChunks;
+        const uint64_t policy = w.s.groups > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
+        for (int row = tid / kChunks; row < valid; row += kStep) {
+            const long long at = ((long long)tree_row(p, w.b, t0 + row, report && chunk == 0) * p.hkv + g) * D + chunk * 8;
+            cp_async_16(tile + (chunk / 8) * C::kPartBytes + row * 128 + (((chunk & 7) ^ (row & 7)) << 4), cache + 2 * at, policy);
+        }
+    }
+}
+
+// The four warps that convert FP8 tiles, or copy small pages: K and V tiles in
+// turn.  Copies of one tile run while the next one's are issued.
+template <int D, int KV, int LOAD>
+__device__ __forceinline__ void tree_copy(const TreeParams &p, TreeMisc &m, uint32_t k_ring, uint32_t v_ring,
+                                          uint32_t raw_k, uint32_t raw_v, int tid)
+{
+    using C = TreeCfg<D, LOAD>;
+    constexpr bool kAsync = LOAD == kTreeCopy && !kv_is_fp8(KV);
+    volatile int *abort_flag = &m.abort;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        const bool r = mbar_wait_bounded(smem_addr(bar), parity, p.timeout_ns, abort_flag);
+        return __all_sync(0xffffffffu, r) != 0;
+    };
+    TreeRing rk = {0, 0}, rv = {0, 0}, rr = {0, 0};
+    uint64_t *pending = nullptr;   // the full barrier of a tile whose copies are in flight
+    auto finish = [&]() {
+        fence_async_shared();      // the MMAs read what these threads wrote
+        mbar_arrive(smem_addr(pending));
+        pending = nullptr;
+    };
+    bool ok = true, first = true;
+    TreeWalk<D> w;
+    for (w.start(p, m); ok && w.n > 0; w.next(p))
+        for (int j = w.j0; ok && j < w.j0 + w.n; ++j) {
+            const int t0 = j * C::kN, valid = min(C::kN, w.r.L - t0);
+#pragma unroll 1
+            for (int half = 0; ok && half < 2; ++half) {
+                TreeRing &r = half ? rv : rk;
+                uint64_t *full = half ? &m.vfull[r.slot] : &m.kfull[r.slot], *empty = half ? &m.vempty[r.slot] : &m.kempty[r.slot];
+                const uint32_t tile = (half ? v_ring : k_ring) + r.slot * C::kSlotBytes;
+                if (kAsync && pending && !__all_sync(0xffffffffu, mbar_try_wait(smem_addr(empty), r.ph ^ 1u))) {
+                    // do not hold a tile back while waiting for a slot
+                    cp_async_wait<0>();
+                    finish();
+                }
+                if (!(ok = wait(empty, r.ph ^ 1u)))
+                    break;
+                if constexpr (LOAD == kTreeConvert) {
+                    if (!(ok = wait(half ? &m.rvfull[rr.slot] : &m.rkfull[rr.slot], rr.ph)))
+                        break;
+                    tree_convert<D, KV>((half ? raw_v : raw_k) + rr.slot * C::kRawBytes, tile, tid);
+                    mbar_arrive(smem_addr(half ? &m.rvempty[rr.slot] : &m.rkempty[rr.slot]));
+                } else
+                    tree_copy_rows<D, KV>(p, half ? p.v : p.k, w, t0, valid, tile, tid, !half);
+                // the test hook leaves out an arrival, so that the first tile never becomes full
+                const bool starve = LOAD == kTreeCopy && p.starve && first && blockIdx.x == 0 && tid == 0;
+                first = false;
+                if constexpr (kAsync) {
+                    cp_async_commit();
+                    if (pending) {
+                        cp_async_wait<1>();
+                        finish();
+                    }
+                    if (!starve)
+                        pending = full;
+                } else if (!starve) {
+                    pending = full;
+                    finish();
+                }
+                r.next(half ? p.v_slots : p.k_slots);
+            }
+            if (LOAD == kTreeConvert)
+                rr.next(p.raw_slots);
+        }
+    if (kAsync) {
+        cp_async_wait<0>();
+        if (ok && pending)
+            finish();
     }
     // every release has arrived: nothing signals this CTA's barriers any more
-    for (int k = 0; ok && k < slots; ++k) {
-        ok = mbar_wait_bounded(empty0 + 8 * slot, ph ^ 1u, p.timeout_ns, abort_flag);
-        if (++slot == slots) {
-            slot = 0;
-            ph ^= 1u;
-        }
-    }
+    for (int k = 0; ok && k < p.k_slots; ++k, rk.next(p.k_slots))
+        ok = wait(&m.kempty[rk.slot], rk.ph ^ 1u);
+    for (int k = 0; ok && k < p.v_slots; ++k, rv.next(p.v_slots))
+        ok = wait(&m.vempty[rv.slot], rv.ph ^ 1u);
     if (!ok) {
         atomicOr(p.ws_err, kErrTimeout);
         *abort_flag = 1;
@@ -465,11 +579,11 @@ __device__ __forceinline__ TreeUnits tree_units(const TreeParams &p, const TreeW
 }
 
 // The MMA issuer: one thread.
-template <int D, bool F16, bool TMA>
+template <int D, bool F16, int LOAD>
 __device__ __forceinline__ void tree_mma(const TreeParams &p, TreeMisc &m, uint32_t q_smem, uint32_t k_ring,
                                          uint32_t v_ring, uint32_t tmem)
 {
-    using C = TreeCfg<D, TMA>;
+    using C = TreeCfg<D, LOAD>;
     constexpr uint32_t kIdescS = umma_idesc_f16(128, C::kN, F16, false);
     constexpr uint32_t kIdescO = umma_idesc_f16(128, D, F16, true);
     volatile int *abort_flag = &m.abort;
@@ -548,36 +662,71 @@ __device__ __forceinline__ void tree_mma(const TreeParams &p, TreeMisc &m, uint3
 }
 
 // Copies this CTA's query rows of a segment into the swizzled operand: rows
-// [0, 128) of one 128-row tile, by `threads` threads.  Rows without a node are zero.
-template <int D>
+// [first_row, first_row + 128) by THREADS threads, all loads in flight
+// together.  Rows without a node are zero.  For FP8 caches (TO_F16) bf16 rows
+// become fp16 ones divided by a power of two that brings their largest element
+// to [2^14, 2^15); power[r] and power2[r] get it.
+template <int D, int THREADS, bool TO_F16>
 __device__ __forceinline__ void tree_load_q(const TreeParams &p, const TreeWalk<D> &w, uint32_t q_smem, int first_row,
-                                            int tid, int threads)
+                                            int tid, [[maybe_unused]] float2 *power, [[maybe_unused]] float2 *power2)
 {
-    constexpr int kChunks = D / 8;
+    constexpr int kChunks = D / 8, kStep = THREADS / kChunks, kRounds = 128 / kStep, kBatch = kRounds < 8 ? kRounds : 8;
     const int g = w.seg / w.s.groups;
     const uint32_t flip = p.negate_q ? 0x80008000u : 0u;
     const int chunk = tid % kChunks;
-    for (int r = tid / kChunks; r < 128; r += threads / kChunks) {
-        const int row = first_row + r, i = row / p.group, h = row - i * p.group;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (i < w.r.t) {
-            x = __ldg(reinterpret_cast<const uint4 *>(
-                    p.q + (((long long)w.b * p.tree_len + i) * p.hq + g * p.group + h) * D) + chunk);
-            x.x ^= flip;
-            x.y ^= flip;
-            x.z ^= flip;
-            x.w ^= flip;
+#pragma unroll 1
+    for (int n = 0; n < kRounds; n += kBatch) {
+        uint4 x[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int row = first_row + tid / kChunks + (n + k) * kStep, i = row / p.group, h = row - i * p.group;
+            x[k] = make_uint4(0, 0, 0, 0);
+            if (i < w.r.t)
+                x[k] = __ldg(reinterpret_cast<const uint4 *>(
+                                 p.q + (((long long)w.b * p.tree_len + i) * p.hq + g * p.group + h) * D) + chunk);
         }
-        sts128(q_smem + (chunk / 8) * (128 * 128) + r * 128 + (((chunk & 7) ^ (r & 7)) << 4), x);
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int r = tid / kChunks + (n + k) * kStep;
+            uint32_t v[4] = {x[k].x ^ flip, x[k].y ^ flip, x[k].z ^ flip, x[k].w ^ flip};
+            if constexpr (TO_F16) {
+                float up = 1.f;   // the power of two
+                if (!p.q_f16) {
+                    float top = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 f = bf16x2_to_float2(v[e]);
+                        top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+                    }
+#pragma unroll
+                    for (int off = kChunks / 2; off; off >>= 1)
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+                    // exponent of the largest, kept where 2^(+-) are normal numbers (infinite: the largest one)
+                    const int ex = min(max((__float_as_int(top) >> 23 & 255) - 127 - 14, -120), 113);
+                    up = __int_as_float((127 + ex) << 23);
+                    const float down = __int_as_float((127 - ex) << 23);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 f = bf16x2_to_float2(v[e]);
+                        v[e] = pack_f16x2(f.x * down, f.y * down);
+                    }
+                }
+                if (chunk == 0) {
+                    power[r].x = up;
+                    power2[r].x = up;
+                }
+            }
+            sts128(q_smem + (chunk / 8) * (128 * 128) + r * 128 + (((chunk & 7) ^ (r & 7)) << 4), make_uint4(v[0], v[1], v[2], v[3]));
+        }
     }
 }
 
 // V tile rows from `from` on: those at or past `valid` become zero, and in the
 // others (tree nodes) elements that are not finite do, their node marked in bad.
-template <int D, bool F16, bool TMA>
+template <int D, bool F16, int LOAD>
 __device__ __forceinline__ void tree_clean_v(uint32_t tile, int from, int valid, int node0, unsigned int *bad, int tid)
 {
-    using C = TreeCfg<D, TMA>;
+    using C = TreeCfg<D, LOAD>;
     constexpr int kChunks = D / 8;
     constexpr uint32_t kExp = F16 ? 0x7c00u : 0x7f80u;
     for (int e = from * kChunks + tid; e < C::kN * kChunks; e += 128) {
@@ -620,11 +769,11 @@ __device__ __forceinline__ float tree_element(const uint8_t *cache, long long e)
 }
 
 // A group of 128 threads, one query row each.
-template <int D, bool F16, int KV, bool TMA>
+template <int D, bool F16, int KV, int LOAD>
 __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, uint32_t q_smem, uint32_t v_ring,
                                              uint32_t tmem)
 {
-    using C = TreeCfg<D, TMA>;
+    using C = TreeCfg<D, LOAD>;
     // fp16 weights: 2^8 more keeps weights down to 2^-33 of the largest among
     // the 16-bit parts (fp16 ends at 2^-25), and 2^7 of slack ends at 2^15.
     constexpr float kShift = F16 ? 8.f : 0.f, kSlack = F16 ? 7.f : 8.f;
@@ -635,8 +784,8 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
     const bool shared_rows = C::kGroups == 2 && !own_rows;
     const uint32_t t_lane = tmem + ((uint32_t)lane_base << 16);
     const uint32_t t_o = t_lane + C::kTmemO + (C::kGroups == 2 ? group * D : 0);
-    const float sl = p.scale_log2;
-    uint32_t sph = 0, pvph = 0, pairph = 0;
+    float sl = p.scale_log2;                         // FP8: times the row's power of two
+    uint32_t qph = 0, sph = 0, pvph = 0, pairph = 0;
     int vcount = 0;                                  // tiles before the current segment
     bool ok = true;
     auto wait = [&](uint64_t *bar, uint32_t parity) {
@@ -686,9 +835,9 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
     auto load_q = [&]() {
         const int first = (w.seg % w.s.groups) * p.rows;
         if (shared_rows)
-            tree_load_q<D>(p, w, q_smem, first, threadIdx.x, C::kSoftThreads);
+            tree_load_q<D, C::kSoftThreads, kv_is_fp8(KV)>(p, w, q_smem, first, threadIdx.x, m.ml[0], m.ml[1]);
         else
-            tree_load_q<D>(p, w, q_smem + group * C::kQBytes, first + group * 128, tid, 128);
+            tree_load_q<D, 128, kv_is_fp8(KV)>(p, w, q_smem + group * C::kQBytes, first + group * 128, tid, m.ml[group], m.ml[group]);
         fence_async_shared();
         tc_fence_before();
         mbar_arrive(smem_addr(&m.qfull));
@@ -703,6 +852,12 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
         const bool in_call = i < p.tree_len, live = i < t && base + i >= 0;
         const bool warp_live = __any_sync(0xffffffffu, live);
         const uint64_t *mask_row = p.mask && in_call ? p.mask + w.b * p.mask_stride + (long long)i * p.words : nullptr;
+        if constexpr (kv_is_fp8(KV)) {
+            if (!(ok = wait(&m.qfull, qph)))
+                break;
+            qph ^= 1u;
+            sl = p.scale_log2 * m.ml[group][tid].x;
+        }
         float mx = kNegInf, l = 0.f;
         int mine = 0;                                // units of this group so far in the segment
         // own rows: unit 2 j + group (or j); shared: units group, group + 2, ..
@@ -727,23 +882,32 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
                 flushed_at = mx;
             }
             if (warp_live) {
-                float tm = kNegInf;
+                // the row's scores stay in registers: one round trip to tensor
+                // memory a tile, and independent work to hide it behind
+                uint32_t s[C::kN / 32][32];
+                uint32_t bits[C::kN / 32];
+#pragma unroll
+                for (int c = 0; c < C::kN / 32; ++c)
+                    tmem_ld32(t_s + 32 * c, s[c]);
+                if (tail)
+#pragma unroll
+                    for (int c = 0; c < C::kN / 32; ++c)
+                        bits[c] = live ? tree_bits(p, mask_row, i, t0 + 32 * c - base, t) : 0u;
+#pragma unroll
+                for (int c = 0; c < C::kN / 32; ++c)
+                    tmem_wait_ld32(s[c]);
+                float top[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
 #pragma unroll
                 for (int c = 0; c < C::kN / 32; ++c) {
-                    uint32_t s[32];
-                    tmem_ld32(t_s + 32 * c, s);
-                    tmem_wait_ld32(s);
-                    if (tail) {
-                        const uint32_t bits = live ? tree_bits(p, mask_row, i, t0 + 32 * c - base, t) : 0u;
+                    if (tail)
 #pragma unroll
                         for (int k = 0; k < 32; ++k)
-                            tm = fmaxf(tm, bits >> k & 1u ? __uint_as_float(s[k]) : kNegInf);
-                    } else {
+                            s[c][k] = bits[c] >> k & 1u ? s[c][k] : 0xff800000u;   // -inf
 #pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            tm = fmaxf(tm, __uint_as_float(s[k]));
-                    }
+                    for (int k = 0; k < 32; ++k)
+                        top[k & 3] = fmaxf(top[k & 3], __uint_as_float(s[c][k]));
                 }
+                const float tm = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                 const bool grow = tm > mx && (mx == kNegInf || (tm - mx) * sl > kSlack);
                 if (__any_sync(0xffffffffu, grow)) {
                     const float corr = grow ? (mx == kNegInf ? 0.f : exp2_approx((mx - tm) * sl)) : 1.f;
@@ -757,48 +921,42 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
                             break;
                         if (C::kGroups == 1)
                             tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < D / 16; ++c) {
+                            uint32_t o[16];
+                            tmem_ld16(t_o + 16 * c, o);
+                            tmem_wait_ld16(o);
 #pragma unroll
-                        for (int c = 0; c < D / 32; ++c) {
-                            uint32_t o[32];
-                            tmem_ld32(t_o + 32 * c, o);
-                            tmem_wait_ld32(o);
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
+                            for (int k = 0; k < 16; ++k)
                                 o[k] = __float_as_uint(__uint_as_float(o[k]) * corr);
-                            tmem_st32(t_o + 32 * c, o);
+                            tmem_st16(t_o + 16 * c, o);
                         }
                     }
                 }
                 const float off = kShift - (mx == kNegInf ? 0.f : mx * sl);
                 const float2 sl2 = make_float2(sl, sl), off2 = make_float2(off, off), one2 = make_float2(1.f, 1.f),
                              neg2 = make_float2(-1.f, -1.f);
-                float2 sum = make_float2(0.f, 0.f);
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                 for (int c = 0; c < C::kN / 32; ++c) {
-                    uint32_t s[32];
-                    tmem_ld32(t_s + 32 * c, s);
-                    uint32_t bits = 0xffffffffu;
-                    if (tail)
-                        bits = live ? tree_bits(p, mask_row, i, t0 + 32 * c - base, t) : 0u;
-                    tmem_wait_ld32(s);
                     uint32_t out[32];
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
-                        float2 x = fma2(make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), sl2, off2);
+                        float2 x = fma2(make_float2(__uint_as_float(s[c][2 * k]), __uint_as_float(s[c][2 * k + 1])), sl2, off2);
                         x.x = exp2_approx(x.x);
                         x.y = exp2_approx(x.y);
-                        if (tail) {
-                            x.x = bits >> (2 * k) & 1u ? x.x : 0.f;
-                            x.y = bits >> (2 * k + 1) & 1u ? x.y : 0.f;
+                        if (tail) {   // also where the scale is 0 and -inf became NaN
+                            x.x = bits[c] >> (2 * k) & 1u ? x.x : 0.f;
+                            x.y = bits[c] >> (2 * k + 1) & 1u ? x.y : 0.f;
                         }
-                        sum = fma2(x, one2, sum);
+                        sum[k & 1] = fma2(x, one2, sum[k & 1]);
                         out[k] = pack_x2<F16>(x.x, x.y);
                         const float2 rest = fma2(x2_to_float2<F16>(out[k]), neg2, x);
                         out[16 + k] = pack_x2<F16>(rest.x, rest.y);
                     }
                     tmem_st32(t_s + 32 * c, out);
                 }
-                l += sum.x + sum.y;
+                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                 tmem_wait_st();
             }
             if (tail) {
@@ -807,7 +965,7 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
                 if (!own_rows || group == 0) {
                     if (!(ok = wait(&m.vfull[vs], ((vcount + tile) / p.v_slots) & 1)))
                         break;
-                    tree_clean_v<D, F16, TMA>(v_ring + vs * C::kSlotBytes, max(0, base - t0), L - t0, t0 - base, m.bad, tid);
+                    tree_clean_v<D, F16, LOAD>(v_ring + vs * C::kSlotBytes, max(0, base - t0), L - t0, t0 - base, m.bad, tid);
                     fence_async_shared();
                 }
             }
@@ -816,6 +974,11 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
             pvph ^= 1u;
         }
         if (!ok)
+            break;
+        // the accumulator's last MMAs.  With two groups the last score followed
+        // those before; with one the last two may still run, and a barrier is
+        // waited for one phase at a time
+        if (C::kGroups == 1 && mine > 1 && !(ok = wait(&m.pvdone[0], pvph)))
             break;
         if (mine > 0 && !(ok = wait(&m.pvdone[C::kGroups == 2 ? group : 0], pvph ^ 1u)))
             break;
@@ -919,8 +1082,9 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
                 const long long at = ((long long)tree_row(p, w.b, base + node, false) * p.hkv + g) * D;
                 float s = 0.f;
                 for (int d = 0; d < D; ++d)
-                    s = fmaf(x2_to_float2<F16>(p.q[o_row * D + d]).x, tree_element<F16, KV>(p.k, at + d), s);
-                const float weight = exp2_approx((p.negate_q ? -s : s) * sl - lse2);
+                    s = fmaf(p.q_f16 ? f16x2_to_float2(p.q[o_row * D + d]).x : bf16x2_to_float2(p.q[o_row * D + d]).x,
+                             tree_element<F16, KV>(p.k, at + d), s);
+                const float weight = exp2_approx((p.negate_q ? -s : s) * p.scale_log2 - lse2);
                 for (int d = c0; d < c1; ++d) {
                     const float x = tree_element<F16, KV>(p.v, at + d);
                     if (fabsf(x) <= 3.4028235e38f)
@@ -949,12 +1113,12 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
 
 // ---------------------------------------------------------------- kernel
 
-template <int D, bool F16, int KV, bool TMA>
-__global__ void __launch_bounds__(TreeCfg<D, TMA>::kThreads, 1)
+template <int D, bool F16, int KV, int LOAD>
+__global__ void __launch_bounds__(TreeCfg<D, LOAD>::kThreads, 1)
 tree_split_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUtensorMap tmk,
                   const __grid_constant__ CUtensorMap tmv)
 {
-    using C = TreeCfg<D, TMA>;
+    using C = TreeCfg<D, LOAD>;
     extern __shared__ __align__(1024) uint8_t smem[];
     TreeMisc &m = *reinterpret_cast<TreeMisc *>(smem + p.off_misc);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -966,11 +1130,18 @@ tree_split_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ 
     if (warp == C::kMmaWarp)
         tmem_alloc(smem_addr(&m.tmem), C::kTmemCols);
     if (tid == 0) {
+        const int copies = LOAD == kTreeTma ? 1 : C::kCopyThreads;   // arrivals that fill a K or V slot
         for (int s = 0; s < kTreeMaxSlots; ++s) {
-            mbar_init(smem_addr(&m.kfull[s]), TMA ? 1 : 32 * C::kLoadWarps);
-            mbar_init(smem_addr(&m.vfull[s]), TMA ? 1 : 32 * C::kLoadWarps);
+            mbar_init(smem_addr(&m.kfull[s]), copies);
+            mbar_init(smem_addr(&m.vfull[s]), copies);
             mbar_init(smem_addr(&m.kempty[s]), 1);
             mbar_init(smem_addr(&m.vempty[s]), 1);
+        }
+        for (int s = 0; s < kTreeMaxRaw; ++s) {
+            mbar_init(smem_addr(&m.rkfull[s]), 1);
+            mbar_init(smem_addr(&m.rvfull[s]), 1);
+            mbar_init(smem_addr(&m.rkempty[s]), copies);
+            mbar_init(smem_addr(&m.rvempty[s]), copies);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_addr(&m.sfull[s]), 1);
@@ -983,7 +1154,7 @@ tree_split_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ 
         mbar_init_fence();
         m.abort = 0;
         m.b = p.batch;
-        if (TMA) {
+        if (LOAD != kTreeCopy) {
             tma_prefetch_desc(&tmk);
             tma_prefetch_desc(&tmv);
         }
@@ -1011,7 +1182,7 @@ tree_split_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ 
         m.scan[warp] = x;
     __syncthreads();
     long long before = x - mine, total = 0;
-    for (int k = 0; k <= C::kMmaWarp; ++k) {
+    for (int k = 0; k < C::kWarps; ++k) {
         before += k < warp ? m.scan[k] : 0;
         total += m.scan[k];
     }
@@ -1049,22 +1220,27 @@ tree_split_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ 
     tc_fence_after();
     const uint32_t tmem = m.tmem;
     const uint32_t q_smem = smem_addr(smem), k_ring = smem_addr(smem + p.off_k), v_ring = smem_addr(smem + p.off_v);
-    if (warp < C::kSoftWarps)
-        tree_softmax<D, F16, KV, TMA>(p, m, q_smem, v_ring, tmem);
-    else if (warp == C::kMmaWarp) {
-        if (lane == 0)
-            tree_mma<D, F16, TMA>(p, m, q_smem, k_ring, v_ring, tmem);
-        __syncwarp();
-    } else if constexpr (TMA) {
-        if (warp == C::kSoftWarps)
-            tree_load_tma<D, true>(p, m, &tmk, k_ring, p.k_slots, lane);
-        else
-            tree_load_tma<D, false>(p, m, &tmv, v_ring, p.v_slots, lane);
+    if (warp < C::kSoftWarps) {
+        if constexpr (C::kSplitRegs)
+            regs_more<C::kSoftRegs>();
+        tree_softmax<D, F16, KV, LOAD>(p, m, q_smem, v_ring, tmem);
     } else {
-        if (warp < C::kSoftWarps + C::kLoadWarps)
-            tree_load_threads<D, F16, KV, true>(p, m, k_ring, p.k_slots, tid - 32 * C::kSoftWarps);
-        else
-            tree_load_threads<D, F16, KV, false>(p, m, v_ring, p.v_slots, tid - 32 * (C::kSoftWarps + C::kLoadWarps));
+        if constexpr (C::kSplitRegs)
+            regs_fewer<C::kOtherRegs>();
+        const uint32_t raw_k = smem_addr(smem + p.off_raw), raw_v = raw_k + p.raw_slots * C::kRawBytes;
+        if (C::kCopyWarps > 0 && warp < C::kLoadWarp) {
+            if constexpr (LOAD != kTreeTma)
+                tree_copy<D, KV, LOAD>(p, m, k_ring, v_ring, raw_k, raw_v, tid - C::kSoftThreads);
+        } else if (warp == C::kMmaWarp) {
+            if (lane == 0)
+                tree_mma<D, F16, LOAD>(p, m, q_smem, k_ring, v_ring, tmem);
+            __syncwarp();
+        } else if (LOAD != kTreeCopy && warp == C::kLoadWarp)
+            tree_load_tma<D, LOAD, true>(p, m, &tmk, LOAD == kTreeConvert ? raw_k : k_ring,
+                                         LOAD == kTreeConvert ? p.raw_slots : p.k_slots, lane);
+        else if (LOAD != kTreeCopy && warp == C::kLoadWarp + 1)
+            tree_load_tma<D, LOAD, false>(p, m, &tmv, LOAD == kTreeConvert ? raw_v : v_ring,
+                                          LOAD == kTreeConvert ? p.raw_slots : p.v_slots, lane);
     }
     // every role returns, its waits being bounded
     tc_fence_before();
@@ -1074,7 +1250,7 @@ tree_split_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ 
         tmem_dealloc(tmem, C::kTmemCols);
 }
 
-template <int D, bool F16, int KV, bool TMA>
+template <int D, bool F16, int KV, int LOAD>
 cudaError_t launch_tree_variant(const TreeParams &p, const CUtensorMap &tmk, const CUtensorMap &tmv, const TreeLaunch &c)
 {
     // the shared-memory limit is raised once per device, so that later calls
@@ -1086,8 +1262,14 @@ cudaError_t launch_tree_variant(const TreeParams &p, const CUtensorMap &tmk, con
         return e;
     const unsigned long long bit = 1ull << (dev & 63);
     auto configure = [&]() -> cudaError_t {
-        const cudaError_t r = cudaFuncSetAttribute(tree_split_kernel<D, F16, KV, TMA>,
+        const cudaError_t r = cudaFuncSetAttribute(tree_split_kernel<D, F16, KV, LOAD>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, (int)c.smem_optin);
+        // the warps' register shares come out of the launch's: no launch with fewer
+        cudaFuncAttributes fa;
+        if (r == cudaSuccess && TreeCfg<D, LOAD>::kSplitRegs &&
+            (cudaFuncGetAttributes(&fa, tree_split_kernel<D, F16, KV, LOAD>) != cudaSuccess ||
+             fa.numRegs != TreeCfg<D, LOAD>::kLaunchRegs))
+            return cudaErrorInvalidConfiguration;
         if (r == cudaSuccess)
             configured.fetch_or(bit, std::memory_order_release);
         return r;
@@ -1099,17 +1281,17 @@ cudaError_t launch_tree_variant(const TreeParams &p, const CUtensorMap &tmk, con
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)c.grid);
-    cfg.blockDim = dim3(TreeCfg<D, TMA>::kThreads);
+    cfg.blockDim = dim3(TreeCfg<D, LOAD>::kThreads);
     cfg.dynamicSmemBytes = c.smem_bytes;
     cfg.stream = c.stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, tree_split_kernel<D, F16, KV, TMA>, p, tmk, tmv);
+    e = cudaLaunchKernelEx(&cfg, tree_split_kernel<D, F16, KV, LOAD>, p, tmk, tmv);
     if (e == cudaErrorInvalidValue) {
         (void)cudaGetLastError();
         if ((e = configure()) != cudaSuccess)
             return e;
-        e = cudaLaunchKernelEx(&cfg, tree_split_kernel<D, F16, KV, TMA>, p, tmk, tmv);
+        e = cudaLaunchKernelEx(&cfg, tree_split_kernel<D, F16, KV, LOAD>, p, tmk, tmv);
     }
     return e;
 }

@@ -66,10 +66,13 @@ def test_types(fd, dtype, kv, D, T):
 
 
 @pytest.mark.parametrize("T", [1, 20, 70])
-@pytest.mark.parametrize("ctas", [0, 1, 3, 40])
-def test_long_requests_split_many_ways(fd, T, ctas):
-    lens = [2500, 1, 700, 0, 1300]
-    c = make_tree_case(T, 5, T, 4, 1, 128, lens)
+@pytest.mark.parametrize("ctas", [0, 1, 3, 4, 7, 40])
+@pytest.mark.parametrize("D,kv,page", [(64, "same", 0), (128, "same", 0), (256, "same", 64), (128, "e4m3", 16), (256, "e5m2", 0),
+                                       (128, "same", 4)])
+def test_long_requests_split_many_ways(fd, T, ctas, D, kv, page):
+    """Few CTAs: long runs of tiles, several segments a CTA, every kind of partial; flushed accumulators (5000 positions)."""
+    lens = [700, 1, 5000, 0, 300]
+    c = make_tree_case(T, 5, T, 4, 1, D, lens, kv=kv, page=page)
     check_tree(*run(fd, c, 0.09, num_ctas=ctas), want(c, 0.09))
 
 
