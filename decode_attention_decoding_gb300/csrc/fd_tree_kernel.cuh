@@ -164,6 +164,14 @@ __device__ __forceinline__ void cp_async_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
 // A thread's register limit; all warps of a warpgroup execute it.
 template <int N>
 __device__ __forceinline__ void regs_more()
@@ -216,7 +224,7 @@ struct TreeCfg {
     // two groups of them need more than a block's even share, so the other
     // warps give some of theirs up (setmaxnreg): 216 x 256 + 72 x 128 =
     // 168 x 384, and 200 x 256 + 56 x 256 = 128 x 512 registers.
-    static constexpr bool kSplitRegs = kGroups == 2;
+    static constexpr bool kSplitRegs = false;
     static constexpr int kLaunchRegs = LOAD == kTreeTma ? 168 : 128;
     static constexpr int kSoftRegs = LOAD == kTreeTma ? 216 : 200;
     static constexpr int kOtherRegs = LOAD == kTreeTma ? 72 : 56;
@@ -578,7 +586,8 @@ __device__ __forceinline__ TreeUnits tree_units(const TreeParams &p, const TreeW
     return u;
 }
 
-// The MMA issuer: one thread.
+// The MMA issuer: one warp, whose lanes all run the loop (so that addresses and
+// descriptors stay in uniform registers) and whose elected lane issues.
 template <int D, bool F16, int LOAD>
 __device__ __forceinline__ void tree_mma(const TreeParams &p, TreeMisc &m, uint32_t q_smem, uint32_t k_ring,
                                          uint32_t v_ring, uint32_t tmem)
@@ -587,15 +596,22 @@ __device__ __forceinline__ void tree_mma(const TreeParams &p, TreeMisc &m, uint3
     constexpr uint32_t kIdescS = umma_idesc_f16(128, C::kN, F16, false);
     constexpr uint32_t kIdescO = umma_idesc_f16(128, D, F16, true);
     volatile int *abort_flag = &m.abort;
+    const bool leader = elect_one();
     auto wait = [&](uint64_t *bar, uint32_t parity) {
-        return mbar_wait_bounded(smem_addr(bar), parity, p.timeout_ns, abort_flag);
+        const bool r = mbar_wait_bounded(smem_addr(bar), parity, p.timeout_ns, abort_flag);
+        return __all_sync(0xffffffffu, r) != 0;
     };
+    const uint32_t sfull0 = smem_addr(m.sfull), pvdone0 = smem_addr(m.pvdone), kempty0 = smem_addr(m.kempty),
+                   vempty0 = smem_addr(m.vempty);
+    // descriptors: the high words are constants, an address enters the low word
+    const uint64_t desc_k = umma_desc_sw128(0), desc_v = umma_desc_sw128_n_major(0, C::kPartBytes);
     int ks = 0, vs = 0, segs = 0;   // the slot of the newest S's tile, and of the next P V's
     uint32_t kph = 0, vph = 0, pph = 0;
     TreeWalk<D> w;
     bool ok = true;
     for (w.start(p, m); ok && w.n > 0; w.next(p), ++segs) {
         const TreeUnits un = tree_units<D>(p, w);
+        const int active = un.active, ahead = un.ahead(), units = un.units;
         if (!(ok = wait(&m.qfull, segs & 1)))
             break;
         tc_fence_after();
@@ -604,24 +620,30 @@ __device__ __forceinline__ void tree_mma(const TreeParams &p, TreeMisc &m, uint3
                 return false;
             tc_fence_after();
             const int buf = un.buf(u);
-            const uint32_t a = q_smem + (un.active == 2 ? buf * C::kQBytes : 0), b = k_ring + ks * C::kSlotBytes;
+            const bool last = un.last_of_tile(u);
+            if (leader) {
+                const uint64_t a = desc_k + ((q_smem + (active == 2 ? buf * C::kQBytes : 0)) >> 4);
+                const uint64_t b = desc_k + ((k_ring + ks * C::kSlotBytes) >> 4);
+                const uint32_t d = tmem + buf * C::kN;
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-                umma_f16_ss(tmem + buf * C::kN, umma_desc_sw128(a + (k / 4) * (128 * 128) + (k % 4) * 32),
-                            umma_desc_sw128(b + (k / 4) * C::kPartBytes + (k % 4) * 32), kIdescS, k > 0);
-            umma_commit(smem_addr(&m.sfull[buf]));
-            if (un.last_of_tile(u)) {
-                umma_commit(smem_addr(&m.kempty[ks]));
-                if (++ks == p.k_slots) {
-                    ks = 0;
-                    kph ^= 1u;
-                }
+                for (int k = 0; k < D / 16; ++k)
+                    umma_f16_ss(d, a + (((k / 4) * (128 * 128) + (k % 4) * 32) >> 4),
+                                b + (((k / 4) * C::kPartBytes + (k % 4) * 32) >> 4), kIdescS, k > 0);
+                umma_commit(sfull0 + 8 * buf);
+                if (last)
+                    umma_commit(kempty0 + 8 * ks);
+            }
+            __syncwarp();
+            if (last && ++ks == p.k_slots) {
+                ks = 0;
+                kph ^= 1u;
             }
             return true;
         };
-        for (int u = 0; ok && u < un.ahead() && u < un.units; ++u)
+        for (int u = 0; ok && u < ahead && u < units; ++u)
             ok = scores(u);
-        for (int u = 0; ok && u < un.units; ++u) {
+        int nth = 0;   // of the accumulator: a unit that starts it, and one after a flush, overwrites
+        for (int u = 0; ok && u < units; ++u) {
             const int buf = un.buf(u), acc = C::kGroups == 1 ? 0 : buf;
             if (!(ok = wait(&m.pfull[buf], (pph >> buf) & 1u)))
                 break;
@@ -629,36 +651,38 @@ __device__ __forceinline__ void tree_mma(const TreeParams &p, TreeMisc &m, uint3
             if (un.first_of_tile(u) && !(ok = wait(&m.vfull[vs], vph)))
                 break;
             tc_fence_after();
-            // the first unit of an accumulator in this segment, and after a flush, overwrites it
-            const int nth = C::kGroups == 1 ? u : u / un.ahead();
-            const bool fresh = nth % C::kFlush == 0;
-            const uint32_t d = tmem + C::kTmemO + acc * D, b = v_ring + vs * C::kSlotBytes;
+            const bool last = un.last_of_tile(u);
+            if (leader) {
+                const uint32_t d = tmem + C::kTmemO + acc * D, a = tmem + buf * C::kN;
+                const uint64_t b = desc_v + ((v_ring + vs * C::kSlotBytes) >> 4);
 #pragma unroll
-            for (int k = 0; k < C::kN / 16; ++k) {
-                const uint32_t a = tmem + buf * C::kN + (k / 2) * 32 + (k % 2) * 8;
-                const uint64_t bd = umma_desc_sw128_n_major(b + k * 16 * 128, C::kPartBytes);
-                umma_f16_ts(d, a, bd, kIdescO, !(fresh && k == 0));
-                umma_f16_ts(d, a + 16, bd, kIdescO, true);
-            }
-            umma_commit(smem_addr(&m.pvdone[acc]));
-            if (un.last_of_tile(u)) {
-                umma_commit(smem_addr(&m.vempty[vs]));
-                if (++vs == p.v_slots) {
-                    vs = 0;
-                    vph ^= 1u;
+                for (int k = 0; k < C::kN / 16; ++k) {
+                    umma_f16_ts(d, a + (k / 2) * 32 + (k % 2) * 8, b + (k * 16 * 128 >> 4), kIdescO, k > 0 || nth > 0);
+                    umma_f16_ts(d, a + (k / 2) * 32 + (k % 2) * 8 + 16, b + (k * 16 * 128 >> 4), kIdescO, true);
                 }
+                umma_commit(pvdone0 + 8 * acc);
+                if (last)
+                    umma_commit(vempty0 + 8 * vs);
             }
-            if (u + un.ahead() < un.units)
-                ok = scores(u + un.ahead());
+            __syncwarp();
+            if (last && ++vs == p.v_slots) {
+                vs = 0;
+                vph ^= 1u;
+            }
+            if (C::kGroups == 1 || ahead == 1 || (u & 1))
+                nth = nth + 1 == C::kFlush ? 0 : nth + 1;
+            if (u + ahead < units)
+                ok = scores(u + ahead);
         }
     }
-    if (!ok) {
+    if (!ok && leader) {
         atomicOr(p.ws_err, kErrTimeout);
         *abort_flag = 1;
         // gave up: the MMAs in flight end before the tensor memory is freed
         umma_commit(smem_addr(&m.drain));
         mbar_wait_bounded(smem_addr(&m.drain), 0, p.timeout_ns, nullptr);
     }
+    __syncwarp();
 }
 
 // Copies this CTA's query rows of a segment into the swizzled operand: rows
@@ -882,30 +906,25 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
                 flushed_at = mx;
             }
             if (warp_live) {
-                // the row's scores stay in registers: one round trip to tensor
-                // memory a tile, and independent work to hide it behind
-                uint32_t s[C::kN / 32][32];
-                uint32_t bits[C::kN / 32];
-#pragma unroll
-                for (int c = 0; c < C::kN / 32; ++c)
-                    tmem_ld32(t_s + 32 * c, s[c]);
-                if (tail)
-#pragma unroll
-                    for (int c = 0; c < C::kN / 32; ++c)
-                        bits[c] = live ? tree_bits(p, mask_row, i, t0 + 32 * c - base, t) : 0u;
-#pragma unroll
-                for (int c = 0; c < C::kN / 32; ++c)
-                    tmem_wait_ld32(s[c]);
+                // Two passes over the row's scores, 32 columns at a time: the
+                // loops stay small enough for the instruction cache (unrolled
+                // over the tile, with the scores in registers, a third of the
+                // cycles went to fetching instructions).
                 float top[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < C::kN / 32; ++c) {
-                    if (tail)
+                    uint32_t s[32];
+                    tmem_ld32(t_s + 32 * c, s);
+                    tmem_wait_ld32(s);
+                    if (tail) {
+                        const uint32_t bits = live ? tree_bits(p, mask_row, i, t0 + 32 * c - base, t) : 0u;
 #pragma unroll
                         for (int k = 0; k < 32; ++k)
-                            s[c][k] = bits[c] >> k & 1u ? s[c][k] : 0xff800000u;   // -inf
+                            s[k] = bits >> k & 1u ? s[k] : 0xff800000u;   // -inf
+                    }
 #pragma unroll
                     for (int k = 0; k < 32; ++k)
-                        top[k & 3] = fmaxf(top[k & 3], __uint_as_float(s[c][k]));
+                        top[k & 3] = fmaxf(top[k & 3], __uint_as_float(s[k]));
                 }
                 const float tm = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                 const bool grow = tm > mx && (mx == kNegInf || (tm - mx) * sl > kSlack);
@@ -937,21 +956,32 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
                 const float2 sl2 = make_float2(sl, sl), off2 = make_float2(off, off), one2 = make_float2(1.f, 1.f),
                              neg2 = make_float2(-1.f, -1.f);
                 float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < C::kN / 32; ++c) {
+                    uint32_t s[32];
+                    tmem_ld32(t_s + 32 * c, s);
+                    tmem_wait_ld32(s);
+                    float2 x[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        x[k] = fma2(make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), sl2, off2);
+                        x[k].x = exp2_approx(x[k].x);
+                        x[k].y = exp2_approx(x[k].y);
+                    }
+                    if (tail) {
+                        const uint32_t bits = live ? tree_bits(p, mask_row, i, t0 + 32 * c - base, t) : 0u;
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            x[k].x = bits >> (2 * k) & 1u ? x[k].x : 0.f;
+                            x[k].y = bits >> (2 * k + 1) & 1u ? x[k].y : 0.f;
+                        }
+                    }
                     uint32_t out[32];
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
-                        float2 x = fma2(make_float2(__uint_as_float(s[c][2 * k]), __uint_as_float(s[c][2 * k + 1])), sl2, off2);
-                        x.x = exp2_approx(x.x);
-                        x.y = exp2_approx(x.y);
-                        if (tail) {   // also where the scale is 0 and -inf became NaN
-                            x.x = bits[c] >> (2 * k) & 1u ? x.x : 0.f;
-                            x.y = bits[c] >> (2 * k + 1) & 1u ? x.y : 0.f;
-                        }
-                        sum[k & 1] = fma2(x, one2, sum[k & 1]);
-                        out[k] = pack_x2<F16>(x.x, x.y);
-                        const float2 rest = fma2(x2_to_float2<F16>(out[k]), neg2, x);
+                        sum[k & 1] = fma2(x[k], one2, sum[k & 1]);
+                        out[k] = pack_x2<F16>(x[k].x, x[k].y);
+                        const float2 rest = fma2(x2_to_float2<F16>(out[k]), neg2, x[k]);
                         out[16 + k] = pack_x2<F16>(rest.x, rest.y);
                     }
                     tmem_st32(t_s + 32 * c, out);
@@ -1121,7 +1151,7 @@ tree_split_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ 
     using C = TreeCfg<D, LOAD>;
     extern __shared__ __align__(1024) uint8_t smem[];
     TreeMisc &m = *reinterpret_cast<TreeMisc *>(smem + p.off_misc);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     if (smem_addr(smem) & 1023u) {   // the swizzled layout and its descriptors count on it
         if (tid == 0)
             atomicOr(p.ws_err, kErrTimeout);
@@ -1231,11 +1261,9 @@ tree_split_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ 
         if (C::kCopyWarps > 0 && warp < C::kLoadWarp) {
             if constexpr (LOAD != kTreeTma)
                 tree_copy<D, KV, LOAD>(p, m, k_ring, v_ring, raw_k, raw_v, tid - C::kSoftThreads);
-        } else if (warp == C::kMmaWarp) {
-            if (lane == 0)
-                tree_mma<D, F16, LOAD>(p, m, q_smem, k_ring, v_ring, tmem);
-            __syncwarp();
-        } else if (LOAD != kTreeCopy && warp == C::kLoadWarp)
+        } else if (warp == C::kMmaWarp)
+            tree_mma<D, F16, LOAD>(p, m, q_smem, k_ring, v_ring, tmem);
+        else if (LOAD != kTreeCopy && warp == C::kLoadWarp)
             tree_load_tma<D, LOAD, true>(p, m, &tmk, LOAD == kTreeConvert ? raw_k : k_ring,
                                          LOAD == kTreeConvert ? p.raw_slots : p.k_slots, lane);
         else if (LOAD != kTreeCopy && warp == C::kLoadWarp + 1)
