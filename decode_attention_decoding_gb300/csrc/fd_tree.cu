@@ -117,6 +117,8 @@ fd_status launch(TreeParams p, int head_dim, float scale, const fd_options *opts
     p.q_f16 = f16;
     p.negate_q = scale < 0.f;
     p.scale_log2 = (p.negate_q ? -scale : scale) * 1.4426950408889634f;
+    if (p.scale_log2 < kTreeLeastScale)
+        p.scale_log2 = kTreeLeastScale;
     p.v_scale = fp8 && opts->v_scale != 0.f ? opts->v_scale : 1.f;
     p.words = (p.tree_len + 63) / 64;
     p.group = p.hq / p.hkv;

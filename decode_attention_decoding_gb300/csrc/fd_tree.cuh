@@ -33,6 +33,10 @@ constexpr int kTreeMaxCtas = 256;    // split CTAs (sizes the workspace)
 // Cost of a segment start in tiles of the split (below).
 constexpr int kTreeSegCost = 1;
 
+// A scale of 0 becomes this one, so that a hidden score (-inf) keeps its
+// weight of 0; scores below 1e30 are still 0.
+constexpr float kTreeLeastScale = 1e-37f;
+
 // Units of 128 positions that a tensor-core accumulator sums before it is
 // flushed (fd_tree_kernel.cuh).
 constexpr int kTreeFlush = 16;
@@ -63,7 +67,7 @@ struct TreeParams {
     int k_slots, v_slots;          // K and V tiles in shared memory
     int raw_slots;                 // tiles of FP8 codes, of K and of V each
     uint32_t off_k, off_v, off_raw, off_misc;
-    float scale_log2, v_scale;     // scale_log2 >= 0 (a negative scale's sign goes to q)
+    float scale_log2, v_scale;     // scale_log2 > 0 (a negative scale's sign goes to q)
     int q_f16, negate_q, starve;
 };
 

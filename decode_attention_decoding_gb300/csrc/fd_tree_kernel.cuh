@@ -219,6 +219,7 @@ struct TreeCfg {
     static constexpr int kSlotBytes = kParts * kPartBytes;
     static constexpr int kRawBytes = kN * D;                      // of a tile of FP8 codes
     static constexpr int kQBytes = 128 * D * 2;                   // 128 query rows
+    static constexpr int kHalves = kN / 64;                       // of a tile's weights
     static constexpr int kFlush = kTreeFlush * 128 / kN;          // units between flushes
     // Registers.  A softmax thread holds a row's 128 scores and some 70 more;
     // two groups of them need more than a block's even share, so the other
@@ -238,7 +239,7 @@ struct TreeCfg {
 struct TreeMisc {
     uint64_t kfull[kTreeMaxSlots], kempty[kTreeMaxSlots], vfull[kTreeMaxSlots], vempty[kTreeMaxSlots];
     uint64_t rkfull[kTreeMaxRaw], rkempty[kTreeMaxRaw], rvfull[kTreeMaxRaw], rvempty[kTreeMaxRaw];
-    uint64_t sfull[2], pfull[2], pvdone[2], qfull, pair, drain;
+    uint64_t sfull[2], pfull[2][2], pvdone[2], qfull, pair, drain;
     long long scan[18];
     long long segpos, x1;
     int b, seg, j, abort;
@@ -645,26 +646,35 @@ __device__ __forceinline__ void tree_mma(const TreeParams &p, TreeMisc &m, uint3
         int nth = 0;   // of the accumulator: a unit that starts it, and one after a flush, overwrites
         for (int u = 0; ok && u < units; ++u) {
             const int buf = un.buf(u), acc = C::kGroups == 1 ? 0 : buf;
-            if (!(ok = wait(&m.pfull[buf], (pph >> buf) & 1u)))
+            const bool last = un.last_of_tile(u);
+            const uint32_t d = tmem + C::kTmemO + acc * D, a = tmem + buf * C::kN;
+            const uint64_t b = desc_v + ((v_ring + vs * C::kSlotBytes) >> 4);
+#pragma unroll 1
+            for (int half = 0; ok && half < C::kHalves; ++half) {
+                if (!(ok = wait(&m.pfull[buf][half], (pph >> buf) & 1u)))
+                    break;
+                if (half == 0 && un.first_of_tile(u) && !(ok = wait(&m.vfull[vs], vph)))
+                    break;
+                tc_fence_after();
+                if (leader) {
+                    const uint32_t ah = a + 64 * half;
+                    const uint64_t bh = b + (uint32_t)(half * 64 * 128 >> 4);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        umma_f16_ts(d, ah + (k / 2) * 32 + (k % 2) * 8, bh + (k * 16 * 128 >> 4), kIdescO, half > 0 || k > 0 || nth > 0);
+                        umma_f16_ts(d, ah + (k / 2) * 32 + (k % 2) * 8 + 16, bh + (k * 16 * 128 >> 4), kIdescO, true);
+                    }
+                    if (half == C::kHalves - 1) {
+                        umma_commit(pvdone0 + 8 * acc);
+                        if (last)
+                            umma_commit(vempty0 + 8 * vs);
+                    }
+                }
+                __syncwarp();
+            }
+            if (!ok)
                 break;
             pph ^= 1u << buf;
-            if (un.first_of_tile(u) && !(ok = wait(&m.vfull[vs], vph)))
-                break;
-            tc_fence_after();
-            const bool last = un.last_of_tile(u);
-            if (leader) {
-                const uint32_t d = tmem + C::kTmemO + acc * D, a = tmem + buf * C::kN;
-                const uint64_t b = desc_v + ((v_ring + vs * C::kSlotBytes) >> 4);
-#pragma unroll
-                for (int k = 0; k < C::kN / 16; ++k) {
-                    umma_f16_ts(d, a + (k / 2) * 32 + (k % 2) * 8, b + (k * 16 * 128 >> 4), kIdescO, k > 0 || nth > 0);
-                    umma_f16_ts(d, a + (k / 2) * 32 + (k % 2) * 8 + 16, b + (k * 16 * 128 >> 4), kIdescO, true);
-                }
-                umma_commit(pvdone0 + 8 * acc);
-                if (last)
-                    umma_commit(vempty0 + 8 * vs);
-            }
-            __syncwarp();
             if (last && ++vs == p.v_slots) {
                 vs = 0;
                 vph ^= 1u;
@@ -880,7 +890,7 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
             if (!(ok = wait(&m.qfull, qph)))
                 break;
             qph ^= 1u;
-            sl = p.scale_log2 * m.ml[group][tid].x;
+            sl = fmaxf(p.scale_log2 * m.ml[group][tid].x, kTreeLeastScale);
         }
         float mx = kNegInf, l = 0.f;
         int mine = 0;                                // units of this group so far in the segment
@@ -905,26 +915,44 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
                 flush_sums(mine == C::kFlush, mx);
                 flushed_at = mx;
             }
+            float mx_off = 0.f;
             if (warp_live) {
-                // Two passes over the row's scores, 32 columns at a time: the
-                // loops stay small enough for the instruction cache (unrolled
-                // over the tile, with the scores in registers, a third of the
-                // cycles went to fetching instructions).
+                // Two passes over the row's scores, 32 columns at a time, the next
+                // ones on their way: the maximum, then the weights.  The loops
+                // stay small for the instruction cache (with a tile unrolled and
+                // its scores in registers, a third of the cycles went to
+                // fetching instructions).  What the row does not see becomes
+                // -inf in tensor memory, so the second pass needs no mask.
                 float top[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+                auto upper = [&](const uint32_t (&s)[32]) {
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2)   // a three-way maximum each
+                        top[k / 2 & 3] = fmaxf(fmaxf(top[k / 2 & 3], __uint_as_float(s[k])), __uint_as_float(s[k + 1]));
+                };
+                if (tail) {
 #pragma unroll 1
-                for (int c = 0; c < C::kN / 32; ++c) {
-                    uint32_t s[32];
-                    tmem_ld32(t_s + 32 * c, s);
-                    tmem_wait_ld32(s);
-                    if (tail) {
+                    for (int c = 0; c < C::kN / 32; ++c) {
+                        uint32_t s[32];
+                        tmem_ld32(t_s + 32 * c, s);
                         const uint32_t bits = live ? tree_bits(p, mask_row, i, t0 + 32 * c - base, t) : 0u;
+                        tmem_wait_ld32(s);
 #pragma unroll
                         for (int k = 0; k < 32; ++k)
-                            s[k] = bits >> k & 1u ? s[k] : 0xff800000u;   // -inf
+                            s[k] = bits >> k & 1u ? s[k] : 0xff800000u;
+                        tmem_st32(t_s + 32 * c, s);
+                        upper(s);
                     }
+                    tmem_wait_st();
+                } else {
+                    uint32_t s[2][32];
+                    tmem_ld32(t_s, s[0]);
 #pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        top[k & 3] = fmaxf(top[k & 3], __uint_as_float(s[k]));
+                    for (int c = 0; c < C::kN / 32; ++c) {
+                        tmem_wait_ld32(s[c & 1]);
+                        if (c + 1 < C::kN / 32)
+                            tmem_ld32(t_s + 32 * (c + 1), s[c + 1 & 1]);
+                        upper(s[c & 1]);
+                    }
                 }
                 const float tm = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                 const bool grow = tm > mx && (mx == kNegInf || (tm - mx) * sl > kSlack);
@@ -952,55 +980,54 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
                         }
                     }
                 }
-                const float off = kShift - (mx == kNegInf ? 0.f : mx * sl);
-                const float2 sl2 = make_float2(sl, sl), off2 = make_float2(off, off), one2 = make_float2(1.f, 1.f),
-                             neg2 = make_float2(-1.f, -1.f);
-                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll 1
-                for (int c = 0; c < C::kN / 32; ++c) {
-                    uint32_t s[32];
-                    tmem_ld32(t_s + 32 * c, s);
-                    tmem_wait_ld32(s);
-                    float2 x[16];
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        x[k] = fma2(make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), sl2, off2);
-                        x[k].x = exp2_approx(x[k].x);
-                        x[k].y = exp2_approx(x[k].y);
-                    }
-                    if (tail) {
-                        const uint32_t bits = live ? tree_bits(p, mask_row, i, t0 + 32 * c - base, t) : 0u;
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            x[k].x = bits >> (2 * k) & 1u ? x[k].x : 0.f;
-                            x[k].y = bits >> (2 * k + 1) & 1u ? x[k].y : 0.f;
-                        }
-                    }
-                    uint32_t out[32];
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        sum[k & 1] = fma2(x[k], one2, sum[k & 1]);
-                        out[k] = pack_x2<F16>(x[k].x, x[k].y);
-                        const float2 rest = fma2(x2_to_float2<F16>(out[k]), neg2, x[k]);
-                        out[16 + k] = pack_x2<F16>(rest.x, rest.y);
-                    }
-                    tmem_st32(t_s + 32 * c, out);
-                }
-                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-                tmem_wait_st();
+                mx_off = kShift - (mx == kNegInf ? 0.f : mx * sl);
             }
-            if (tail) {
+            if (tail && (!own_rows || group == 0)) {
                 // this group's tile (with rows of their own: the first group cleans for both)
                 const int vs = (vcount + tile) % p.v_slots;
-                if (!own_rows || group == 0) {
-                    if (!(ok = wait(&m.vfull[vs], ((vcount + tile) / p.v_slots) & 1)))
-                        break;
-                    tree_clean_v<D, F16, LOAD>(v_ring + vs * C::kSlotBytes, max(0, base - t0), L - t0, t0 - base, m.bad, tid);
-                    fence_async_shared();
-                }
+                if (!(ok = wait(&m.vfull[vs], ((vcount + tile) / p.v_slots) & 1)))
+                    break;
+                tree_clean_v<D, F16, LOAD>(v_ring + vs * C::kSlotBytes, max(0, base - t0), L - t0, t0 - base, m.bad, tid);
+                fence_async_shared();
             }
-            tc_fence_before();
-            mbar_arrive(smem_addr(&m.pfull[buf]));
+            // The weights, 64 positions at a time: the MMAs of the first half
+            // run beside the exponentials of the second.
+            const float2 sl2 = make_float2(sl, sl), off2 = make_float2(mx_off, mx_off), one2 = make_float2(1.f, 1.f),
+                         neg2 = make_float2(-1.f, -1.f);
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            auto weights = [&](int c, uint32_t (&s)[32]) {
+                float2 x[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    x[k] = fma2(make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), sl2, off2);
+                    x[k].x = exp2_approx(x[k].x);
+                    x[k].y = exp2_approx(x[k].y);
+                }
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    sum[k & 1] = fma2(x[k], one2, sum[k & 1]);
+                    s[k] = pack_x2<F16>(x[k].x, x[k].y);
+                    const float2 rest = fma2(x2_to_float2<F16>(s[k]), neg2, x[k]);
+                    s[16 + k] = pack_x2<F16>(rest.x, rest.y);
+                }
+                tmem_st32(t_s + 32 * c, s);
+            };
+#pragma unroll 1
+            for (int half = 0; half < C::kHalves; ++half) {
+                if (warp_live) {
+                    uint32_t s0[32], s1[32];
+                    tmem_ld32(t_s + 64 * half, s0);
+                    tmem_wait_ld32(s0);
+                    tmem_ld32(t_s + 64 * half + 32, s1);
+                    weights(2 * half, s0);
+                    tmem_wait_ld32(s1);
+                    weights(2 * half + 1, s1);
+                    tmem_wait_st();
+                }
+                tc_fence_before();
+                mbar_arrive(smem_addr(&m.pfull[buf][half]));
+            }
+            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             pvph ^= 1u;
         }
         if (!ok)
@@ -1175,7 +1202,8 @@ tree_split_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ 
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_addr(&m.sfull[s]), 1);
-            mbar_init(smem_addr(&m.pfull[s]), 128);
+            mbar_init(smem_addr(&m.pfull[s][0]), 128);
+            mbar_init(smem_addr(&m.pfull[s][1]), 128);
             mbar_init(smem_addr(&m.pvdone[s]), 1);
         }
         mbar_init(smem_addr(&m.qfull), C::kSoftThreads);
