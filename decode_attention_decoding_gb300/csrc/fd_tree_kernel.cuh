@@ -164,6 +164,11 @@ __device__ __forceinline__ void cp_async_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+__device__ __forceinline__ void red_add_v4(float *at, float4 x)
+{
+    asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(at), "f"(x.x), "f"(x.y), "f"(x.z), "f"(x.w) : "memory");
+}
+
 // True in one lane of the (converged) warp.
 __device__ __forceinline__ bool elect_one()
 {
@@ -836,31 +841,43 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
     // this thread's sums of the units before the last flush, relative to the maximum then
     float *sums = p.ws_sums + ((long long)(blockIdx.x * C::kGroups + group) * (D / 4) * p.sum_rows + tid) * 4;
     const bool has_sums = tid < p.sum_rows;
-    float flushed_at = kNegInf;
-    // sums = sums * 2^((their maximum - mx) scale) + the accumulator, `fresh`: = the accumulator
+    float ref = 0.f;   // the maximum that the sums are relative to: the one at the segment's first flush
+    // sums += accumulator * 2^((now - ref) scale), by reductions that nothing waits
+    // for: the rows are this thread's own, so their order is the program's
     auto flush_sums = [&](bool fresh, float now) {
-        const float corr = fresh || flushed_at == kNegInf ? 0.f : exp2_approx((flushed_at - now) * sl);
-#pragma unroll
+        if (fresh)
+            ref = now == kNegInf ? 0.f : now;
+        float up = now == kNegInf ? 0.f : (now - ref) * sl;
+        if (!fresh && __any_sync(0xffffffffu, up > 60.f)) {   // rare: move the reference
+            const float corr = exp2_approx(-up);
+            if (has_sums)
+#pragma unroll 1
+                for (int c = 0; c < D / 4; ++c) {
+                    float4 *at = reinterpret_cast<float4 *>(sums + (long long)c * p.sum_rows * 4);
+                    const float4 x = __ldcg(at);
+                    *at = make_float4(x.x * corr, x.y * corr, x.z * corr, x.w * corr);
+                }
+            ref = now == kNegInf ? ref : now;
+            up = 0.f;
+        }
+        const float scale = exp2_approx(up);
+#pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
             uint32_t o[32];
             tmem_ld32(t_o + 32 * c, o);
-            float4 old[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                old[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (!fresh && has_sums)
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    old[k] = *reinterpret_cast<const float4 *>(sums + (long long)(8 * c + k) * p.sum_rows * 4);
             tmem_wait_ld32(o);
-            if (has_sums)
+            if (!has_sums)
+                continue;
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    *reinterpret_cast<float4 *>(sums + (long long)(8 * c + k) * p.sum_rows * 4) =
-                        make_float4(fmaf(old[k].x, corr, __uint_as_float(o[4 * k])),
-                                    fmaf(old[k].y, corr, __uint_as_float(o[4 * k + 1])),
-                                    fmaf(old[k].z, corr, __uint_as_float(o[4 * k + 2])),
-                                    fmaf(old[k].w, corr, __uint_as_float(o[4 * k + 3])));
+            for (int k = 0; k < 8; ++k) {
+                float *at = sums + (long long)(8 * c + k) * p.sum_rows * 4;
+                const float4 x = make_float4(__uint_as_float(o[4 * k]) * scale, __uint_as_float(o[4 * k + 1]) * scale,
+                                             __uint_as_float(o[4 * k + 2]) * scale, __uint_as_float(o[4 * k + 3]) * scale);
+                if (fresh)
+                    *reinterpret_cast<float4 *>(at) = x;
+                else
+                    red_add_v4(at, x);
+            }
         }
         tc_fence_before();
     };
@@ -913,7 +930,6 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
             if (flush && warp_live) {
                 tc_fence_after();
                 flush_sums(mine == C::kFlush, mx);
-                flushed_at = mx;
             }
             float mx_off = 0.f;
             if (warp_live) {
@@ -1044,7 +1060,11 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
 
         // the segment's result: O / l and the log-sum-exp (base 2), final or partial
         if (mine > C::kFlush && warp_live) {
-            flush_sums(false, mx);   // the segment's whole sum, relative to the final maximum
+            flush_sums(false, mx);   // the segment's whole sum, relative to ref
+            if (mx != kNegInf) {
+                l *= exp2_approx((mx - ref) * sl);
+                mx = ref;
+            }
             __threadfence_block();   // with shared rows the other group reads half of it
         }
         if (!live) {
@@ -1090,7 +1110,7 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
                         const float *src = p.ws_sums + (((long long)(blockIdx.x * C::kGroups + of) * (D / 4) + c / 4) * p.sum_rows + tid) * 4;
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
-                            const float4 o = *reinterpret_cast<const float4 *>(src + (long long)k * p.sum_rows * 4);
+                            const float4 o = __ldcg(reinterpret_cast<const float4 *>(src + (long long)k * p.sum_rows * 4));
                             v[4 * k] = fmaf(o.x, weight, v[4 * k]);
                             v[4 * k + 1] = fmaf(o.y, weight, v[4 * k + 1]);
                             v[4 * k + 2] = fmaf(o.z, weight, v[4 * k + 2]);
