@@ -226,14 +226,10 @@ struct TreeCfg {
     static constexpr int kQBytes = 128 * D * 2;                   // 128 query rows
     static constexpr int kHalves = kN / 64;                       // of a tile's weights
     static constexpr int kFlush = kTreeFlush * 128 / kN;          // units between flushes
-    // Registers.  A softmax thread holds a row's 128 scores and some 70 more;
-    // two groups of them need more than a block's even share, so the other
-    // warps give some of theirs up (setmaxnreg): 216 x 256 + 72 x 128 =
-    // 168 x 384, and 200 x 256 + 56 x 256 = 128 x 512 registers.
-    static constexpr bool kSplitRegs = false;
-    static constexpr int kLaunchRegs = LOAD == kTreeTma ? 168 : 128;
-    static constexpr int kSoftRegs = LOAD == kTreeTma ? 216 : 200;
-    static constexpr int kOtherRegs = LOAD == kTreeTma ? 72 : 56;
+    // Registers.  A softmax thread wants some 160, more than an even share of
+    // a block with the copying warps, which give some of theirs up (setmaxnreg).
+    static constexpr bool kSplitRegs = kGroups == 2 && LOAD != kTreeTma;
+    static constexpr int kLaunchRegs = 128, kSoftRegs = 160, kOtherRegs = 96;
     static_assert(!kSplitRegs || kSoftRegs * kSoftThreads + kOtherRegs * (kThreads - kSoftThreads) <= kLaunchRegs * kThreads,
                   "the shares come out of what the block was launched with");
     // tensor memory: two score buffers, then the accumulators
@@ -244,14 +240,14 @@ struct TreeCfg {
 struct TreeMisc {
     uint64_t kfull[kTreeMaxSlots], kempty[kTreeMaxSlots], vfull[kTreeMaxSlots], vempty[kTreeMaxSlots];
     uint64_t rkfull[kTreeMaxRaw], rkempty[kTreeMaxRaw], rvfull[kTreeMaxRaw], rvempty[kTreeMaxRaw];
-    uint64_t sfull[2], pfull[2][2], pvdone[2], qfull, pair, drain;
+    uint64_t sfull[2], pfull[2][2], pvdone[2], qfull, ofree, pair, drain;
     long long scan[18];
     long long segpos, x1;
     int b, seg, j, abort;
     uint32_t tmem;
-    unsigned int bad[kMaxTree / 32];   // nodes whose V row is not finite
-    // a softmax thread's running maximum and sum at the end of a segment; at its
-    // start (FP8) the power of two that the row was divided by
+    unsigned int bad[2][kMaxTree / 32];   // nodes whose V row is not finite, of even and odd segments
+    int8_t power[2][128];                 // FP8: exponents of the powers of two that the rows were divided by
+    // a softmax thread's maximum and sum at the end of a segment, when both groups have some of it
     float2 ml[2][128];
 };
 
@@ -430,45 +426,67 @@ __device__ __forceinline__ void tree_convert(uint32_t raw, uint32_t tile, int ti
     using C = TreeCfg<D, kTreeConvert>;
     constexpr int kRowUnits = D / 16, kUnits = C::kN * kRowUnits;
     static_assert(kUnits % C::kCopyThreads == 0, "whole rounds");
-#pragma unroll 4
-    for (int e = tid; e < kUnits; e += C::kCopyThreads) {
-        const int quad = e / 8, in = e & 7;                     // 8 lanes: units 4 n .. 4 n + 3 of rows 2 k, 2 k + 1
-        const int row = 2 * (quad / (kRowUnits / 4)) + (in >> 2), unit = 4 * (quad % (kRowUnits / 4)) + (in & 3);
-        const uint4 x = lds128(raw + row * D + unit * 16);
-        const uint32_t at = tile + (unit / 4) * C::kPartBytes + row * 128;
-        const int c = 2 * (unit & 3);
-        sts128(at + ((c ^ (row & 7)) << 4), make_uint4(fp8x2_to_f16x2<KV>(lo16(x.x)), fp8x2_to_f16x2<KV>(hi16(x.x)),
-                                                       fp8x2_to_f16x2<KV>(lo16(x.y)), fp8x2_to_f16x2<KV>(hi16(x.y))));
-        sts128(at + (((c + 1) ^ (row & 7)) << 4),
-               make_uint4(fp8x2_to_f16x2<KV>(lo16(x.z)), fp8x2_to_f16x2<KV>(hi16(x.z)), fp8x2_to_f16x2<KV>(lo16(x.w)),
-                          fp8x2_to_f16x2<KV>(hi16(x.w))));
+    constexpr int kRounds = kUnits / C::kCopyThreads, kBatch = 4;
+    static_assert(kRounds % kBatch == 0, "whole batches");
+    // 8 lanes: units 4 n .. 4 n + 3 of rows 2 k, 2 k + 1
+    auto row_of = [](int e) { return 2 * (e / 8 / (kRowUnits / 4)) + ((e & 7) >> 2); };
+    auto unit_of = [](int e) { return 4 * (e / 8 % (kRowUnits / 4)) + (e & 3); };
+#pragma unroll 1
+    for (int n = 0; n < kRounds; n += kBatch) {
+        uint4 x[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int e = tid + (n + k) * C::kCopyThreads;
+            x[k] = lds128(raw + row_of(e) * D + unit_of(e) * 16);
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int e = tid + (n + k) * C::kCopyThreads, row = row_of(e), unit = unit_of(e);
+            const uint32_t at = tile + (unit / 4) * C::kPartBytes + row * 128;
+            const int c = 2 * (unit & 3);
+            const uint4 lo = make_uint4(fp8x2_to_f16x2<KV>(lo16(x[k].x)), fp8x2_to_f16x2<KV>(hi16(x[k].x)),
+                                        fp8x2_to_f16x2<KV>(lo16(x[k].y)), fp8x2_to_f16x2<KV>(hi16(x[k].y)));
+            const uint4 hi = make_uint4(fp8x2_to_f16x2<KV>(lo16(x[k].z)), fp8x2_to_f16x2<KV>(hi16(x[k].z)),
+                                        fp8x2_to_f16x2<KV>(lo16(x[k].w)), fp8x2_to_f16x2<KV>(hi16(x[k].w)));
+            sts128(at + ((c ^ (row & 7)) << 4), lo);
+            sts128(at + (((c + 1) ^ (row & 7)) << 4), hi);
+        }
     }
 }
 
 // Small pages: one tile's rows by 128 threads, converted on the way if they
 // are FP8 codes; 16-bit rows by asynchronous copies, complete after
-// cp_async_wait.  Rows from `valid` on are left as they are.
+// cp_async_wait.  A warp takes a quarter of the tile's rows; `rows` holds the
+// pool row of its row `lane`.  Rows from `valid` on are left as they are.
 template <int D, int KV>
-__device__ __forceinline__ void tree_copy_rows(const TreeParams &p, const uint8_t *cache, const TreeWalk<D> &w, int t0,
-                                               int valid, uint32_t tile, int tid, bool report)
+__device__ __forceinline__ void tree_copy_rows(const TreeParams &p, const uint8_t *cache, int g, bool once, int rows,
+                                               int valid, uint32_t tile, int warp, int lane)
 {
     using C = TreeCfg<D, kTreeCopy>;
-    const int g = w.seg / w.s.groups;
+    constexpr int kRows = C::kN / C::kCopyWarps, kPieces = kv_is_fp8(KV) ? D / 16 : D / 8, kStep = 32 / kPieces;
+    static_assert(kRows <= 32 && 32 % kPieces == 0, "a lane a row");
+    const int piece = lane % kPieces;
+    const uint8_t *base = cache + (size_t)g * D * (kv_is_fp8(KV) ? 1 : 2) + piece * 16;
+    const size_t row_bytes = (size_t)p.hkv * D * (kv_is_fp8(KV) ? 1 : 2);
     if constexpr (kv_is_fp8(KV)) {
-        constexpr int kRowUnits = D / 16, kStep = C::kCopyThreads / kRowUnits, kBatch = 4;
-        const int unit = tid % kRowUnits, c = 2 * (unit & 3);
-        for (int r0 = tid / kRowUnits; r0 < valid; r0 += kStep * kBatch) {
+        constexpr int kBatch = 4;
+        const int c = 2 * (piece & 3);
+#pragma unroll 1
+        for (int r0 = 0; r0 < kRows; r0 += kStep * kBatch) {
             uint4 x[kBatch];
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k)
-                if (r0 + k * kStep < valid)
-                    x[k] = ldg128_nc(cache + ((long long)tree_row(p, w.b, t0 + r0 + k * kStep, report && unit == 0) * p.hkv + g) * D + unit * 16);
+            for (int k = 0; k < kBatch; ++k) {
+                const int r = r0 + k * kStep + lane / kPieces, from = __shfl_sync(0xffffffffu, rows, r & 31);
+                x[k] = make_uint4(0, 0, 0, 0);
+                if (r < kRows && warp * kRows + r < valid)
+                    x[k] = ldg128_nc(base + (size_t)from * row_bytes);
+            }
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
-                const int row = r0 + k * kStep;
-                if (row >= valid)
-                    break;
-                const uint32_t at = tile + (unit / 4) * C::kPartBytes + row * 128;
+                const int r = r0 + k * kStep + lane / kPieces, row = warp * kRows + r;
+                if (r >= kRows || row >= valid)
+                    continue;
+                const uint32_t at = tile + (piece / 4) * C::kPartBytes + row * 128;
                 sts128(at + ((c ^ (row & 7)) << 4),
                        make_uint4(fp8x2_to_f16x2<KV>(lo16(x[k].x)), fp8x2_to_f16x2<KV>(hi16(x[k].x)),
                                   fp8x2_to_f16x2<KV>(lo16(x[k].y)), fp8x2_to_f16x2<KV>(hi16(x[k].y))));
@@ -478,12 +496,13 @@ __device__ __forceinline__ void tree_copy_rows(const TreeParams &p, const uint8_
             }
         }
     } else {
-        constexpr int kChunks = D / 8, kStep = C::kCopyThreads / kChunks;
-        const int chunk = tid % kChunks;
-        const uint64_t policy = w.s.groups > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
-        for (int row = tid / kChunks; row < valid; row += kStep) {
-            const long long at = ((long long)tree_row(p, w.b, t0 + row, report && chunk == 0) * p.hkv + g) * D + chunk * 8;
-            cp_async_16(tile + (chunk / 8) * C::kPartBytes + row * 128 + (((chunk & 7) ^ (row & 7)) << 4), cache + 2 * at, policy);
+        const uint64_t policy = once ? l2_policy_evict_first() : l2_policy_evict_normal();
+#pragma unroll 4
+        for (int r0 = 0; r0 < kRows; r0 += kStep) {
+            const int r = r0 + lane / kPieces, from = __shfl_sync(0xffffffffu, rows, r & 31), row = warp * kRows + r;
+            if (row < valid)
+                cp_async_16(tile + (piece / 8) * C::kPartBytes + row * 128 + (((piece & 7) ^ (row & 7)) << 4),
+                            base + (size_t)from * row_bytes, policy);
         }
     }
 }
@@ -513,6 +532,12 @@ __device__ __forceinline__ void tree_copy(const TreeParams &p, TreeMisc &m, uint
     for (w.start(p, m); ok && w.n > 0; w.next(p))
         for (int j = w.j0; ok && j < w.j0 + w.n; ++j) {
             const int t0 = j * C::kN, valid = min(C::kN, w.r.L - t0);
+            [[maybe_unused]] int rows = 0;   // small pages: the pool row of this warp's row `lane`
+            if constexpr (LOAD == kTreeCopy) {
+                const int r = (tid >> 5) * (C::kN / C::kCopyWarps) + (tid & 31);
+                if ((tid & 31) < C::kN / C::kCopyWarps && r < valid)
+                    rows = tree_row(p, w.b, t0 + r, true);
+            }
 #pragma unroll 1
             for (int half = 0; ok && half < 2; ++half) {
                 TreeRing &r = half ? rv : rk;
@@ -531,7 +556,8 @@ __device__ __forceinline__ void tree_copy(const TreeParams &p, TreeMisc &m, uint
                     tree_convert<D, KV>((half ? raw_v : raw_k) + rr.slot * C::kRawBytes, tile, tid);
                     mbar_arrive(smem_addr(half ? &m.rvempty[rr.slot] : &m.rkempty[rr.slot]));
                 } else
-                    tree_copy_rows<D, KV>(p, half ? p.v : p.k, w, t0, valid, tile, tid, !half);
+                    tree_copy_rows<D, KV>(p, half ? p.v : p.k, w.seg / w.s.groups, w.s.groups == 1, rows, valid, tile,
+                                          tid >> 5, tid & 31);
                 // the test hook leaves out an arrival, so that the first tile never becomes full
                 const bool starve = LOAD == kTreeCopy && p.starve && first && blockIdx.x == 0 && tid == 0;
                 first = false;
@@ -660,6 +686,9 @@ __device__ __forceinline__ void tree_mma(const TreeParams &p, TreeMisc &m, uint3
                     break;
                 if (half == 0 && un.first_of_tile(u) && !(ok = wait(&m.vfull[vs], vph)))
                     break;
+                // the accumulators of the last segment have been read
+                if (half == 0 && u == 0 && segs > 0 && !(ok = wait(&m.ofree, (segs - 1) & 1)))
+                    break;
                 tc_fence_after();
                 if (leader) {
                     const uint32_t ah = a + 64 * half;
@@ -700,36 +729,41 @@ __device__ __forceinline__ void tree_mma(const TreeParams &p, TreeMisc &m, uint3
     __syncwarp();
 }
 
-// Copies this CTA's query rows of a segment into the swizzled operand: rows
-// [first_row, first_row + 128) by THREADS threads, all loads in flight
-// together.  Rows without a node are zero.  For FP8 caches (TO_F16) bf16 rows
-// become fp16 ones divided by a power of two that brings their largest element
-// to [2^14, 2^15); power[r] and power2[r] get it.
+// Query rows of a segment on their way into the swizzled operand: rows
+// [first_row, first_row + 128) by THREADS threads, 8 (or fewer) 16-byte pieces
+// of each in registers between fetch and store, BATCHES times.  Rows without a
+// node are zero.  For FP8 caches (TO_F16) bf16 rows become fp16 ones divided by
+// a power of two that brings their largest element to [2^14, 2^15).
 template <int D, int THREADS, bool TO_F16>
-__device__ __forceinline__ void tree_load_q(const TreeParams &p, const TreeWalk<D> &w, uint32_t q_smem, int first_row,
-                                            int tid, [[maybe_unused]] float2 *power, [[maybe_unused]] float2 *power2)
-{
-    constexpr int kChunks = D / 8, kStep = THREADS / kChunks, kRounds = 128 / kStep, kBatch = kRounds < 8 ? kRounds : 8;
-    const int g = w.seg / w.s.groups;
-    const uint32_t flip = p.negate_q ? 0x80008000u : 0u;
-    const int chunk = tid % kChunks;
-#pragma unroll 1
-    for (int n = 0; n < kRounds; n += kBatch) {
-        uint4 x[kBatch];
+struct TreeQuery {
+    static constexpr int kChunks = D / 8, kStep = THREADS / kChunks, kRounds = 128 / kStep;
+    static constexpr int kBatch = kRounds < 8 ? kRounds : 8, kBatches = kRounds / kBatch;
+    uint4 x[kBatch];
+
+    __device__ __forceinline__ void fetch(const TreeParams &p, const TreeWalk<D> &w, int first_row, int tid, int batch)
+    {
+        const int g = w.seg / w.s.groups, chunk = tid % kChunks;
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            const int row = first_row + tid / kChunks + (n + k) * kStep, i = row / p.group, h = row - i * p.group;
+            const int row = first_row + tid / kChunks + (batch * kBatch + k) * kStep, i = row / p.group, h = row - i * p.group;
             x[k] = make_uint4(0, 0, 0, 0);
             if (i < w.r.t)
                 x[k] = __ldg(reinterpret_cast<const uint4 *>(
                                  p.q + (((long long)w.b * p.tree_len + i) * p.hq + g * p.group + h) * D) + chunk);
         }
+    }
+    // power, power2: where the rows' exponents go
+    __device__ __forceinline__ void store(const TreeParams &p, uint32_t q_smem, int tid, int batch,
+                                          [[maybe_unused]] int8_t *power, [[maybe_unused]] int8_t *power2)
+    {
+        const uint32_t flip = p.negate_q ? 0x80008000u : 0u;
+        const int chunk = tid % kChunks;
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            const int r = tid / kChunks + (n + k) * kStep;
+            const int r = tid / kChunks + (batch * kBatch + k) * kStep;
             uint32_t v[4] = {x[k].x ^ flip, x[k].y ^ flip, x[k].z ^ flip, x[k].w ^ flip};
             if constexpr (TO_F16) {
-                float up = 1.f;   // the power of two
+                int ex = 0;
                 if (!p.q_f16) {
                     float top = 0.f;
 #pragma unroll
@@ -740,9 +774,8 @@ __device__ __forceinline__ void tree_load_q(const TreeParams &p, const TreeWalk<
 #pragma unroll
                     for (int off = kChunks / 2; off; off >>= 1)
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-                    // exponent of the largest, kept where 2^(+-) are normal numbers (infinite: the largest one)
-                    const int ex = min(max((__float_as_int(top) >> 23 & 255) - 127 - 14, -120), 113);
-                    up = __int_as_float((127 + ex) << 23);
+                    // kept where 2^(+-ex) are normal numbers (infinite: as the largest number)
+                    ex = min(max((__float_as_int(top) >> 23 & 255) - 127 - 14, -120), 113);
                     const float down = __int_as_float((127 - ex) << 23);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -751,14 +784,14 @@ __device__ __forceinline__ void tree_load_q(const TreeParams &p, const TreeWalk<
                     }
                 }
                 if (chunk == 0) {
-                    power[r].x = up;
-                    power2[r].x = up;
+                    power[r] = (int8_t)ex;
+                    power2[r] = (int8_t)ex;
                 }
             }
             sts128(q_smem + (chunk / 8) * (128 * 128) + r * 128 + (((chunk & 7) ^ (r & 7)) << 4), make_uint4(v[0], v[1], v[2], v[3]));
         }
     }
-}
+};
 
 // V tile rows from `from` on: those at or past `valid` become zero, and in the
 // others (tree nodes) elements that are not finite do, their node marked in bad.
@@ -841,12 +874,12 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
     // this thread's sums of the units before the last flush, relative to the maximum then
     float *sums = p.ws_sums + ((long long)(blockIdx.x * C::kGroups + group) * (D / 4) * p.sum_rows + tid) * 4;
     const bool has_sums = tid < p.sum_rows;
-    float ref = 0.f;   // the maximum that the sums are relative to: the one at the segment's first flush
+    float ref = kNegInf;   // the maximum that the sums are relative to: the one at the segment's first flush
     // sums += accumulator * 2^((now - ref) scale), by reductions that nothing waits
     // for: the rows are this thread's own, so their order is the program's
     auto flush_sums = [&](bool fresh, float now) {
-        if (fresh)
-            ref = now == kNegInf ? 0.f : now;
+        if (fresh || ref == kNegInf)
+            ref = now;   // nothing was added yet, or only zeros
         float up = now == kNegInf ? 0.f : (now - ref) * sl;
         if (!fresh && __any_sync(0xffffffffu, up > 60.f)) {   // rare: move the reference
             const float corr = exp2_approx(-up);
@@ -857,7 +890,7 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
                     const float4 x = __ldcg(at);
                     *at = make_float4(x.x * corr, x.y * corr, x.z * corr, x.w * corr);
                 }
-            ref = now == kNegInf ? ref : now;
+            ref = now;
             up = 0.f;
         }
         const float scale = exp2_approx(up);
@@ -883,18 +916,40 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
     };
     TreeWalk<D> w;
     w.start(p, m);
-    auto load_q = [&]() {
-        const int first = (w.seg % w.s.groups) * p.rows;
-        if (shared_rows)
-            tree_load_q<D, C::kSoftThreads, kv_is_fp8(KV)>(p, w, q_smem, first, threadIdx.x, m.ml[0], m.ml[1]);
-        else
-            tree_load_q<D, 128, kv_is_fp8(KV)>(p, w, q_smem + group * C::kQBytes, first + group * 128, tid, m.ml[group], m.ml[group]);
+    // the rows of a segment, fetched early (with one set of rows, by all
+    // threads) and stored when the MMAs are done with those before
+    auto first_row = [&](const TreeWalk<D> &of) { return (of.seg % of.s.groups) * p.rows; };
+    TreeQuery<D, C::kSoftThreads, kv_is_fp8(KV)> q_all;
+    auto fetch_q = [&](const TreeWalk<D> &of) {
+        if (!own_rows)
+            q_all.fetch(p, of, first_row(of), threadIdx.x, 0);
+    };
+    auto store_q = [&](const TreeWalk<D> &of) {
+        if (!own_rows) {
+            q_all.store(p, q_smem, threadIdx.x, 0, m.power[0], m.power[1]);
+            if constexpr (q_all.kBatches > 1) {
+#pragma unroll 1
+                for (int n = 1; n < q_all.kBatches; ++n) {
+                    q_all.fetch(p, of, first_row(of), threadIdx.x, n);
+                    q_all.store(p, q_smem, threadIdx.x, n, m.power[0], m.power[1]);
+                }
+            }
+        } else {
+            TreeQuery<D, 128, kv_is_fp8(KV)> q_own;
+#pragma unroll 1
+            for (int n = 0; n < q_own.kBatches; ++n) {
+                q_own.fetch(p, of, first_row(of) + group * 128, tid, n);
+                q_own.store(p, q_smem + group * C::kQBytes, tid, n, m.power[group], m.power[group]);
+            }
+        }
         fence_async_shared();
-        tc_fence_before();
         mbar_arrive(smem_addr(&m.qfull));
     };
-    if (w.n > 0)
-        load_q();
+    if (w.n > 0) {
+        fetch_q(w);
+        store_q(w);
+    }
+    int odd = 0;   // segments, modulo 2
     while (w.n > 0) {
         const TreeUnits un = tree_units<D>(p, w);
         const int L = w.r.L, t = w.r.t, base = L - t;
@@ -907,7 +962,7 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
             if (!(ok = wait(&m.qfull, qph)))
                 break;
             qph ^= 1u;
-            sl = fmaxf(p.scale_log2 * m.ml[group][tid].x, kTreeLeastScale);
+            sl = fmaxf(p.scale_log2 * __int_as_float((127 + m.power[group][tid]) << 23), kTreeLeastScale);
         }
         float mx = kNegInf, l = 0.f;
         int mine = 0;                                // units of this group so far in the segment
@@ -1003,7 +1058,7 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
                 const int vs = (vcount + tile) % p.v_slots;
                 if (!(ok = wait(&m.vfull[vs], ((vcount + tile) / p.v_slots) & 1)))
                     break;
-                tree_clean_v<D, F16, LOAD>(v_ring + vs * C::kSlotBytes, max(0, base - t0), L - t0, t0 - base, m.bad, tid);
+                tree_clean_v<D, F16, LOAD>(v_ring + vs * C::kSlotBytes, max(0, base - t0), L - t0, t0 - base, m.bad[odd], tid);
                 fence_async_shared();
             }
             // The weights, 64 positions at a time: the MMAs of the first half
@@ -1057,6 +1112,10 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
             break;
         tc_fence_after();
         vcount += w.n;
+        TreeWalk<D> next = w;
+        next.next(p);
+        if (next.n > 0)
+            fetch_q(next);
 
         // the segment's result: O / l and the log-sum-exp (base 2), final or partial
         if (mine > C::kFlush && warp_live) {
@@ -1071,14 +1130,21 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
             mx = kNegInf;
             l = 0.f;
         }
-        if (shared_rows)
+        const bool two = shared_rows && w.n > 1;     // the second group had a tile
+        if (shared_rows && (group == 0 || two))
             m.ml[group][tid] = make_float2(mx, l);
         if (!(ok = pair_sync()))
             break;
+        // both groups' units are done: the next rows may come, and their scores
+        // be formed beside what follows.  (ml of the next segment is written by
+        // groups with units, after their MMAs, which wait for ofree.)
+        if (threadIdx.x < kMaxTree / 32)
+            m.bad[odd ^ 1][threadIdx.x] = 0;         // the last segment's, read before its end
+        if (next.n > 0)
+            store_q(next);
         float a0 = 1.f, a1 = 0.f;
-        const bool two = shared_rows && w.n > 1;     // the second group had a tile
         if (shared_rows) {
-            const float2 x = m.ml[0][tid], y = m.ml[1][tid];
+            const float2 x = m.ml[0][tid], y = two ? m.ml[1][tid] : make_float2(kNegInf, 0.f);
             mx = fmaxf(x.x, y.x);
             a0 = x.x == kNegInf ? 0.f : exp2_approx((x.x - mx) * sl);
             a1 = y.x == kNegInf ? 0.f : exp2_approx((y.x - mx) * sl);
@@ -1143,6 +1209,8 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
                     *reinterpret_cast<float4 *>(dst + k * stride) = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
             }
         }
+        tc_fence_before();
+        mbar_arrive(smem_addr(&m.ofree));
         if (in_call && (!shared_rows || group == 0)) {
             if (!whole)
                 p.ws_lse[slot * p.slot_rows + srow] = lse2;
@@ -1151,7 +1219,7 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
         }
         // values that are not finite, of nodes in this CTA's tiles
         for (int wd = 0; wd < kMaxTree / 32; ++wd) {
-            uint32_t nodes = m.bad[wd];
+            uint32_t nodes = m.bad[odd][wd];
             for (; nodes; nodes &= nodes - 1) {
                 const int node = 32 * wd + __ffs(nodes) - 1;
                 if (!any || !(tree_bits(p, mask_row, i, node, t) & 1u))
@@ -1172,14 +1240,8 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
                 }
             }
         }
-        tc_fence_before();
-        if (!(ok = pair_sync()))
-            break;
-        if (threadIdx.x < kMaxTree / 32)
-            m.bad[threadIdx.x] = 0;
-        w.next(p);
-        if (w.n > 0)
-            load_q();
+        w = next;
+        odd ^= 1;
     }
     if (!ok) {
         atomicOr(p.ws_err, kErrTimeout);
@@ -1227,6 +1289,7 @@ tree_split_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ 
             mbar_init(smem_addr(&m.pvdone[s]), 1);
         }
         mbar_init(smem_addr(&m.qfull), C::kSoftThreads);
+        mbar_init(smem_addr(&m.ofree), C::kSoftThreads);
         mbar_init(smem_addr(&m.pair), C::kSoftThreads);
         mbar_init(smem_addr(&m.drain), 1);
         mbar_init_fence();
@@ -1237,8 +1300,8 @@ tree_split_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ 
             tma_prefetch_desc(&tmv);
         }
     }
-    if (tid < kMaxTree / 32)
-        m.bad[tid] = 0;
+    if (tid < 2 * (kMaxTree / 32))
+        (&m.bad[0][0])[tid] = 0;
     pdl_wait_prior_grid();
     pdl_launch_dependents();
 
@@ -1278,7 +1341,7 @@ tree_split_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ 
         const long long cost = tree_cost(s);
         if (works && at <= x0 && x0 < at + cost) {
             const long long rel = x0 - at - kTreeSegCost;
-            long long seg = rel < 0 ? 0 : rel / (s.nb + kTreeSegCost);
+            long long seg = rel < 0 ? 0 : TreeSplit::quotient(rel, s.nb + kTreeSegCost);
             long long j = rel < 0 ? 0 : rel - seg * (s.nb + kTreeSegCost);
             if (j >= s.nb) {   // the gap before the next segment (there is one: the last ends with its tiles)
                 ++seg;
