@@ -427,29 +427,29 @@ __device__ __forceinline__ void tree_convert(uint32_t raw, uint32_t tile, int ti
     constexpr int kRowUnits = D / 16, kUnits = C::kN * kRowUnits;
     static_assert(kUnits % C::kCopyThreads == 0, "whole rounds");
     constexpr int kRounds = kUnits / C::kCopyThreads, kBatch = 4;
-    static_assert(kRounds % kBatch == 0, "whole batches");
-    // 8 lanes: units 4 n .. 4 n + 3 of rows 2 k, 2 k + 1
-    auto row_of = [](int e) { return 2 * (e / 8 / (kRowUnits / 4)) + ((e & 7) >> 2); };
-    auto unit_of = [](int e) { return 4 * (e / 8 % (kRowUnits / 4)) + (e & 3); };
-#pragma unroll 1
+    // 8 lanes: units 4 n .. 4 n + 3 of rows 2 k, 2 k + 1.  From round to round a
+    // thread stays on its unit and moves on by a multiple of 8 rows, so its
+    // addresses move by constants.
+    constexpr int kQuads = kRowUnits / 4, kRowStep = 2 * (C::kCopyThreads / 8) / kQuads;
+    static_assert(kRounds % kBatch == 0 && kRowStep % 8 == 0, "whole batches and swizzle periods");
+    const int row = 2 * (tid / 8 / kQuads) + ((tid & 7) >> 2), unit = 4 * (tid / 8 % kQuads) + (tid & 3), c = 2 * (unit & 3);
+    const uint32_t from = raw + row * D + unit * 16;
+    const uint32_t at = tile + (unit / 4) * C::kPartBytes + row * 128;
+    const uint32_t to0 = at + ((c ^ (row & 7)) << 4), to1 = at + (((c + 1) ^ (row & 7)) << 4);
+#pragma unroll
     for (int n = 0; n < kRounds; n += kBatch) {
         uint4 x[kBatch];
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            const int e = tid + (n + k) * C::kCopyThreads;
-            x[k] = lds128(raw + row_of(e) * D + unit_of(e) * 16);
-        }
+        for (int k = 0; k < kBatch; ++k)
+            x[k] = lds128(from + (n + k) * kRowStep * D);
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            const int e = tid + (n + k) * C::kCopyThreads, row = row_of(e), unit = unit_of(e);
-            const uint32_t at = tile + (unit / 4) * C::kPartBytes + row * 128;
-            const int c = 2 * (unit & 3);
             const uint4 lo = make_uint4(fp8x2_to_f16x2<KV>(lo16(x[k].x)), fp8x2_to_f16x2<KV>(hi16(x[k].x)),
                                         fp8x2_to_f16x2<KV>(lo16(x[k].y)), fp8x2_to_f16x2<KV>(hi16(x[k].y)));
             const uint4 hi = make_uint4(fp8x2_to_f16x2<KV>(lo16(x[k].z)), fp8x2_to_f16x2<KV>(hi16(x[k].z)),
                                         fp8x2_to_f16x2<KV>(lo16(x[k].w)), fp8x2_to_f16x2<KV>(hi16(x[k].w)));
-            sts128(at + ((c ^ (row & 7)) << 4), lo);
-            sts128(at + (((c + 1) ^ (row & 7)) << 4), hi);
+            sts128(to0 + (n + k) * kRowStep * 128, lo);
+            sts128(to1 + (n + k) * kRowStep * 128, hi);
         }
     }
 }
