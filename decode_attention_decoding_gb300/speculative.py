@@ -8,7 +8,10 @@ fd_cache_compact (include/fd.h).
     lens = fd_cache_compact(k_pages, v_pages, tables.seq_lens, accepted, accept_lens, tree_len, block_table=table)
 
 Like the package's other functions these only check and marshal arguments;
-tensors live on one GPU, outputs are allocated unless they are given.
+tensors live on one GPU, outputs are allocated unless they are given.  A call
+runs on that GPU's current stream, whatever device is current.  These calls
+take a few microseconds on the GPU, so the checks are kept to a few attribute
+reads a tensor.
 """
 from __future__ import annotations
 
@@ -18,14 +21,16 @@ from typing import NamedTuple
 
 import torch
 
-from . import (FD_ERR_INVALID_ARG, FD_OK, FdError, FdOptions, _bits, _dtype_code, _kv_code, _lib, _options,
-               _ptr, _stream_ptr, fd_workspace_init)
+from . import (FD_ERR_INVALID_ARG, FD_OK, FdError, FdOptions, _dtype_code, _kv_code, _lib, _options,
+               fd_workspace_init)
 
 __all__ = ["fd_build_tables", "fd_cache_write", "fd_cache_compact", "fd_tree_workspace_size", "make_tree_workspace",
            "fd_tree_decode", "fd_tree_decode_paged", "Tables", "FD_DEVICE_STATUS_BAD_LENGTH",
            "FD_DEVICE_STATUS_NO_PAGES", "FD_DEVICE_STATUS_BAD_SLOT"]
 
 FD_DEVICE_STATUS_BAD_LENGTH, FD_DEVICE_STATUS_NO_PAGES, FD_DEVICE_STATUS_BAD_SLOT = 0x2, 0x4, 0x8
+
+_I32, _F32, _I64, _BF16, _F16 = torch.int32, torch.float32, torch.int64, torch.bfloat16, torch.float16
 
 
 class Tables(NamedTuple):
@@ -38,31 +43,44 @@ class Tables(NamedTuple):
     free_count: torch.Tensor    # [1] int32
 
 
-def _dev(t, name, dtype, shape, device):
-    """t as a contiguous tensor of this type and shape on the call's device (shape entries None: any)."""
-    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the call runs on {device}")
-    if t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
-        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
-    return t
+def _gpu(t, name):
+    """Index of the GPU that t is on."""
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return index
 
 
-def _status(t, device):
+def _ptr_of(t, name, dtype, shape, gpu):
+    """Address of a contiguous tensor of this type and shape on the call's GPU."""
+    if t.dtype is not dtype or t.get_device() != gpu or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on cuda:{gpu}, got "
+                         f"{t.dtype} {list(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _table_of(t, rows, gpu):
+    """(address, columns) of a block table [rows, max_blocks]."""
+    if t.dim() != 2:
+        raise ValueError(f"block_table must be [{rows}, max_blocks], got {list(t.shape)}")
+    return _ptr_of(t, "block_table", _I32, (rows, t.shape[1]), gpu), t.shape[1]
+
+
+def _status(t, gpu):
     if t is None:
         return None
-    if t.dtype not in (torch.int32, torch.uint32) or not t.is_cuda or t.device != device or t.numel() != 1:
+    if t.dtype not in (torch.int32, torch.uint32) or t.get_device() != gpu or t.numel() != 1:
         raise ValueError("device_status must be one int32 or uint32 on the call's device")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
-def _launch(device, f, *args):
-    """Call f with the call's device current (kernels launch on the current device)."""
-    if torch.cuda.current_device() == device.index:
-        return f(*args)
-    with torch.cuda.device(device):
-        return f(*args)
+def _launch(gpu, stream, f, *args):
+    """Call f with the stream as its last argument and the call's GPU current (kernels launch on the current one)."""
+    s = torch.cuda.current_stream(gpu).cuda_stream if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == gpu:
+        return f(*args, s)
+    with torch.cuda.device(gpu):
+        return f(*args, s)
 
 
 def fd_build_tables(seq_lens, new_lens, block_table, free_pages, free_count, page_size, num_pages, max_tokens,
@@ -73,40 +91,37 @@ def fd_build_tables(seq_lens, new_lens, block_table, free_pages, free_count, pag
     max_blocks], updated in place; free_pages int32 [n], a stack whose first
     free_count (int32 [1]) entries are free; max_tokens the length of the slot
     map (entries behind the last token are -1).  Returns a Tables."""
-    i32 = torch.int32
-    dev = block_table.device
+    gpu = _gpu(block_table, "block_table")
     B = seq_lens.shape[0]
-    _dev(block_table, "block_table", i32, (B, None), dev)
-    _dev(seq_lens, "seq_lens", i32, (B,), dev)
-    _dev(new_lens, "new_lens", i32, (B,), dev)
-    _dev(free_pages, "free_pages", i32, (None,), dev)
-    _dev(free_count, "free_count", i32, (1,), dev)
-    if held_pages is not None:
-        _dev(held_pages, "held_pages", i32, (B,), dev)
+    per_request, n = (B,), int(max_tokens)
+    table, blocks = _table_of(block_table, B, gpu)
+    dev = block_table.device
     if slot_map is None:
-        slot_map = torch.empty(int(max_tokens), dtype=torch.int64, device=dev)
-    else:
-        _dev(slot_map, "slot_map", torch.int64, (int(max_tokens),), dev)
-    cu, lens, held, left = torch.empty(3 * B + 2, dtype=i32, device=dev).split((B + 1, B, B, 1))
-    st = _launch(dev, _lib.fd_build_tables, _ptr(seq_lens), _ptr(new_lens), _ptr(held_pages), _ptr(free_pages),
-                 _ptr(free_count), free_pages.shape[0], B, int(page_size), int(num_pages), block_table.shape[1],
-                 int(max_tokens), _ptr(block_table), _ptr(slot_map), _ptr(cu), _ptr(lens), _ptr(held), _ptr(left),
-                 _status(device_status, dev), _stream_ptr(stream, dev))
+        slot_map = torch.empty(n, dtype=_I64, device=dev)
+    if free_pages.dim() != 1:
+        raise ValueError("free_pages must be 1-d")
+    cu, lens, held, left = torch.split_with_sizes(torch.empty(3 * B + 2, dtype=_I32, device=dev), (B + 1, B, B, 1))
+    st = _launch(gpu, stream, _lib.fd_build_tables, _ptr_of(seq_lens, "seq_lens", _I32, per_request, gpu),
+                 _ptr_of(new_lens, "new_lens", _I32, per_request, gpu),
+                 None if held_pages is None else _ptr_of(held_pages, "held_pages", _I32, per_request, gpu),
+                 _ptr_of(free_pages, "free_pages", _I32, free_pages.shape, gpu),
+                 _ptr_of(free_count, "free_count", _I32, (1,), gpu), free_pages.shape[0], B, int(page_size),
+                 int(num_pages), blocks, n, table, _ptr_of(slot_map, "slot_map", _I64, (n,), gpu), cu.data_ptr(),
+                 lens.data_ptr(), held.data_ptr(), left.data_ptr(), _status(device_status, gpu))
     if check and st != FD_OK:
         raise FdError(st, "fd_build_tables")
     return Tables(block_table, slot_map, cu, lens, held, left)
 
 
-def _token_rows(t, name, device):
-    """(pointer, stride in elements) of new K or V rows [n, Hkv, D], dense inside a row."""
-    if t.dtype not in (torch.bfloat16, torch.float16) or not t.is_cuda or t.dim() != 3:
-        raise ValueError(f"{name} must be a bf16 or fp16 CUDA tensor [n, Hkv, D]")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the call runs on {device}")
-    n, h, d = t.shape
-    if t.stride(2) != 1 or (h > 1 and t.stride(1) != d):
+def _token_rows(t, name, gpu):
+    """Check new K or V rows [n, Hkv, D], dense inside a token's row; their stride in elements."""
+    if (t.dtype is not _BF16 and t.dtype is not _F16) or t.dim() != 3 or t.get_device() != gpu:
+        raise ValueError(f"{name} must be a bf16 or fp16 tensor [n, Hkv, D] on cuda:{gpu}, got {t.dtype} "
+                         f"{list(t.shape)} on {t.device}")
+    token, head, element = t.stride()
+    if element != 1 or (head != t.shape[2] and t.shape[1] > 1):
         raise ValueError(f"{name}: a token's heads must be dense (only the token stride is free)")
-    return t.stride(0)
+    return token
 
 
 def fd_cache_write(k_new, v_new, slot_map, k_cache, v_cache, kv_dtype=None, k_scale=1.0, v_scale=1.0,
@@ -118,21 +133,20 @@ def fd_cache_write(k_new, v_new, slot_map, k_cache, v_cache, kv_dtype=None, k_sc
     (pages [num_pages, P, Hkv, D], a contiguous cache [B, S, Hkv, D], or flat
     slots) of the same type, or FP8: float8 tensors, or uint8 codes with
     kv_dtype 'e4m3' / 'e5m2', quantised by k_scale / v_scale."""
-    dev = k_cache.device
-    ks, vs = _token_rows(k_new, "k_new", dev), _token_rows(v_new, "v_new", dev)
+    gpu = _gpu(k_cache, "k_cache")
+    ks, vs = _token_rows(k_new, "k_new", gpu), _token_rows(v_new, "v_new", gpu)
     kv = _kv_code(k_cache, v_cache, kv_dtype)
-    n, h, d = k_new.shape
-    if v_new.shape != k_new.shape or v_new.dtype != k_new.dtype:
+    n, h, d = shape = k_new.shape
+    if v_new.shape != shape or v_new.dtype is not k_new.dtype:
         raise ValueError("k_new and v_new must have one shape and type")
-    if k_cache.shape != v_cache.shape or v_cache.device != dev or k_cache.dim() < 3 or tuple(k_cache.shape[-2:]) != (h, d):
+    if k_cache.shape != v_cache.shape or v_cache.get_device() != gpu or k_cache.dim() < 3 or k_cache.shape[-2:] != (h, d):
         raise ValueError(f"k_cache and v_cache must have one shape [..., {h}, {d}] on one device")
-    if kv == 0 and (k_cache.dtype != k_new.dtype or v_cache.dtype != k_new.dtype):
+    if kv == 0 and (k_cache.dtype is not k_new.dtype or v_cache.dtype is not k_new.dtype):
         raise TypeError("a 16-bit cache must be of the new rows' type")
-    _dev(slot_map, "slot_map", torch.int64, (n,), dev)
-    opts = FdOptions(0, 0, 0, None, None, _dtype_code(k_new, None), kv, float(k_scale), float(v_scale), 1)
-    st = _launch(dev, _lib.fd_cache_write, _ptr(k_new), _ptr(v_new), ks, vs, _ptr(slot_map), n, h, d, _ptr(k_cache),
-                 _ptr(v_cache), k_cache.numel() // (h * d), ctypes.byref(opts), _status(device_status, dev),
-                 _stream_ptr(stream, dev))
+    opts = FdOptions(0, 0, 0, None, None, 1 if k_new.dtype is _F16 else 0, kv, k_scale, v_scale, 1)
+    st = _launch(gpu, stream, _lib.fd_cache_write, k_new.data_ptr(), v_new.data_ptr(), ks, vs,
+                 _ptr_of(slot_map, "slot_map", _I64, (n,), gpu), n, h, d, k_cache.data_ptr(), v_cache.data_ptr(),
+                 k_cache.numel() // (h * d) if h * d else 0, opts, _status(device_status, gpu))
     if check and st != FD_OK:
         raise FdError(st, "fd_cache_write")
 
@@ -147,32 +161,33 @@ def fd_cache_compact(k_cache, v_cache, seq_lens, accepted, accept_lens, tree_len
     [B] with the drafted tokens; accepted int32 [B, max_accept], ascending node
     indices; accept_lens int32 [B]; tree_lens int32 [B] or None (tree_len for
     every request).  Returns the new lengths int32 [B]."""
-    dev, i32 = k_cache.device, torch.int32
+    gpu = _gpu(k_cache, "k_cache")
     B = seq_lens.shape[0]
+    per_request = (B,)
+    size = k_cache.element_size()
     for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if not t.is_cuda or not t.is_contiguous() or t.dim() != 4 or t.device != dev or t.element_size() > 2:
-            raise ValueError(f"{name} must be a contiguous 4-d CUDA tensor of 16-bit or FP8 elements")
-    if k_cache.shape != v_cache.shape or k_cache.element_size() != v_cache.element_size():
+        if not t.is_contiguous() or t.dim() != 4 or t.get_device() != gpu or size > 2:
+            raise ValueError(f"{name} must be a contiguous 4-d tensor of 16-bit or FP8 elements on cuda:{gpu}")
+    if k_cache.shape != v_cache.shape or size != v_cache.element_size():
         raise ValueError("k_cache and v_cache must have one shape and type")
-    _dev(seq_lens, "seq_lens", i32, (B,), dev)
-    _dev(accepted, "accepted", i32, (B, None), dev)
-    _dev(accept_lens, "accept_lens", i32, (B,), dev)
-    if tree_lens is not None:
-        _dev(tree_lens, "tree_lens", i32, (B,), dev)
+    if accepted.dim() != 2:
+        raise ValueError(f"accepted must be [{B}, max_accept], got {list(accepted.shape)}")
     pages, page, h, d = k_cache.shape
-    blocks = 0
+    table, blocks = None, 0
     if block_table is not None:
-        blocks = _dev(block_table, "block_table", i32, (B, None), dev).shape[1]
+        table, blocks = _table_of(block_table, B, gpu)
     elif pages != B:
         raise ValueError(f"a contiguous cache must hold {B} requests, got {pages}")
     if seq_lens_out is None:
         seq_lens_out = torch.empty_like(seq_lens)
-    else:
-        _dev(seq_lens_out, "seq_lens_out", i32, (B,), dev)
-    opts = FdOptions(0, 0, 0, None, None, 0, 1 if k_cache.element_size() == 1 else 0, 0.0, 0.0, 1)
-    st = _launch(dev, _lib.fd_cache_compact, _ptr(k_cache), _ptr(v_cache), _ptr(block_table), blocks, page, pages,
-                 _ptr(seq_lens), _ptr(tree_lens), int(tree_len), _ptr(accepted), _ptr(accept_lens), accepted.shape[1],
-                 B, h, d, _ptr(seq_lens_out), ctypes.byref(opts), _status(device_status, dev), _stream_ptr(stream, dev))
+    most = accepted.shape[1]
+    opts = FdOptions(0, 0, 0, None, None, 0, 1 if size == 1 else 0, 0.0, 0.0, 1)
+    st = _launch(gpu, stream, _lib.fd_cache_compact, k_cache.data_ptr(), v_cache.data_ptr(), table, blocks, page, pages,
+                 _ptr_of(seq_lens, "seq_lens", _I32, per_request, gpu),
+                 None if tree_lens is None else _ptr_of(tree_lens, "tree_lens", _I32, per_request, gpu), int(tree_len),
+                 _ptr_of(accepted, "accepted", _I32, (B, most), gpu),
+                 _ptr_of(accept_lens, "accept_lens", _I32, per_request, gpu), most, B, h, d,
+                 _ptr_of(seq_lens_out, "seq_lens_out", _I32, per_request, gpu), opts, _status(device_status, gpu))
     if check and st != FD_OK:
         raise FdError(st, "fd_cache_compact")
     return seq_lens_out
@@ -188,66 +203,66 @@ def make_tree_workspace(batch, tree_len, num_q_heads, num_kv_heads, head_dim=128
     if n == 0:
         raise FdError(FD_ERR_INVALID_ARG, "fd_tree_workspace_size")
     ws = torch.empty(n, dtype=torch.uint8, device=device)
-    _launch(ws.device, fd_workspace_init, ws)
+    with torch.cuda.device(ws.device):
+        fd_workspace_init(ws)
     return ws
 
 
-def _tree_args(q, k, v, tree_mask, tree_lens, seq_lens, seq_lens_host, scale, out, lse, workspace, num_ctas, flags,
-               wait_timeout_ns, split_events, dtype, kv_dtype, k_scale, v_scale, block_table):
-    """Checks shared by both layouts; the arguments of the C calls that they share."""
-    i32 = torch.int32
-    _bits(q, "q")
+def _tree(name, q, k, v, block_table, seq_lens, tree_mask, tree_lens, seq_lens_host, scale, out, lse, workspace, num_ctas,
+          flags, wait_timeout_ns, split_events, stream, check, dtype, kv_dtype, k_scale, v_scale):
+    """Both layouts: checks, outputs, and the call `name`."""
+    gpu = _gpu(q, "q")
+    if q.dim() != 4 or not q.is_contiguous() or q.element_size() != 2:
+        raise ValueError("q must be a contiguous bf16 or fp16 tensor [B, tree_len, Hq, D]")
     kv = _kv_code(k, v, kv_dtype)
-    dev = q.device
-    if q.dim() != 4:
-        raise ValueError("q must be [B, tree_len, Hq, D]")
-    B, T, hq, d = q.shape
-    if k.dim() != 4 or k.shape != v.shape or k.device != dev or v.device != dev or k.shape[3] != d:
-        raise ValueError(f"k and v must have one 4-d shape with head_dim {d} on {dev}")
-    if kv == 0 and (k.element_size() != 2 or v.element_size() != 2):
+    B, T, hq, d = shape = q.shape
+    if k.dim() != 4 or k.shape != v.shape or k.get_device() != gpu or v.get_device() != gpu or k.shape[3] != d:
+        raise ValueError(f"k and v must have one 4-d shape with head_dim {d} on cuda:{gpu}")
+    if kv == 0 and (k.element_size() != 2 or v.element_size() != 2 or
+                    (_F16 in (q.dtype, k.dtype, v.dtype) and _BF16 in (q.dtype, k.dtype, v.dtype))):
         raise TypeError("a 16-bit cache must be of q's type")
-    if kv == 0 and torch.float16 in (q.dtype, k.dtype, v.dtype) and torch.bfloat16 in (q.dtype, k.dtype, v.dtype):
-        raise TypeError("a 16-bit cache must be of q's type")
-    hkv = k.shape[2]
-    if tree_lens is not None:
-        _dev(tree_lens, "tree_lens", i32, (B,), dev)
-    if seq_lens is not None:
-        _dev(seq_lens, "seq_lens", i32, (B,), dev)
+    pages, page, hkv, _ = k.shape
+    per_request = (B,)
+    layout = ()
     if block_table is not None:
-        _dev(block_table, "block_table", i32, (B, None), dev)
-    elif k.shape[0] != B:
-        raise ValueError(f"a contiguous cache must hold {B} requests, got {k.shape[0]}")
-    stride, words = 0, (T + 63) // 64
+        layout = _table_of(block_table, B, gpu)
+    elif pages != B:
+        raise ValueError(f"a contiguous cache must hold {B} requests, got {pages}")
+    stride, words, mask = 0, (T + 63) // 64, None
     if tree_mask is not None:
-        if tree_mask.dtype not in (torch.int64, torch.uint64):
+        if tree_mask.dtype is not _I64 and tree_mask.dtype is not torch.uint64:
             raise ValueError("tree_mask must be int64 or uint64 words")
         if tree_mask.dim() == 3:
-            _dev(tree_mask, "tree_mask", tree_mask.dtype, (B, T, words), dev)
             stride = T * words
+            mask = _ptr_of(tree_mask, "tree_mask", tree_mask.dtype, (B, T, words), gpu)
         else:
-            _dev(tree_mask, "tree_mask", tree_mask.dtype, (T, words), dev)
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
+            mask = _ptr_of(tree_mask, "tree_mask", tree_mask.dtype, (T, words), gpu)
     if out is None:
-        out = torch.empty((B, T, hq, d), dtype=torch.float32, device=dev)
-    else:
-        _dev(out, "out", torch.float32, (B, T, hq, d), dev)
+        out = torch.empty(shape, dtype=_F32, device=q.device)
     if lse is None:
-        lse = torch.empty((B, T, hq), dtype=torch.float32, device=dev)
-    elif lse is not False:
-        _dev(lse, "lse", torch.float32, (B, T, hq), dev)
+        lse = torch.empty((B, T, hq), dtype=_F32, device=q.device)
+    elif lse is False:
+        lse = None
     if workspace is None:
-        workspace = make_tree_workspace(B, T, hq, hkv, d, dev)
-    elif not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-    lh = None if seq_lens_host is None else seq_lens_host.to(torch.int32).contiguous().cpu()
-    if lh is not None and lh.numel() != B:
-        raise ValueError(f"seq_lens_host must hold {B} lengths")
+        workspace = make_tree_workspace(B, T, hq, hkv, d, q.device)
+    elif workspace.get_device() != gpu or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{gpu}")
+    host = None
+    if seq_lens_host is not None:
+        host = seq_lens_host.to(torch.int32).contiguous().cpu()
+        if host.numel() != B:
+            raise ValueError(f"seq_lens_host must hold {B} lengths")
     opts = _options(num_ctas, flags, wait_timeout_ns, split_events, _dtype_code(q, dtype), kv, k_scale, v_scale, 1)
-    mask = (_ptr(tree_mask), stride, _ptr(tree_lens), _ptr(seq_lens), _ptr(lh), B, T, hq, hkv, d)
-    tail = (float(scale), _ptr(out), None if lse is False else _ptr(lse), _ptr(workspace),
-            workspace.numel() * workspace.element_size(), ctypes.byref(opts))
-    return dev, mask, tail, out, (None if lse is False else lse), (lh, opts, workspace)
+    st = _launch(gpu, stream, getattr(_lib, name), q.data_ptr(), k.data_ptr(), v.data_ptr(), *layout, mask, stride,
+                 None if tree_lens is None else _ptr_of(tree_lens, "tree_lens", _I32, per_request, gpu),
+                 None if seq_lens is None else _ptr_of(seq_lens, "seq_lens", _I32, per_request, gpu),
+                 None if host is None else host.data_ptr(), B, T, hq, hkv, d, page, *((pages,) if layout else ()),
+                 1.0 / math.sqrt(d) if scale is None else scale, _ptr_of(out, "out", _F32, shape, gpu),
+                 None if lse is None else _ptr_of(lse, "lse", _F32, (B, T, hq), gpu), workspace.data_ptr(),
+                 workspace.numel() * workspace.element_size(), opts)
+    if check and st != FD_OK:
+        raise FdError(st, name)
+    return out, lse
 
 
 def fd_tree_decode(q, k, v, seq_lens=None, tree_mask=None, tree_lens=None, seq_lens_host=None, scale=None, out=None,
@@ -260,14 +275,9 @@ def fd_tree_decode(q, k, v, seq_lens=None, tree_mask=None, tree_lens=None, seq_l
     [T, ceil(T / 64)] for all requests (bit j of row i: node i sees node j;
     None: a causal chain); tree_lens int32 [B] (None: T nodes each).  The other
     arguments are fd_decode's.  Returns (out fp32 [B, T, Hq, D], lse [B, T, Hq])."""
-    dev, mask, tail, out, lse_out, keep = _tree_args(
-        q, k, v, tree_mask, tree_lens, seq_lens, seq_lens_host, scale, out, lse, workspace, num_ctas, flags,
-        wait_timeout_ns, split_events, dtype, kv_dtype, k_scale, v_scale, None)
-    st = _launch(dev, _lib.fd_tree_decode, _ptr(q), _ptr(k), _ptr(v), *mask, k.shape[1], *tail,
-                 _stream_ptr(stream, dev))
-    if check and st != FD_OK:
-        raise FdError(st, "fd_tree_decode")
-    return out, lse_out
+    return _tree("fd_tree_decode", q, k, v, None, seq_lens, tree_mask, tree_lens, seq_lens_host, scale, out, lse,
+                 workspace, num_ctas, flags, wait_timeout_ns, split_events, stream, check, dtype, kv_dtype, k_scale,
+                 v_scale)
 
 
 def fd_tree_decode_paged(q, k_pages, v_pages, block_table, seq_lens, tree_mask=None, tree_lens=None,
@@ -277,11 +287,6 @@ def fd_tree_decode_paged(q, k_pages, v_pages, block_table, seq_lens, tree_mask=N
     """fd_tree_decode over pages [num_pages, P, Hkv, D] behind block_table int32 [B, max_blocks]."""
     if seq_lens is None or block_table is None:
         raise ValueError("a paged cache needs its block_table and seq_lens")
-    dev, mask, tail, out, lse_out, keep = _tree_args(
-        q, k_pages, v_pages, tree_mask, tree_lens, seq_lens, seq_lens_host, scale, out, lse, workspace, num_ctas,
-        flags, wait_timeout_ns, split_events, dtype, kv_dtype, k_scale, v_scale, block_table)
-    st = _launch(dev, _lib.fd_tree_decode_paged, _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(block_table),
-                 block_table.shape[1], *mask, k_pages.shape[1], k_pages.shape[0], *tail, _stream_ptr(stream, dev))
-    if check and st != FD_OK:
-        raise FdError(st, "fd_tree_decode_paged")
-    return out, lse_out
+    return _tree("fd_tree_decode_paged", q, k_pages, v_pages, block_table, seq_lens, tree_mask, tree_lens,
+                 seq_lens_host, scale, out, lse, workspace, num_ctas, flags, wait_timeout_ns, split_events, stream,
+                 check, dtype, kv_dtype, k_scale, v_scale)
