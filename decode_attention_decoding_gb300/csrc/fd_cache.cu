@@ -18,6 +18,7 @@ namespace {
 struct TablesParams {
     const int32_t *seq_lens, *new_lens, *held_pages, *free_pages, *free_count;
     int max_free, batch, page_size, num_pages, max_blocks, max_tokens;
+    int page_shift;   // page_size = 2^page_shift, or -1
     int32_t *block_table;
     int64_t *slot_map;
     int32_t *cu_new_lens, *seq_lens_out, *held_out, *free_out;
@@ -26,6 +27,11 @@ struct TablesParams {
 
 constexpr int kTablesThreads = 256;
 constexpr int kTablesTokensPerThread = 4;
+// CTAs an SM: more hide the slots' chains of loads, and each scans the lengths
+// once more.  1.6 M tokens of 384 requests: 2, 4, 8, 16 an SM 15.5, 12.1, 14.0,
+// 15.5 us; 512 threads a CTA are slower at either end (64 tokens of 64
+// requests 4.4 -> 4.8 us).
+constexpr int kTablesCtasPerSm = 4;
 
 // Sum of v over the threads before this one, and over all of them in *total.
 template <class T>
@@ -90,120 +96,118 @@ __device__ __forceinline__ int free_page(const TablesParams &p, int count, int o
     return page;
 }
 
-// The last b with prefix[b] <= x, among prefix[0 .. n], prefix[n] > x.
-__device__ __forceinline__ int owner_of(const int *prefix, int n, int x)
-{
-    return request_of_tile(prefix, n, x);
-}
-
 // One launch and no waits between CTAs: every CTA scans the lengths itself
-// (they are a few KB in L2) into two prefix sums in shared memory, new tokens
-// and new pages of the requests before b, and then takes its share of the
-// slots and of the new table entries.  A slot in a new page reads the free
-// stack, not the table entry that another CTA may still have to write.
+// (they are a few KB in L2) into prefix sums in shared memory, new tokens and
+// new pages of the requests before b, beside the requests' lengths and held
+// pages; then it takes its share of the slots and of the new table entries.  A
+// slot in a new page reads the free stack, not the table entry that another CTA
+// may still have to write.  Small calls are one chain of dependent loads; large
+// ones are bound by it too (a search, then a page per slot), hence several
+// independent slots a thread.
 __global__ void __launch_bounds__(kTablesThreads) build_tables_kernel(const __grid_constant__ TablesParams p)
 {
-    extern __shared__ int s_prefix[];
-    int *cu = s_prefix, *pages = s_prefix + p.batch + 1;
+    extern __shared__ int s_req[];
+    int *cu = s_req, *pages = cu + p.batch + 1, *old = pages + p.batch + 1, *held = old + p.batch;
     __shared__ long long s_tmp_l[kTablesThreads / 32];
     __shared__ int s_tmp_i[kTablesThreads / 32];
     const int tid = threadIdx.x;
     const bool first_cta = blockIdx.x == 0;
     const int per = ceil_div(p.batch, kTablesThreads);   // batch <= kMaxBatch
     const int b0 = min(tid * per, p.batch), b1 = min(b0 + per, p.batch);
+    const int count_in = *p.free_count;
     bool bad = false;
 
     long long mine = 0, total_l;
+    for (int b = tid; b < p.batch; b += kTablesThreads) {
+        const TableReq r = table_req(p, b, &bad);
+        old[b] = r.old;
+        held[b] = r.held;
+        cu[b] = r.fresh;   // for now
+    }
+    __syncthreads();
     for (int b = b0; b < b1; ++b)
-        mine += table_req(p, b, &bad).fresh;
-    long long before = block_exclusive_scan(mine, s_tmp_l, &total_l);
+        mine += cu[b];
+    long long at = block_exclusive_scan(mine, s_tmp_l, &total_l);
     bad = bad || total_l > p.max_tokens;
     // tokens past max_tokens do not exist: the prefix stops there
     int need = 0, total_pages;
-    long long at = before;
     for (int b = b0; b < b1; ++b) {
-        const TableReq r = table_req(p, b, &bad);
         const int c0 = (int)min(at, (long long)p.max_tokens);
-        at += r.fresh;
+        at += cu[b];
         const int c1 = (int)min(at, (long long)p.max_tokens);
         cu[b] = c0;
-        need += pages_needed(p, r.old + c1 - c0, r.held);
+        pages[b] = pages_needed(p, old[b] + c1 - c0, held[b]);   // for now
+        need += pages[b];
     }
     const int total_tokens = (int)min(total_l, (long long)p.max_tokens);
     int pg = block_exclusive_scan(need, s_tmp_i, &total_pages);
-    const int count_in = *p.free_count;
     const int count = min(max(count_in, 0), p.max_free);
     bad = bad || count != count_in;
-    at = before;
     for (int b = b0; b < b1; ++b) {
-        bool ignore = false;
-        const TableReq r = table_req(p, b, &ignore);
-        const int c0 = (int)min(at, (long long)p.max_tokens);
-        at += r.fresh;
-        const int c1 = (int)min(at, (long long)p.max_tokens);
-        const int tokens = r.old + c1 - c0;
-        const int n = pages_needed(p, tokens, r.held);
+        const int n = pages[b];
         pages[b] = pg;
-        if (first_cta) {
-            const int granted = min(n, max(0, count - pg));
-            p.cu_new_lens[b] = c0;
-            p.held_out[b] = r.held + granted;
-            p.seq_lens_out[b] = granted < n ? min(tokens, (r.held + granted) * p.page_size) : tokens;
-        }
         pg += n;
     }
     if (tid == 0) {
         cu[p.batch] = total_tokens;
         pages[p.batch] = total_pages;
-        if (first_cta) {
-            p.cu_new_lens[p.batch] = total_tokens;
+    }
+    if (first_cta && bad && p.status)
+        atomicOr(p.status, FD_DEVICE_STATUS_BAD_LENGTH);
+    __syncthreads();
+    if (first_cta) {
+        for (int b = tid; b <= p.batch; b += kTablesThreads) {
+            p.cu_new_lens[b] = cu[b];
+            if (b == p.batch)
+                break;
+            const int n = pages[b + 1] - pages[b], granted = min(n, max(0, count - pages[b]));
+            const int tokens = old[b] + cu[b + 1] - cu[b];
+            p.held_out[b] = held[b] + granted;
+            p.seq_lens_out[b] = granted < n ? min(tokens, (held[b] + granted) * p.page_size) : tokens;
+        }
+        if (tid == 0) {
             p.free_out[0] = max(0, count - total_pages);
             if (p.status && total_pages > count)
                 atomicOr(p.status, FD_DEVICE_STATUS_NO_PAGES);
         }
     }
-    if (first_cta && bad && p.status)
-        atomicOr(p.status, FD_DEVICE_STATUS_BAD_LENGTH);
-    __syncthreads();
 
     const int gthreads = gridDim.x * kTablesThreads, gid = blockIdx.x * kTablesThreads + tid;
     bool bad_page = false;
     // new table entries
     for (long long ord = gid; ord < total_pages; ord += gthreads) {
-        const int b = owner_of(pages, p.batch, (int)ord);
-        bool ignore = false;
-        const TableReq r = table_req(p, b, &ignore);
-        p.block_table[(long long)b * p.max_blocks + r.held + ((int)ord - pages[b])] =
-            free_page(p, count, (int)ord, &bad_page);
+        const int b = request_of_tile(pages, p.batch, (int)ord);
+        p.block_table[(long long)b * p.max_blocks + held[b] + ((int)ord - pages[b])] = free_page(p, count, (int)ord, &bad_page);
     }
     // slots: a warp takes 32 x kTablesTokensPerThread consecutive ones
     const int lane = tid & 31;
     const long long step = (long long)gthreads * kTablesTokensPerThread;
     for (long long w0 = (long long)(gid >> 5) * 32 * kTablesTokensPerThread; w0 < p.max_tokens; w0 += step) {
+        int page[kTablesTokensPerThread], in[kTablesTokensPerThread];
         int b = -1;
-        TableReq r = {0, 0, 0};
 #pragma unroll
         for (int k = 0; k < kTablesTokensPerThread; ++k) {
             const long long i = w0 + 32 * k + lane;
-            if (i >= p.max_tokens)
-                break;
-            long long slot = -1;
+            page[k] = -1;
+            in[k] = 0;
             if (i < total_tokens) {
-                if (b < 0 || i >= cu[b + 1]) {
-                    b = owner_of(cu, p.batch, (int)i);
-                    bool ignore = false;
-                    r = table_req(p, b, &ignore);
-                }
-                const unsigned pos = (unsigned)(r.old + ((int)i - cu[b]));
-                const unsigned blk = pos / (unsigned)p.page_size, in = pos - blk * (unsigned)p.page_size;
-                const int page = (int)blk < r.held ? p.block_table[(long long)b * p.max_blocks + blk]
-                                                   : free_page(p, count, pages[b] + (int)blk - r.held, &bad_page);
-                if ((unsigned)page < (unsigned)p.num_pages)
-                    slot = (long long)page * p.page_size + in;
-                else
-                    bad_page = bad_page || (int)blk < r.held;
+                if (b < 0 || i >= cu[b + 1])
+                    b = request_of_tile(cu, p.batch, (int)i);
+                const unsigned pos = (unsigned)(old[b] + ((int)i - cu[b]));
+                const int blk = (int)(p.page_shift >= 0 ? pos >> p.page_shift : pos / (unsigned)p.page_size);
+                in[k] = (int)(pos - (unsigned)blk * (unsigned)p.page_size);
+                if (blk < held[b]) {
+                    page[k] = p.block_table[(long long)b * p.max_blocks + blk];
+                    bad_page = bad_page || (unsigned)page[k] >= (unsigned)p.num_pages;
+                } else
+                    page[k] = free_page(p, count, pages[b] + blk - held[b], &bad_page);
             }
-            p.slot_map[i] = slot;
+        }
+#pragma unroll
+        for (int k = 0; k < kTablesTokensPerThread; ++k) {
+            const long long i = w0 + 32 * k + lane;
+            if (i < p.max_tokens)
+                p.slot_map[i] = (unsigned)page[k] < (unsigned)p.num_pages ? (long long)page[k] * p.page_size + in[k] : -1;
         }
     }
     if (bad_page && p.status)
@@ -229,14 +233,31 @@ constexpr int kWriteUnitsPerThread = 4;
 
 enum : int { kWriteCopy = 0, kWriteE4m3 = 1, kWriteE5m2 = 2 };
 
-// Four fp32 values to four FP8 codes, nearest even, saturating, NaN kept.
-template <int MODE>
-__device__ __forceinline__ uint32_t quantise4(float2 a, float2 b, float scale)
+// x / scale as IEEE fp32 division rounds it.  FAST: from the rounded reciprocal
+// r of the scale, by one correction (Markstein 1990): q = x r, q + (x - q
+// scale) r with both steps fused is the correctly rounded quotient, for every
+// fp32 scale and every x of up to 11 significant bits (all mantissas of both
+// were tried; the exponents do not matter while nothing under- or overflows,
+// which scales in [2^-60, 2^60] see to for quotients that an FP8 type can tell
+// from 0 and from its largest value).  Quotients past 2^20 are cut to that
+// first, so that infinities reach the end as infinities.
+template <bool FAST>
+__device__ __forceinline__ float quotient(float x, float scale, float r)
 {
-    a.x = __fdiv_rn(a.x, scale);
-    a.y = __fdiv_rn(a.y, scale);
-    b.x = __fdiv_rn(b.x, scale);
-    b.y = __fdiv_rn(b.y, scale);
+    if constexpr (!FAST)
+        return __fdiv_rn(x, scale);
+    const float q = fminf(fmaxf(x * r, -1048576.f), 1048576.f);
+    return copysignf(fmaf(fmaf(-q, scale, x), r, q), x);   // -0 stays -0
+}
+
+// Four fp32 values to four FP8 codes, nearest even, saturating, NaN kept.
+template <int MODE, bool FAST>
+__device__ __forceinline__ uint32_t quantise4(float2 a, float2 b, float scale, float r)
+{
+    a.x = quotient<FAST>(a.x, scale, r);
+    a.y = quotient<FAST>(a.y, scale, r);
+    b.x = quotient<FAST>(b.x, scale, r);
+    b.y = quotient<FAST>(b.y, scale, r);
     if constexpr (MODE == kWriteE4m3)
         return (uint32_t)pack_e4m3x2(a.x, a.y) | ((uint32_t)pack_e4m3x2(b.x, b.y) << 16);
     else
@@ -246,7 +267,7 @@ __device__ __forceinline__ uint32_t quantise4(float2 a, float2 b, float scale)
 // A CTA takes tokens_per_cta tokens of K (blockIdx.y = 0) or V; a unit is 16
 // bytes of the cache row, so every store is a full 16-byte one: 8 elements
 // copied, or 16 elements (two loads) quantised.
-template <int MODE, bool F16>
+template <int MODE, bool F16, bool FAST>
 __global__ void __launch_bounds__(kWriteThreads) cache_write_kernel(const __grid_constant__ WriteParams p)
 {
     const int t0 = blockIdx.x * p.tokens_per_cta;   // < num_tokens: fits an int
@@ -255,7 +276,7 @@ __global__ void __launch_bounds__(kWriteThreads) cache_write_kernel(const __grid
     const int which = blockIdx.y;
     const uint8_t *src = p.src[which];
     uint8_t *dst = p.dst[which];
-    const float scale = p.scale[which];
+    const float scale = p.scale[which], r = __frcp_rn(scale);
     constexpr int kLoads = MODE == kWriteCopy ? 1 : 2;
     for (unsigned u0 = threadIdx.x; u0 < total; u0 += kWriteThreads * kWriteUnitsPerThread) {
         uint4 x[kWriteUnitsPerThread][kLoads];
@@ -284,18 +305,31 @@ __global__ void __launch_bounds__(kWriteThreads) cache_write_kernel(const __grid
                 continue;
             uint4 y = x[k][0];
             if constexpr (MODE != kWriteCopy) {
-                uint32_t r[4];
+                uint32_t y4[4];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const uint4 w = x[k][i];
-                    r[2 * i] = quantise4<MODE>(x2_to_float2<F16>(w.x), x2_to_float2<F16>(w.y), scale);
-                    r[2 * i + 1] = quantise4<MODE>(x2_to_float2<F16>(w.z), x2_to_float2<F16>(w.w), scale);
+                    y4[2 * i] = quantise4<MODE, FAST>(x2_to_float2<F16>(w.x), x2_to_float2<F16>(w.y), scale, r);
+                    y4[2 * i + 1] = quantise4<MODE, FAST>(x2_to_float2<F16>(w.z), x2_to_float2<F16>(w.w), scale, r);
                 }
-                y = make_uint4(r[0], r[1], r[2], r[3]);
+                y = make_uint4(y4[0], y4[1], y4[2], y4[3]);
             }
             *reinterpret_cast<uint4 *>(to[k]) = y;
         }
     }
+}
+
+template <bool FAST>
+void launch_quantise(bool e4m3, bool f16, dim3 grid, cudaStream_t s, const WriteParams &p)
+{
+    if (e4m3 && f16)
+        cache_write_kernel<kWriteE4m3, true, FAST><<<grid, kWriteThreads, 0, s>>>(p);
+    else if (e4m3)
+        cache_write_kernel<kWriteE4m3, false, FAST><<<grid, kWriteThreads, 0, s>>>(p);
+    else if (f16)
+        cache_write_kernel<kWriteE5m2, true, FAST><<<grid, kWriteThreads, 0, s>>>(p);
+    else
+        cache_write_kernel<kWriteE5m2, false, FAST><<<grid, kWriteThreads, 0, s>>>(p);
 }
 
 // ---------------------------------------------------------------- compact
@@ -473,6 +507,7 @@ fd_status fd_build_tables(const int32_t *seq_lens, const int32_t *new_lens, cons
     p.max_free = max_free;
     p.batch = batch;
     p.page_size = page_size;
+    p.page_shift = (page_size & (page_size - 1)) == 0 ? __builtin_ctz((unsigned)page_size) : -1;
     p.num_pages = num_pages;
     p.max_blocks = max_blocks_per_seq;
     p.max_tokens = max_tokens;
@@ -484,8 +519,11 @@ fd_status fd_build_tables(const int32_t *seq_lens, const int32_t *new_lens, cons
     p.free_out = free_count_out;
     p.status = device_status;
     const long long want = pieces(max_tokens, kTablesThreads * kTablesTokensPerThread);
-    const int grid = (int)(want < 1 ? 1 : want > 2 * sms ? 2 * sms : want);
-    const size_t smem = 2 * sizeof(int) * ((size_t)batch + 1);   // at most 32 KB and a bit: no opt-in
+    const int grid = (int)(want < 1 ? 1 : want > kTablesCtasPerSm * sms ? kTablesCtasPerSm * sms : want);
+    const size_t smem = sizeof(int) * (4 * (size_t)batch + 2);
+    if (smem > 48 * 1024 - 256 &&   // beside the kernel's static part: large batches only
+        cudaFuncSetAttribute(build_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        return FD_ERR_CUDA;
     build_tables_kernel<<<grid, kTablesThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(p);
     return cudaGetLastError() == cudaSuccess ? FD_OK : FD_ERR_CUDA;
 }
@@ -530,16 +568,13 @@ fd_status fd_cache_write(const void *k_new, const void *v_new, long long k_strid
     p.tokens_per_cta = p.units >= per_pass ? 1 : per_pass / p.units;
     const dim3 grid((unsigned)pieces(num_tokens, p.tokens_per_cta), 2);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    auto fast = [](float x) { return x >= 0x1p-60f && x <= 0x1p60f; };
     if (kv == FD_KV_AS_Q)
-        cache_write_kernel<kWriteCopy, false><<<grid, kWriteThreads, 0, s>>>(p);
-    else if (kv == FD_KV_FP8_E4M3 && f16)
-        cache_write_kernel<kWriteE4m3, true><<<grid, kWriteThreads, 0, s>>>(p);
-    else if (kv == FD_KV_FP8_E4M3)
-        cache_write_kernel<kWriteE4m3, false><<<grid, kWriteThreads, 0, s>>>(p);
-    else if (f16)
-        cache_write_kernel<kWriteE5m2, true><<<grid, kWriteThreads, 0, s>>>(p);
+        cache_write_kernel<kWriteCopy, false, true><<<grid, kWriteThreads, 0, s>>>(p);
+    else if (fast(p.scale[0]) && fast(p.scale[1]))
+        launch_quantise<true>(kv == FD_KV_FP8_E4M3, f16, grid, s, p);
     else
-        cache_write_kernel<kWriteE5m2, false><<<grid, kWriteThreads, 0, s>>>(p);
+        launch_quantise<false>(kv == FD_KV_FP8_E4M3, f16, grid, s, p);
     return cudaGetLastError() == cudaSuccess ? FD_OK : FD_ERR_CUDA;
 }
 

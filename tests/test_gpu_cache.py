@@ -132,7 +132,7 @@ def test_write_fp8(fd, kv, dtype, n, h, d):
                                    device="cuda").to(k.dtype)   # 17, 19: ties of E4M3 (between 16, 18 and 20) at scale 1
     slots = torch.randperm(n + 9, generator=g, device="cuda")[:n]
     ck, cv = (torch.zeros(n + 9, h, d, device="cuda").to(TYPES[kv]) for _ in range(2))
-    for ks, vs in ((1.0, 0.37), (0.03, 0.02), (0.01234, 3.0)):
+    for ks, vs in ((1.0, 0.37), (0.03, 0.02), (1e-30, 2e30), (2.0 ** -60, 3.3e-7), (0.01234, 3.0)):
         fd.fd_cache_write(k, v, slots, ck, cv, k_scale=ks, v_scale=vs)
         for x, c, s in ((k, ck, ks), (v, cv, vs)):
             want = fp8_quantise(x, s, kv)
