@@ -55,7 +55,8 @@ __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy
 
 // 32 consecutive 32-bit columns of this thread's tensor-memory lane.  The
 // registers are valid after tmem_wait_ld32, which takes them so that no use
-// moves ahead of it.
+// moves ahead of it.  These instructions want the whole warp together: behind
+// code that lanes may take differently stands a __syncwarp.
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32])
 {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
@@ -225,7 +226,8 @@ struct TreeCfg {
     static constexpr int kRawBytes = kN * D;                      // of a tile of FP8 codes
     static constexpr int kQBytes = 128 * D * 2;                   // 128 query rows
     static constexpr int kHalves = kN / 64;                       // of a tile's weights
-    static constexpr int kFlush = kTreeFlush * 128 / kN;          // units between flushes
+    // Units between flushes: with shared rows an accumulator gets 64 positions of a unit, else all of them.
+    static constexpr int kFlush = kTreeFlush, kFlushShared = 2 * kTreeFlush;
     // Registers.  A softmax thread wants some 160, more than an even share of
     // a block with the copying warps, which give some of theirs up (setmaxnreg).
     static constexpr bool kSplitRegs = kGroups == 2 && LOAD != kTreeTma;
@@ -521,13 +523,16 @@ __device__ __forceinline__ void tree_copy(const TreeParams &p, TreeMisc &m, uint
         return __all_sync(0xffffffffu, r) != 0;
     };
     TreeRing rk = {0, 0}, rv = {0, 0}, rr = {0, 0};
-    uint64_t *pending = nullptr;   // the full barrier of a tile whose copies are in flight
+    uint64_t *pending = nullptr;   // the full barrier of a tile whose copies are in flight (the same in every thread)
+    bool starve = LOAD == kTreeCopy && p.starve && blockIdx.x == 0 && tid == 0;
     auto finish = [&]() {
         fence_async_shared();      // the MMAs read what these threads wrote
-        mbar_arrive(smem_addr(pending));
+        if (!starve)               // the test hook leaves out an arrival, so that the first tile never becomes full
+            mbar_arrive(smem_addr(pending));
+        starve = false;
         pending = nullptr;
     };
-    bool ok = true, first = true;
+    bool ok = true;
     TreeWalk<D> w;
     for (w.start(p, m); ok && w.n > 0; w.next(p))
         for (int j = w.j0; ok && j < w.j0 + w.n; ++j) {
@@ -558,18 +563,14 @@ __device__ __forceinline__ void tree_copy(const TreeParams &p, TreeMisc &m, uint
                 } else
                     tree_copy_rows<D, KV>(p, half ? p.v : p.k, w.seg / w.s.groups, w.s.groups == 1, rows, valid, tile,
                                           tid >> 5, tid & 31);
-                // the test hook leaves out an arrival, so that the first tile never becomes full
-                const bool starve = LOAD == kTreeCopy && p.starve && first && blockIdx.x == 0 && tid == 0;
-                first = false;
                 if constexpr (kAsync) {
                     cp_async_commit();
                     if (pending) {
                         cp_async_wait<1>();
                         finish();
                     }
-                    if (!starve)
-                        pending = full;
-                } else if (!starve) {
+                    pending = full;
+                } else {
                     pending = full;
                     finish();
                 }
@@ -674,11 +675,11 @@ __device__ __forceinline__ void tree_mma(const TreeParams &p, TreeMisc &m, uint3
         };
         for (int u = 0; ok && u < ahead && u < units; ++u)
             ok = scores(u);
-        int nth = 0;   // of the accumulator: a unit that starts it, and one after a flush, overwrites
+        int nth = 0;   // of the accumulators: a unit that starts them, and one after a flush, overwrites
         for (int u = 0; ok && u < units; ++u) {
-            const int buf = un.buf(u), acc = C::kGroups == 1 ? 0 : buf;
-            const bool last = un.last_of_tile(u);
-            const uint32_t d = tmem + C::kTmemO + acc * D, a = tmem + buf * C::kN;
+            const int buf = un.buf(u);
+            const bool last = un.last_of_tile(u), halves = active == 0 && C::kGroups == 2;
+            const uint32_t a = tmem + buf * C::kN;
             const uint64_t b = desc_v + ((v_ring + vs * C::kSlotBytes) >> 4);
 #pragma unroll 1
             for (int half = 0; ok && half < C::kHalves; ++half) {
@@ -690,19 +691,21 @@ __device__ __forceinline__ void tree_mma(const TreeParams &p, TreeMisc &m, uint3
                 if (half == 0 && u == 0 && segs > 0 && !(ok = wait(&m.ofree, (segs - 1) & 1)))
                     break;
                 tc_fence_after();
+                // each half has its group's accumulator, or both that of the unit's group
+                const int acc = C::kGroups == 1 ? 0 : halves ? half : buf;
+                const bool fresh = nth == 0 && (halves || half == 0);
                 if (leader) {
-                    const uint32_t ah = a + 64 * half;
+                    const uint32_t d = tmem + C::kTmemO + acc * D, ah = a + 64 * half;
                     const uint64_t bh = b + (uint32_t)(half * 64 * 128 >> 4);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        umma_f16_ts(d, ah + (k / 2) * 32 + (k % 2) * 8, bh + (k * 16 * 128 >> 4), kIdescO, half > 0 || k > 0 || nth > 0);
+                        umma_f16_ts(d, ah + (k / 2) * 32 + (k % 2) * 8, bh + (k * 16 * 128 >> 4), kIdescO, k > 0 || !fresh);
                         umma_f16_ts(d, ah + (k / 2) * 32 + (k % 2) * 8 + 16, bh + (k * 16 * 128 >> 4), kIdescO, true);
                     }
-                    if (half == C::kHalves - 1) {
+                    if (halves || half == C::kHalves - 1)
                         umma_commit(pvdone0 + 8 * acc);
-                        if (last)
-                            umma_commit(vempty0 + 8 * vs);
-                    }
+                    if (last && half == C::kHalves - 1)
+                        umma_commit(vempty0 + 8 * vs);
                 }
                 __syncwarp();
             }
@@ -713,8 +716,8 @@ __device__ __forceinline__ void tree_mma(const TreeParams &p, TreeMisc &m, uint3
                 vs = 0;
                 vph ^= 1u;
             }
-            if (C::kGroups == 1 || ahead == 1 || (u & 1))
-                nth = nth + 1 == C::kFlush ? 0 : nth + 1;
+            if (active != 2 || (u & 1))
+                nth = nth + 1 == (active == 0 ? C::kFlushShared : C::kFlush) ? 0 : nth + 1;
             if (u + ahead < units)
                 ok = scores(u + ahead);
         }
@@ -793,15 +796,15 @@ struct TreeQuery {
     }
 };
 
-// V tile rows from `from` on: those at or past `valid` become zero, and in the
+// V tile rows [from, upto): those at or past `valid` become zero, and in the
 // others (tree nodes) elements that are not finite do, their node marked in bad.
 template <int D, bool F16, int LOAD>
-__device__ __forceinline__ void tree_clean_v(uint32_t tile, int from, int valid, int node0, unsigned int *bad, int tid)
+__device__ __forceinline__ void tree_clean_v(uint32_t tile, int from, int upto, int valid, int node0, unsigned int *bad, int tid)
 {
     using C = TreeCfg<D, LOAD>;
     constexpr int kChunks = D / 8;
     constexpr uint32_t kExp = F16 ? 0x7c00u : 0x7f80u;
-    for (int e = from * kChunks + tid; e < C::kN * kChunks; e += 128) {
+    for (int e = from * kChunks + tid; e < upto * kChunks; e += 128) {
         const int row = e / kChunks, chunk = e % kChunks;
         const uint32_t at = tile + (chunk / 8) * C::kPartBytes + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
         if (row >= valid) {
@@ -894,23 +897,25 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
             up = 0.f;
         }
         const float scale = exp2_approx(up);
+        __syncwarp();
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
             uint32_t o[32];
             tmem_ld32(t_o + 32 * c, o);
             tmem_wait_ld32(o);
-            if (!has_sums)
-                continue;
+            if (has_sums) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                float *at = sums + (long long)(8 * c + k) * p.sum_rows * 4;
-                const float4 x = make_float4(__uint_as_float(o[4 * k]) * scale, __uint_as_float(o[4 * k + 1]) * scale,
-                                             __uint_as_float(o[4 * k + 2]) * scale, __uint_as_float(o[4 * k + 3]) * scale);
-                if (fresh)
-                    *reinterpret_cast<float4 *>(at) = x;
-                else
-                    red_add_v4(at, x);
+                for (int k = 0; k < 8; ++k) {
+                    float *at = sums + (long long)(8 * c + k) * p.sum_rows * 4;
+                    const float4 x = make_float4(__uint_as_float(o[4 * k]) * scale, __uint_as_float(o[4 * k + 1]) * scale,
+                                                 __uint_as_float(o[4 * k + 2]) * scale, __uint_as_float(o[4 * k + 3]) * scale);
+                    if (fresh)
+                        *reinterpret_cast<float4 *>(at) = x;
+                    else
+                        red_add_v4(at, x);
+                }
             }
+            __syncwarp();
         }
         tc_fence_before();
     };
@@ -966,25 +971,28 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
         }
         float mx = kNegInf, l = 0.f;
         int mine = 0;                                // units of this group so far in the segment
-        // own rows: unit 2 j + group (or j); shared: units group, group + 2, ..
-        const int u0 = C::kGroups == 1 || un.active == 1 ? 0 : group;
-        const int step = C::kGroups == 1 || un.active == 1 ? 1 : 2;
-        const int end = un.active == 1 && group == 1 ? 0 : un.units;
+        // own rows: unit 2 j + group (or j), whole tiles; shared: this group's 64 positions of every tile
+        const int u0 = own_rows && un.active == 2 ? group : 0;
+        const int step = own_rows && un.active == 2 ? 2 : 1;
+        const int end = own_rows && un.active == 1 && group == 1 ? 0 : un.units;
+        const int columns = own_rows ? C::kN : 64, col0 = shared_rows ? 64 * group : 0;
+        const int flush_every = own_rows ? C::kFlush : C::kFlushShared;
+        uint64_t *pvdone = &m.pvdone[C::kGroups == 2 ? group : 0];
         for (int u = u0; u < end; u += step, ++mine) {
             const int tile = un.tile(u), buf = un.buf(u);
-            const int t0 = (w.j0 + tile) * C::kN;
-            const uint32_t t_s = t_lane + buf * C::kN;
-            const bool tail = t0 + C::kN > base;
+            const int t0 = (w.j0 + tile) * C::kN + col0;   // the first position of this group's
+            const uint32_t t_s = t_lane + buf * C::kN + col0;
+            const bool tail = t0 + columns > base;
             if (!(ok = wait(&m.sfull[buf], (sph >> buf) & 1u)))
                 break;
             sph ^= 1u << buf;
             tc_fence_after();
-            const bool flush = mine > 0 && mine % C::kFlush == 0;
-            if (C::kGroups == 1 && flush && !(ok = wait(&m.pvdone[0], pvph ^ 1u)))
+            const bool flush = mine > 0 && mine % flush_every == 0;
+            if (!own_rows && flush && !(ok = wait(pvdone, pvph ^ 1u)))
                 break;
             if (flush && warp_live) {
                 tc_fence_after();
-                flush_sums(mine == C::kFlush, mx);
+                flush_sums(mine == flush_every, mx);
             }
             float mx_off = 0.f;
             if (warp_live) {
@@ -1002,10 +1010,11 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
                 };
                 if (tail) {
 #pragma unroll 1
-                    for (int c = 0; c < C::kN / 32; ++c) {
+                    for (int c = 0; c < columns / 32; ++c) {
                         uint32_t s[32];
                         tmem_ld32(t_s + 32 * c, s);
                         const uint32_t bits = live ? tree_bits(p, mask_row, i, t0 + 32 * c - base, t) : 0u;
+                        __syncwarp();
                         tmem_wait_ld32(s);
 #pragma unroll
                         for (int k = 0; k < 32; ++k)
@@ -1015,14 +1024,17 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
                     }
                     tmem_wait_st();
                 } else {
-                    uint32_t s[2][32];
-                    tmem_ld32(t_s, s[0]);
-#pragma unroll
-                    for (int c = 0; c < C::kN / 32; ++c) {
-                        tmem_wait_ld32(s[c & 1]);
-                        if (c + 1 < C::kN / 32)
-                            tmem_ld32(t_s + 32 * (c + 1), s[c + 1 & 1]);
-                        upper(s[c & 1]);
+                    uint32_t s0[32], s1[32];
+                    tmem_ld32(t_s, s0);
+#pragma unroll 1
+                    for (int c = 0; c < columns; c += 64) {
+                        tmem_wait_ld32(s0);
+                        tmem_ld32(t_s + c + 32, s1);
+                        upper(s0);
+                        tmem_wait_ld32(s1);
+                        if (c + 64 < columns)
+                            tmem_ld32(t_s + c + 64, s0);
+                        upper(s1);
                     }
                 }
                 const float tm = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
@@ -1033,12 +1045,12 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
                         mx = tm;
                     l *= corr;
                     if (mine > 0 && !flush) {   // after a flush there is nothing to rescale
-                        // with two groups the score that was waited for follows this
-                        // accumulator's last MMAs; with one, the last unit's may still run
-                        if (C::kGroups == 1 && !(ok = wait(&m.pvdone[0], pvph ^ 1u)))
+                        // with own rows the score that was waited for follows this
+                        // accumulator's last MMAs; with two score buffers the last unit's
+                        // may still run
+                        if (!own_rows && !(ok = wait(pvdone, pvph ^ 1u)))
                             break;
-                        if (C::kGroups == 1)
-                            tc_fence_after();
+                        tc_fence_after();
 #pragma unroll 1
                         for (int c = 0; c < D / 16; ++c) {
                             uint32_t o[16];
@@ -1054,13 +1066,20 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
                 mx_off = kShift - (mx == kNegInf ? 0.f : mx * sl);
             }
             if (tail && (!own_rows || group == 0)) {
-                // this group's tile (with rows of their own: the first group cleans for both)
+                // the V rows of these weights (with own rows the first group cleans for both)
                 const int vs = (vcount + tile) % p.v_slots;
                 if (!(ok = wait(&m.vfull[vs], ((vcount + tile) / p.v_slots) & 1)))
                     break;
-                tree_clean_v<D, F16, LOAD>(v_ring + vs * C::kSlotBytes, max(0, base - t0), L - t0, t0 - base, m.bad[odd], tid);
+                tree_clean_v<D, F16, LOAD>(v_ring + vs * C::kSlotBytes, col0 + max(0, base - t0), col0 + columns,
+                                           L - t0 + col0, t0 - col0 - base, m.bad[odd], tid);
                 fence_async_shared();
+                __syncwarp();
             }
+            // A barrier's phases are told apart by parity alone: each has to be waited
+            // for before the next but one can end.  The last unit's MMAs are waited
+            // for below; those before them here, as long as the last cannot run.
+            if (!own_rows && mine > 0 && u + step >= end && !(ok = wait(pvdone, pvph ^ 1u)))
+                break;
             // The weights, 64 positions at a time: the MMAs of the first half
             // run beside the exponentials of the second.
             const float2 sl2 = make_float2(sl, sl), off2 = make_float2(mx_off, mx_off), one2 = make_float2(1.f, 1.f),
@@ -1084,7 +1103,7 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
                 tmem_st32(t_s + 32 * c, s);
             };
 #pragma unroll 1
-            for (int half = 0; half < C::kHalves; ++half) {
+            for (int half = 0; half < columns / 64; ++half) {
                 if (warp_live) {
                     uint32_t s0[32], s1[32];
                     tmem_ld32(t_s + 64 * half, s0);
@@ -1096,19 +1115,16 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
                     tmem_wait_st();
                 }
                 tc_fence_before();
-                mbar_arrive(smem_addr(&m.pfull[buf][half]));
+                mbar_arrive(smem_addr(&m.pfull[buf][shared_rows ? group : half]));
             }
             l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             pvph ^= 1u;
         }
         if (!ok)
             break;
-        // the accumulator's last MMAs.  With two groups the last score followed
-        // those before; with one the last two may still run, and a barrier is
-        // waited for one phase at a time
-        if (C::kGroups == 1 && mine > 1 && !(ok = wait(&m.pvdone[0], pvph)))
-            break;
-        if (mine > 0 && !(ok = wait(&m.pvdone[C::kGroups == 2 ? group : 0], pvph ^ 1u)))
+        // the accumulator's last MMAs (those before: with own rows the last score
+        // followed them, else they were waited for)
+        if (mine > 0 && !(ok = wait(pvdone, pvph ^ 1u)))
             break;
         tc_fence_after();
         vcount += w.n;
@@ -1118,7 +1134,7 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
             fetch_q(next);
 
         // the segment's result: O / l and the log-sum-exp (base 2), final or partial
-        if (mine > C::kFlush && warp_live) {
+        if (mine > flush_every && warp_live) {
             flush_sums(false, mx);   // the segment's whole sum, relative to ref
             if (mx != kNegInf) {
                 l *= exp2_approx((mx - ref) * sl);
@@ -1130,11 +1146,12 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
             mx = kNegInf;
             l = 0.f;
         }
-        const bool two = shared_rows && w.n > 1;     // the second group had a tile
-        if (shared_rows && (group == 0 || two))
+        if (shared_rows)
             m.ml[group][tid] = make_float2(mx, l);
+        tc_fence_before();
         if (!(ok = pair_sync()))
             break;
+        tc_fence_after();
         // both groups' units are done: the next rows may come, and their scores
         // be formed beside what follows.  (ml of the next segment is written by
         // groups with units, after their MMAs, which wait for ofree.)
@@ -1144,7 +1161,7 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
             store_q(next);
         float a0 = 1.f, a1 = 0.f;
         if (shared_rows) {
-            const float2 x = m.ml[0][tid], y = two ? m.ml[1][tid] : make_float2(kNegInf, 0.f);
+            const float2 x = m.ml[0][tid], y = m.ml[1][tid];
             mx = fmaxf(x.x, y.x);
             a0 = x.x == kNegInf ? 0.f : exp2_approx((x.x - mx) * sl);
             a1 = y.x == kNegInf ? 0.f : exp2_approx((y.x - mx) * sl);
@@ -1160,28 +1177,29 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
         const int slot = 2 * (int)blockIdx.x + (w.j0 > 0 ? 0 : 1);
         const int srow = (own_rows ? group * 128 : 0) + tid;   // row of the partial
         const int c0 = shared_rows ? group * (D / 2) : 0, c1 = shared_rows ? c0 + D / 2 : D;
-        const bool computed = mine > 0 || (shared_rows && w.n > 0);
+        __syncwarp();
         for (int c = c0; c < c1; c += 32) {
             float v[32];
             [[maybe_unused]] uint32_t x[32];
 #pragma unroll
             for (int k = 0; k < 32; ++k)
                 v[k] = 0.f;
-            if (computed && warp_live) {
+            if (mine > 0 && warp_live) {
                 // columns c .. c + 31 of a group's sum: in the workspace once it was flushed
                 auto add = [&](int of, bool flushed, float weight) {
                     if (flushed) {
-                        if (!has_sums)
-                            return;
-                        const float *src = p.ws_sums + (((long long)(blockIdx.x * C::kGroups + of) * (D / 4) + c / 4) * p.sum_rows + tid) * 4;
+                        if (has_sums) {
+                            const float *src = p.ws_sums + (((long long)(blockIdx.x * C::kGroups + of) * (D / 4) + c / 4) * p.sum_rows + tid) * 4;
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const float4 o = __ldcg(reinterpret_cast<const float4 *>(src + (long long)k * p.sum_rows * 4));
-                            v[4 * k] = fmaf(o.x, weight, v[4 * k]);
-                            v[4 * k + 1] = fmaf(o.y, weight, v[4 * k + 1]);
-                            v[4 * k + 2] = fmaf(o.z, weight, v[4 * k + 2]);
-                            v[4 * k + 3] = fmaf(o.w, weight, v[4 * k + 3]);
+                            for (int k = 0; k < 8; ++k) {
+                                const float4 o = __ldcg(reinterpret_cast<const float4 *>(src + (long long)k * p.sum_rows * 4));
+                                v[4 * k] = fmaf(o.x, weight, v[4 * k]);
+                                v[4 * k + 1] = fmaf(o.y, weight, v[4 * k + 1]);
+                                v[4 * k + 2] = fmaf(o.z, weight, v[4 * k + 2]);
+                                v[4 * k + 3] = fmaf(o.w, weight, v[4 * k + 3]);
+                            }
                         }
+                        __syncwarp();
                     } else {
                         tmem_ld32(t_lane + C::kTmemO + of * D + c, x);
                         tmem_wait_ld32(x);
@@ -1191,11 +1209,10 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
                     }
                 };
                 if (shared_rows) {
-                    add(0, (w.n + 1) / 2 > C::kFlush, a0);
-                    if (two)
-                        add(1, w.n / 2 > C::kFlush, a1);
+                    add(0, mine > flush_every, a0);
+                    add(1, mine > flush_every, a1);
                 } else
-                    add(C::kGroups == 1 ? 0 : group, mine > C::kFlush, 1.f);
+                    add(C::kGroups == 1 ? 0 : group, mine > flush_every, 1.f);
 #pragma unroll
                 for (int k = 0; k < 32; ++k)
                     v[k] = any ? v[k] * inv : 0.f;
@@ -1208,6 +1225,7 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
                 for (int k = 0; k < 8; ++k)
                     *reinterpret_cast<float4 *>(dst + k * stride) = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
             }
+            __syncwarp();
         }
         tc_fence_before();
         mbar_arrive(smem_addr(&m.ofree));
