@@ -31,9 +31,10 @@ constexpr int kMaxTreeRows = 4096;   // nodes x query heads of a kv head
 constexpr int kTreeMaxCtas = 256;    // split CTAs (sizes the workspace)
 
 // Cost of a segment start in tiles of the split (below).  Measured on GB300
-// with 2, 3, 5, 8: 16 ragged GQA-4 requests of up to 8192 tokens 75, 70, 66, 70
-// us, 64 of up to 16384 377, 367, 362, 365.
-constexpr int kTreeSegCost = 5;
+// with 3, 4, 5, 7: 16 ragged GQA-4 requests of up to 8192 tokens 74, 70, 72, 73
+// us, 64 of up to 16384 364, 362, 361, 363, one of 2048 tokens 17.7, 17.8, 18.7,
+// 18.7.
+constexpr int kTreeSegCost = 4;
 
 // A scale of 0 becomes this one, so that a hidden score (-inf) keeps its
 // weight of 0; scores below 1e30 are still 0.

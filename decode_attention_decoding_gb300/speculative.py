@@ -9,13 +9,14 @@ fd_cache_compact (include/fd.h).
 
 Like the package's other functions these only check and marshal arguments;
 tensors live on one GPU, outputs are allocated unless they are given.  A call
-runs on that GPU's current stream, whatever device is current.  These calls
-take a few microseconds on the GPU, so the checks are kept to a few attribute
-reads a tensor.
+runs on that GPU's current stream, whatever device is current, or on the
+stream given as `stream=`, which then owns what the call allocates.  These
+calls take a few microseconds on the GPU, so the checks are kept to a few
+attribute reads a tensor.
 """
 from __future__ import annotations
 
-import ctypes
+import functools
 import math
 from typing import NamedTuple
 
@@ -74,17 +75,29 @@ def _status(t, gpu):
     return t.data_ptr()
 
 
-def _launch(gpu, stream, f, *args):
-    """Call f with the stream as its last argument and the call's GPU current (kernels launch on the current one)."""
-    s = torch.cuda.current_stream(gpu).cuda_stream if stream is None else stream.cuda_stream
+def _launch(gpu, f, *args):
+    """Call f with the GPU's current stream as its last argument and the GPU current (kernels launch on the current one)."""
+    s = torch.cuda.current_stream(gpu).cuda_stream
     if torch.cuda.current_device() == gpu:
         return f(*args, s)
     with torch.cuda.device(gpu):
         return f(*args, s)
 
 
+def _on_stream(f):
+    """f(.., stream=s) as f(..) with s current, so that what f allocates belongs to s and is initialised on it."""
+    @functools.wraps(f)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return f(*args, **kw)
+        with torch.cuda.stream(stream):
+            return f(*args, **kw)
+    return call
+
+
+@_on_stream
 def fd_build_tables(seq_lens, new_lens, block_table, free_pages, free_count, page_size, num_pages, max_tokens,
-                    held_pages=None, slot_map=None, device_status=None, stream=None, check=True):
+                    held_pages=None, slot_map=None, device_status=None, check=True):
     """Give requests pages and slots for their new tokens (see fd_build_tables in include/fd.h).
 
     seq_lens, new_lens and held_pages int32 [B]; block_table int32 [B,
@@ -101,7 +114,7 @@ def fd_build_tables(seq_lens, new_lens, block_table, free_pages, free_count, pag
     if free_pages.dim() != 1:
         raise ValueError("free_pages must be 1-d")
     cu, lens, held, left = torch.split_with_sizes(torch.empty(3 * B + 2, dtype=_I32, device=dev), (B + 1, B, B, 1))
-    st = _launch(gpu, stream, _lib.fd_build_tables, _ptr_of(seq_lens, "seq_lens", _I32, per_request, gpu),
+    st = _launch(gpu, _lib.fd_build_tables, _ptr_of(seq_lens, "seq_lens", _I32, per_request, gpu),
                  _ptr_of(new_lens, "new_lens", _I32, per_request, gpu),
                  None if held_pages is None else _ptr_of(held_pages, "held_pages", _I32, per_request, gpu),
                  _ptr_of(free_pages, "free_pages", _I32, free_pages.shape, gpu),
@@ -124,8 +137,9 @@ def _token_rows(t, name, gpu):
     return token
 
 
+@_on_stream
 def fd_cache_write(k_new, v_new, slot_map, k_cache, v_cache, kv_dtype=None, k_scale=1.0, v_scale=1.0,
-                   device_status=None, stream=None, check=True):
+                   device_status=None, check=True):
     """Write new K/V rows into the cache's slots (see fd_cache_write in include/fd.h).
 
     k_new, v_new bf16 or fp16 [n, Hkv, D], any token stride that is a multiple
@@ -144,15 +158,16 @@ def fd_cache_write(k_new, v_new, slot_map, k_cache, v_cache, kv_dtype=None, k_sc
     if kv == 0 and (k_cache.dtype is not k_new.dtype or v_cache.dtype is not k_new.dtype):
         raise TypeError("a 16-bit cache must be of the new rows' type")
     opts = FdOptions(0, 0, 0, None, None, 1 if k_new.dtype is _F16 else 0, kv, k_scale, v_scale, 1)
-    st = _launch(gpu, stream, _lib.fd_cache_write, k_new.data_ptr(), v_new.data_ptr(), ks, vs,
+    st = _launch(gpu, _lib.fd_cache_write, k_new.data_ptr(), v_new.data_ptr(), ks, vs,
                  _ptr_of(slot_map, "slot_map", _I64, (n,), gpu), n, h, d, k_cache.data_ptr(), v_cache.data_ptr(),
                  k_cache.numel() // (h * d) if h * d else 0, opts, _status(device_status, gpu))
     if check and st != FD_OK:
         raise FdError(st, "fd_cache_write")
 
 
+@_on_stream
 def fd_cache_compact(k_cache, v_cache, seq_lens, accepted, accept_lens, tree_len, block_table=None, tree_lens=None,
-                     seq_lens_out=None, device_status=None, stream=None, check=True):
+                     seq_lens_out=None, device_status=None, check=True):
     """Move the accepted path's rows to the front of the drafted tail, in place
     (see fd_cache_compact in include/fd.h).
 
@@ -182,7 +197,7 @@ def fd_cache_compact(k_cache, v_cache, seq_lens, accepted, accept_lens, tree_len
         seq_lens_out = torch.empty_like(seq_lens)
     most = accepted.shape[1]
     opts = FdOptions(0, 0, 0, None, None, 0, 1 if size == 1 else 0, 0.0, 0.0, 1)
-    st = _launch(gpu, stream, _lib.fd_cache_compact, k_cache.data_ptr(), v_cache.data_ptr(), table, blocks, page, pages,
+    st = _launch(gpu, _lib.fd_cache_compact, k_cache.data_ptr(), v_cache.data_ptr(), table, blocks, page, pages,
                  _ptr_of(seq_lens, "seq_lens", _I32, per_request, gpu),
                  None if tree_lens is None else _ptr_of(tree_lens, "tree_lens", _I32, per_request, gpu), int(tree_len),
                  _ptr_of(accepted, "accepted", _I32, (B, most), gpu),
@@ -209,7 +224,7 @@ def make_tree_workspace(batch, tree_len, num_q_heads, num_kv_heads, head_dim=128
 
 
 def _tree(name, q, k, v, block_table, seq_lens, tree_mask, tree_lens, seq_lens_host, scale, out, lse, workspace, num_ctas,
-          flags, wait_timeout_ns, split_events, stream, check, dtype, kv_dtype, k_scale, v_scale):
+          flags, wait_timeout_ns, split_events, check, dtype, kv_dtype, k_scale, v_scale):
     """Both layouts: checks, outputs, and the call `name`."""
     gpu = _gpu(q, "q")
     if q.dim() != 4 or not q.is_contiguous() or q.element_size() != 2:
@@ -253,7 +268,7 @@ def _tree(name, q, k, v, block_table, seq_lens, tree_mask, tree_lens, seq_lens_h
         if host.numel() != B:
             raise ValueError(f"seq_lens_host must hold {B} lengths")
     opts = _options(num_ctas, flags, wait_timeout_ns, split_events, _dtype_code(q, dtype), kv, k_scale, v_scale, 1)
-    st = _launch(gpu, stream, getattr(_lib, name), q.data_ptr(), k.data_ptr(), v.data_ptr(), *layout, mask, stride,
+    st = _launch(gpu, getattr(_lib, name), q.data_ptr(), k.data_ptr(), v.data_ptr(), *layout, mask, stride,
                  None if tree_lens is None else _ptr_of(tree_lens, "tree_lens", _I32, per_request, gpu),
                  None if seq_lens is None else _ptr_of(seq_lens, "seq_lens", _I32, per_request, gpu),
                  None if host is None else host.data_ptr(), B, T, hq, hkv, d, page, *((pages,) if layout else ()),
@@ -265,9 +280,10 @@ def _tree(name, q, k, v, block_table, seq_lens, tree_mask, tree_lens, seq_lens_h
     return out, lse
 
 
+@_on_stream
 def fd_tree_decode(q, k, v, seq_lens=None, tree_mask=None, tree_lens=None, seq_lens_host=None, scale=None, out=None,
-                   lse=None, workspace=None, num_ctas=0, flags=0, wait_timeout_ns=0, split_events=None, stream=None,
-                   check=True, dtype=None, kv_dtype=None, k_scale=1.0, v_scale=1.0):
+                   lse=None, workspace=None, num_ctas=0, flags=0, wait_timeout_ns=0, split_events=None, check=True,
+                   dtype=None, kv_dtype=None, k_scale=1.0, v_scale=1.0):
     """Attention of a drafted tree over a contiguous cache (see fd_tree_decode in include/fd.h).
 
     q [B, T, Hq, D]; k/v [B, S, Hkv, D] with the T nodes as the last positions
@@ -276,17 +292,17 @@ def fd_tree_decode(q, k, v, seq_lens=None, tree_mask=None, tree_lens=None, seq_l
     None: a causal chain); tree_lens int32 [B] (None: T nodes each).  The other
     arguments are fd_decode's.  Returns (out fp32 [B, T, Hq, D], lse [B, T, Hq])."""
     return _tree("fd_tree_decode", q, k, v, None, seq_lens, tree_mask, tree_lens, seq_lens_host, scale, out, lse,
-                 workspace, num_ctas, flags, wait_timeout_ns, split_events, stream, check, dtype, kv_dtype, k_scale,
-                 v_scale)
+                 workspace, num_ctas, flags, wait_timeout_ns, split_events, check, dtype, kv_dtype, k_scale, v_scale)
 
 
+@_on_stream
 def fd_tree_decode_paged(q, k_pages, v_pages, block_table, seq_lens, tree_mask=None, tree_lens=None,
                          seq_lens_host=None, scale=None, out=None, lse=None, workspace=None, num_ctas=0, flags=0,
-                         wait_timeout_ns=0, split_events=None, stream=None, check=True, dtype=None, kv_dtype=None,
+                         wait_timeout_ns=0, split_events=None, check=True, dtype=None, kv_dtype=None,
                          k_scale=1.0, v_scale=1.0):
     """fd_tree_decode over pages [num_pages, P, Hkv, D] behind block_table int32 [B, max_blocks]."""
     if seq_lens is None or block_table is None:
         raise ValueError("a paged cache needs its block_table and seq_lens")
     return _tree("fd_tree_decode_paged", q, k_pages, v_pages, block_table, seq_lens, tree_mask, tree_lens,
-                 seq_lens_host, scale, out, lse, workspace, num_ctas, flags, wait_timeout_ns, split_events, stream,
-                 check, dtype, kv_dtype, k_scale, v_scale)
+                 seq_lens_host, scale, out, lse, workspace, num_ctas, flags, wait_timeout_ns, split_events, check,
+                 dtype, kv_dtype, k_scale, v_scale)

@@ -437,6 +437,8 @@ fd_status fd_decode_noalloc(const void *q, const void *k, const void *v,
  *   - device_status: NULL, or a device uint32 into which a call ORs its
  *     FD_DEVICE_STATUS_* bits, stream-ordered (the caller zeroes it).
  *   - The stream must belong to the current device, as for every call here.
+ *   - Calls may be captured in a graph and replayed: lengths, tables, masks and
+ *     paths are read on the device, and slots of -1 pad a fixed batch.
  *   - Inputs and outputs of one call must not overlap unless an argument says so.
  */
 
@@ -539,8 +541,10 @@ fd_status fd_cache_compact(void *k_cache, void *v_cache, const int32_t *block_ta
                            const fd_options *opts, unsigned int *device_status, fd_stream_t stream);
 
 /* Bytes of workspace that fd_tree_decode / fd_tree_decode_paged need for a
- * shape; initialise it once with fd_workspace_init.  Pure host function; 0 for
- * shapes that no call accepts. */
+ * shape (the CTAs' partial outputs and running sums, whatever the lengths: up
+ * to 101 MB for more than 128 query rows a kv head); initialise it once with
+ * fd_workspace_init.  A workspace of one shape serves every smaller one.  Pure
+ * host function; 0 for shapes that no call accepts. */
 size_t fd_tree_workspace_size(int batch, int tree_len, int num_q_heads, int num_kv_heads, int head_dim);
 
 /*
@@ -569,9 +573,13 @@ size_t fd_tree_workspace_size(int batch, int tree_len, int num_q_heads, int num_
  *                LSE = -inf.
  *   workspace    at least fd_tree_workspace_size(...) bytes, as for fd_decode (its
  *                error word is read with fd_get_device_error).
- *   opts         as for fd_decode; q_len must be 0 or 1 (tree_len replaces it).
- *                No user flag changes the call.
+ *   opts         as for fd_decode; num_ctas is at most 256, q_len must be 0 or 1
+ *                (tree_len replaces it), and no user flag changes the call.
  *   The other arguments are fd_decode's.
+ * Runs on the tcgen05 tensor cores with fp32 scores, sums and accumulation; each
+ * softmax weight is taken as a 16-bit part plus its 16-bit remainder.  Results
+ * are bitwise the same from call to call (with the same num_ctas).  The first
+ * call of a shape on a device sets a kernel attribute: make it before a capture.
  * Any whole group Hq/Hkv; tree_len 1 .. 256; tree_len * Hq/Hkv <= 4096; batch
  * <= 4096; head_dim 64, 128 or 256; bf16, fp16 or FP8 caches.  What the cache
  * holds at positions that no row sees (behind L_b, nodes without a set bit in

@@ -109,7 +109,9 @@ def tree_attention(q, k, v, vis, lens, trees, scale, v_scale=1.0):
     rounding of its argument (|s - m| 2^-23 and 2^-22 of the function) and,
     where it is taken in two bf16 parts, by 2^-8 2^-8.  Sums over n positions
     add n 2^-23 relatively to sum p |v|, twice (O and the normalising sum),
-    and merging adds a few steps."""
+    and merging adds a few steps.  A weight in fp16 parts, 2^8 times itself,
+    ends at half of fp16's least step, 2^-25: below 2^-33 of the row's largest
+    weight it may be lost whole, which adds 2^-33 sum |v|."""
     B, T, hq, D = q.shape
     hkv = k[0].shape[1]
     G = hq // hkv
@@ -138,7 +140,7 @@ def tree_attention(q, k, v, vis, lens, trees, scale, v_scale=1.0):
                     lse[b, i, h] = m + np.log(l)
                     o[b, i, h] = p @ vv / l * v_scale
                     rel = 2 * es + 2.0 ** -16 + 2.0 ** -21 + (m - s[np.isfinite(s)].min()) * 2.0 ** -22 + (2 * n + 64) * 2.0 ** -23
-                    eo[b, i, h] = 2 * rel * (p @ np.abs(vv) / l) * abs(v_scale)
+                    eo[b, i, h] = (2 * rel * (p @ np.abs(vv) / l) + 2.0 ** -33 * np.abs(vv).sum(0)) * abs(v_scale)
                     el[b, i, h] = 2 * rel + abs(lse[b, i, h]) * 2.0 ** -21
     return o, lse, eo, el
 

@@ -77,3 +77,131 @@ def test_loop(fd, kv, page):
                 ref[b][i] = np.concatenate([ref[b][i][:base], ref[b][i][[base + x for x in p]]])
     assert int(status) == 0 and fd.fd_get_device_error(ws) == fd.FD_OK
     assert int(free_count) == pages - sum(held.tolist())   # no page was lost
+
+
+def state(kv, seed=0, B=3, T=9, hq=8, hkv=2, D=128, page=16, pages=64):
+    """What a program keeps between steps, and one step over it: all four calls, into given buffers."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    rng = np.random.default_rng(seed)
+    kt = TYPES["bf16" if kv == "same" else kv]
+    s = dict(k=torch.randn(pages, page, hkv, D, generator=g, device="cuda").to(kt),
+             v=torch.randn(pages, page, hkv, D, generator=g, device="cuda").to(kt),
+             table=torch.full((B, 24), -1, dtype=torch.int32, device="cuda"), free=i32(rng.permutation(pages).tolist()),
+             count=i32([pages]), lens=i32([0] * B), held=i32([0] * B), new=i32([100, 17, 260]),
+             kv_new=torch.randn(B, T, 2 * hkv, D, generator=g, device="cuda").to(torch.bfloat16),
+             prompt=torch.randn(377, 2 * hkv, D, generator=g, device="cuda").to(torch.bfloat16),
+             q=torch.randn(B, T, hq, D, generator=g, device="cuda").to(torch.bfloat16),
+             path=i32([[0, 3, 5], [1, 2, 8], [4, 0, 0]]), npath=i32([3, 2, 1]), status=i32([0]), T=T, page=page, pages=pages, hkv=hkv)
+    vis = np.stack([tree_visibility(random_tree(rng, T)) for _ in range(B)])
+    s["mask"] = torch.from_numpy(pack_mask(vis).view(np.int64)).cuda()
+    return s
+
+
+def step(fd, s, ws):
+    """Append T drafted rows to every request, attend, keep a path; the state's lengths, pages and stack move on."""
+    h, B = s["hkv"], s["lens"].shape[0]
+    scales = dict(k_scale=0.02, v_scale=0.03) if s["k"].element_size() == 1 else {}
+    t = fd.fd_build_tables(s["lens"], s["new"], s["table"], s["free"], s["count"], s["page"], s["pages"], B * s["T"],
+                           held_pages=s["held"], device_status=s["status"])
+    rows = s["kv_new"].view(B * s["T"], 2 * h, -1)
+    fd.fd_cache_write(rows[:, :h], rows[:, h:], t.slot_map, s["k"], s["v"], device_status=s["status"], **scales)
+    out, lse = fd.fd_tree_decode_paged(s["q"], s["k"], s["v"], s["table"], t.seq_lens, s["mask"], workspace=ws, **scales)
+    lens = fd.fd_cache_compact(s["k"], s["v"], t.seq_lens, s["path"], s["npath"], s["T"], block_table=s["table"],
+                               device_status=s["status"])
+    for name, x in (("lens", lens), ("held", t.held_pages), ("count", t.free_count)):
+        s[name].copy_(x)
+    return out, lse
+
+
+def prefill(fd, s):
+    """The prompts, by the same calls."""
+    h = s["hkv"]
+    scales = dict(k_scale=0.02, v_scale=0.03) if s["k"].element_size() == 1 else {}
+    t = fd.fd_build_tables(s["lens"], s["new"], s["table"], s["free"], s["count"], s["page"], s["pages"], 377,
+                           held_pages=s["held"])
+    fd.fd_cache_write(s["prompt"][:, :h], s["prompt"][:, h:], t.slot_map, s["k"], s["v"], **scales)
+    for name, x in (("lens", t.seq_lens), ("held", t.held_pages), ("count", t.free_count)):
+        s[name].copy_(x)
+    s["new"].fill_(s["T"])
+
+
+def same(a, b):
+    return torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+
+
+@pytest.mark.parametrize("kv", ["same", "e4m3"])
+def test_captured_step_replays_as_eager_steps(fd, kv):
+    """A step captured once and replayed gives bit for bit what eager steps give, with new rows each time."""
+    a, b = state(kv), state(kv)
+    ws_a, ws_b = (fd.make_tree_workspace(3, 9, 8, 2) for _ in range(2))
+    for s in (a, b):
+        prefill(fd, s)
+    eager = []
+    for n in range(4):
+        a["kv_new"].mul_(-1)
+        a["q"].add_(0.25)
+        out, lse = step(fd, a, ws_a)
+        eager.append((out.clone(), lse.clone()))
+    side = state(kv, seed=1)   # a first call of each shape outside the capture
+    prefill(fd, side)
+    step(fd, side, ws_b)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = step(fd, b, ws_b)
+    for n in range(4):
+        b["kv_new"].mul_(-1)
+        b["q"].add_(0.25)
+        graph.replay()
+        assert same(out, eager[n][0]) and same(lse, eager[n][1]), n
+    for name in ("k", "v", "table", "lens", "held", "count", "status"):
+        assert same(a[name], b[name]), name
+    assert int(a["status"]) == 0
+
+
+def test_two_graphs_share_a_workspace_in_order(fd):
+    """Graphs of different shapes replayed in turn on one workspace (of the larger shape), and on other streams."""
+    c = [dict(q=torch.randn(2, T, 8, 128, device="cuda").half(), k=torch.randn(2, 700, 2, 128, device="cuda").half(),
+              lens=i32([700, 90])) for T in (5, 50)]
+    ws = fd.make_tree_workspace(2, 50, 8, 2)
+    want_ = [fd.fd_tree_decode(x["q"], x["k"], x["k"], x["lens"]) for x in c]
+    graphs, outs = [], []
+    for x in c:
+        fd.fd_tree_decode(x["q"], x["k"], x["k"], x["lens"], workspace=ws)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(fd.fd_tree_decode(x["q"], x["k"], x["k"], x["lens"], workspace=ws))
+        graphs.append(g)
+    for _ in range(5):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for (o, l), (wo, wl) in zip(outs, want_):
+        assert same(o, wo) and same(l, wl)
+
+
+def test_concurrent_streams_with_their_own_workspaces(fd):
+    q, k, lens = torch.randn(4, 20, 8, 128, device="cuda").half(), torch.randn(4, 3000, 2, 128, device="cuda").half(), i32([3000, 5, 777, 2000])
+    want_ = fd.fd_tree_decode(q, k, k, lens)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = []
+    for n in range(12):   # each call's outputs and workspace belong to its stream
+        got.append(fd.fd_tree_decode(q, k, k, lens, stream=streams[n % 3]))
+    torch.cuda.synchronize()
+    for o, l in got:
+        assert same(o, want_[0]) and same(l, want_[1])
+    with torch.cuda.stream(streams[0]):
+        o, l = fd.fd_tree_decode(q, k, k, lens)
+    streams[0].synchronize()
+    assert same(o, want_[0])
+
+
+def test_repeated_calls_are_bitwise_equal(fd):
+    q = torch.randn(2, 40, 16, 128, device="cuda").to(torch.bfloat16)
+    k = torch.randn(2, 9000, 2, 128, device="cuda").to(torch.bfloat16)
+    lens = i32([9000, 6000])
+    first = fd.fd_tree_decode(q, k, k, lens)
+    for _ in range(20):
+        o, l = fd.fd_tree_decode(q, k, k, lens)
+        assert same(o, first[0]) and same(l, first[1])

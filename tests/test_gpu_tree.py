@@ -236,3 +236,54 @@ def test_a_starved_wait_times_out_and_the_context_survives(fd, page, kv, T, D):
     assert fd.fd_get_device_error(ws) == fd.FD_ERR_TIMEOUT
     check_tree(*run(fd, c, 0.1, workspace=ws, num_ctas=4), want(c, 0.1))
     assert fd.fd_get_device_error(ws) == fd.FD_OK
+
+
+@pytest.mark.parametrize("page,kv", [(16, "same"), (4, "same"), (16, "e4m3"), (2, "e4m3")])
+def test_pages_past_32_bit_offsets(fd, page, kv):
+    """Pages whose element offsets pass 2^32 (a pool of 2.3 M slots x 8 heads x 256)."""
+    from spec_util import TYPES
+    hkv, D, slots = 8, 256, 2300 * 1024
+    pages = slots // page
+    kt = TYPES["bf16" if kv == "same" else kv]
+    pool = [torch.zeros(pages, page, hkv, D, dtype=torch.uint8 if kv != "same" else torch.int16, device="cuda").view(kt) for _ in range(2)]
+    c = make_tree_case(30, 2, 6, 16, hkv, D, [70, 33], kv=kv)
+    need = [-(-n // page) for n in c["lens"]]
+    table = torch.zeros(2, max(need), dtype=torch.int32)
+    at = pages - sum(need)                  # the pool's last pages
+    for b in range(2):
+        for j in range(need[b]):
+            table[b, j] = at
+            n = min(page, c["lens"][b] - j * page)
+            for t, x in zip(pool, (c["k"], c["v"])):
+                view = torch.uint8 if kv != "same" else torch.int16
+                t.view(view)[at, :n] = x.view(view)[b, j * page:j * page + n].cuda()
+            at += 1
+    mask = torch.from_numpy(pack_mask(c["vis"]).view(np.int64)).cuda()
+    got = fd.fd_tree_decode_paged(c["q"].cuda(), *pool, table.cuda(), i32(c["lens"]), mask, scale=0.06)
+    check_tree(*got, want(c, 0.06))
+
+
+def test_largest_trees_and_groups(fd):
+    """256 nodes; 4096 query rows of one kv head."""
+    c = make_tree_case(31, 1, 256, 2, 1, 64, [300])
+    check_tree(*run(fd, c, 0.1), want(c, 0.1))
+    c = make_tree_case(32, 1, 64, 64, 1, 64, [200], dtype="f16")
+    check_tree(*run(fd, c, 0.1), want(c, 0.1))
+
+
+def test_fp8_rows_of_every_magnitude(fd):
+    """FP8 caches take a bf16 query as fp16 rows over a power of two: rows from 2^-100 to 2^100, zero rows, mixed rows."""
+    c = make_tree_case(33, 2, 8, 4, 2, 128, [200, 70], kv="e4m3")
+    powers = torch.tensor([-100, -30, 0, 20, 60, 100, -126, 8], dtype=torch.float32)
+    q = c["q"].float() * torch.exp2(powers)[None, :, None, None]
+    q[:, 3, 1] = 0
+    q[:, 7, :, ::2] *= 2.0 ** -20
+    for scale_power in (0, -100, 100):       # the scale brings some of them near 1
+        c["q"] = (q / 4).to(torch.bfloat16)
+        c["q64"] = c["q"].double().numpy()
+        scale = 2.0 ** scale_power
+        w = want(c, scale)
+        rows = [i for i in range(8) if np.isfinite(w[2][:, i]).all() and np.abs(w[1][:, i]).max() < 1e4]
+        got = run(fd, c, scale)
+        assert rows
+        check_tree(got[0][:, rows], got[1][:, rows], tuple(x[:, rows] for x in w))
