@@ -287,3 +287,18 @@ def test_fp8_rows_of_every_magnitude(fd):
         got = run(fd, c, scale)
         assert rows
         check_tree(got[0][:, rows], got[1][:, rows], tuple(x[:, rows] for x in w))
+
+
+@pytest.mark.parametrize("kv,page,T", [("e4m3", 0, 12), ("e4m3", 16, 50), ("e5m2", 4, 12)])
+def test_fp8_codes_that_are_no_numbers_in_masked_places(fd, kv, page, T):
+    c = make_tree_case(34, 2, T, 8, 2, 128, [140, 400], kv=kv, page=page)
+    for b, L in enumerate(c["lens"]):
+        pos = L - T + T // 2                  # seen by its descendants and itself
+        at = (int(c["block_table"][b, pos // page]), pos % page) if page else (b, pos)
+        for name in ("k", "v"):
+            c[name].view(torch.uint8)[at[0], at[1], 1, 3::7] = 0x7F   # NaN in both types
+            c[name + "64"][b][pos, 1, 3::7] = float("nan")
+        if kv == "e5m2":                      # and an infinity that few see
+            c["v"].view(torch.uint8)[at[0], at[1], 0, 5] = 0x7C
+            c["v64"][b][pos, 0, 5] = float("inf")
+    check_tree(*run(fd, c, 0.1), want(c, 0.1))
