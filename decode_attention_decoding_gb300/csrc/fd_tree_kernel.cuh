@@ -83,6 +83,28 @@ __device__ __forceinline__ void tmem_wait_ld32(uint32_t (&r)[32])
                  :
                  : "memory");
 }
+// The same 32 columns and, per lane, the largest of them that is a number (NaN
+// if none is).  Of a tile's 64 columns that takes 87 cycles with two warps a
+// scheduler, and 257 with the maximum formed by three-way instructions.
+__device__ __forceinline__ float tmem_ld32_max(uint32_t addr, uint32_t (&r)[32])
+{
+    float m;
+    asm volatile("tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, %32, [%33];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+                   "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+                   "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+                   "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=f"(m)
+                 : "r"(addr)
+                 : "memory");
+    return m;
+}
+__device__ __forceinline__ void tmem_wait_max(float &a, float &b)
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(a), "+f"(b) : : "memory");
+}
 __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32])
 {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
@@ -170,6 +192,24 @@ __device__ __forceinline__ void cp_async_wait()
 __device__ __forceinline__ void red_add_v4(float *at, float4 x)
 {
     asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(at), "f"(x.x), "f"(x.y), "f"(x.z), "f"(x.w) : "memory");
+}
+
+// x minus the packed 16-bit pair w, exact when w is x rounded.
+template <bool F16>
+__device__ __forceinline__ float2 minus_x2(float2 x, uint32_t w)
+{
+    float2 r;
+    if constexpr (F16)
+        asm("{\n\t.reg .b16 lo, hi, m;\n\tmov.b32 {lo, hi}, %2;\n\tmov.b16 m, 0xBC00;\n\t"
+            "fma.rn.f32.f16 %0, lo, m, %3;\n\tfma.rn.f32.f16 %1, hi, m, %4;\n\t}"
+            : "=f"(r.x), "=f"(r.y)
+            : "r"(w), "f"(x.x), "f"(x.y));
+    else
+        asm("{\n\t.reg .b16 lo, hi, m;\n\tmov.b32 {lo, hi}, %2;\n\tmov.b16 m, 0xBF80;\n\t"
+            "fma.rn.f32.bf16 %0, lo, m, %3;\n\tfma.rn.f32.bf16 %1, hi, m, %4;\n\t}"
+            : "=f"(r.x), "=f"(r.y)
+            : "r"(w), "f"(x.x), "f"(x.y));
+    return r;
 }
 
 // True in one lane of the (converged) warp.
@@ -598,28 +638,26 @@ __device__ __forceinline__ void tree_copy(const TreeParams &p, TreeMisc &m, uint
     __syncwarp();
 }
 
+// Groups with rows of their own in segment w; 0: both (or the only one) have the same rows.
+template <int D>
+__device__ __forceinline__ int tree_active(const TreeParams &p, const TreeWalk<D> &w)
+{
+    return p.rows == 128 ? 0 : (w.seg % w.s.groups) * 256 + 128 < w.r.t * p.group ? 2 : 1;
+}
+
 // How the MMAs of a segment follow one another.  With the same rows in both
 // groups (or one group) unit u is tile u, in score buffer u & 1; with rows of
-// their own, tile u / active for group u % active.
+// their own, tile u / active for group u % active, each with a buffer.  (An
+// issuer for each of the two groups, so that neither waits for the other's
+// weights: 64 nodes x 8 heads over 4 x 32768 positions 337 us instead of 297.
+// The groups then fall into step and the tensor core waits for both at once.)
 struct TreeUnits {
-    int active;   // groups with rows of their own: 0 = one set of rows
-    int units;
-    __device__ __forceinline__ int tile(int u) const { return active == 2 ? u >> 1 : u; }
+    int active;
     __device__ __forceinline__ int buf(int u) const { return active == 1 ? 0 : u & 1; }
     __device__ __forceinline__ int ahead() const { return active == 1 ? 1 : 2; }
     __device__ __forceinline__ bool last_of_tile(int u) const { return active != 2 || (u & 1); }
     __device__ __forceinline__ bool first_of_tile(int u) const { return active != 2 || !(u & 1); }
 };
-template <int D>
-__device__ __forceinline__ TreeUnits tree_units(const TreeParams &p, const TreeWalk<D> &w)
-{
-    TreeUnits u;
-    u.active = 0;
-    if (p.rows == 256)
-        u.active = (w.seg % w.s.groups) * 256 + 128 < w.r.t * p.group ? 2 : 1;
-    u.units = u.active == 2 ? 2 * w.n : w.n;
-    return u;
-}
 
 // The MMA issuer: one warp, whose lanes all run the loop (so that addresses and
 // descriptors stay in uniform registers) and whose elected lane issues.
@@ -645,8 +683,9 @@ __device__ __forceinline__ void tree_mma(const TreeParams &p, TreeMisc &m, uint3
     TreeWalk<D> w;
     bool ok = true;
     for (w.start(p, m); ok && w.n > 0; w.next(p), ++segs) {
-        const TreeUnits un = tree_units<D>(p, w);
-        const int active = un.active, ahead = un.ahead(), units = un.units;
+        const int active = tree_active<D>(p, w), units = active == 2 ? 2 * w.n : w.n;
+        const TreeUnits un = {active};
+        const int ahead = un.ahead();
         if (!(ok = wait(&m.qfull, segs & 1)))
             break;
         tc_fence_after();
@@ -854,6 +893,12 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
     // fp16 weights: 2^8 more keeps weights down to 2^-33 of the largest among
     // the 16-bit parts (fp16 ends at 2^-25), and 2^7 of slack ends at 2^15.
     constexpr float kShift = F16 ? 8.f : 0.f, kSlack = F16 ? 7.f : 8.f;
+    // A weight's remainder by fused instructions that take the 16-bit part as it
+    // is, or widened first, which is two instructions more a pair on another
+    // pipe.  The first way costs 67.8 us instead of 69.7 for 16 ragged requests,
+    // 293 instead of 298 for 512 rows, 275 instead of 280 for 4-token pages; but
+    // 203 instead of 200 beside the converting warps, and 141 instead of 137 for 64 dims.
+    constexpr bool kMixed = D > 64 && !kv_is_fp8(KV);
     constexpr float kNegInf = -__builtin_huge_valf();
     const int tid = threadIdx.x & 127, group = threadIdx.x >> 7, lane_base = (threadIdx.x >> 5 & 3) << 5;
     volatile int *abort_flag = &m.abort;
@@ -958,7 +1003,6 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
     }
     int odd = 0;   // segments, modulo 2
     while (w.n > 0) {
-        const TreeUnits un = tree_units<D>(p, w);
         const int L = w.r.L, t = w.r.t, base = L - t;
         const int row = (w.seg % w.s.groups) * p.rows + (own_rows ? group * 128 : 0) + tid;
         const int i = row / p.group, h = row - i * p.group;
@@ -972,44 +1016,40 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
             sl = fmaxf(p.scale_log2 * __int_as_float((127 + m.power[group][tid]) << 23), kTreeLeastScale);
         }
         float mx = kNegInf, l = 0.f;
-        int mine = 0;                                // units of this group so far in the segment
-        // own rows: unit 2 j + group (or j), whole tiles; shared: this group's 64 positions of every tile
-        const int u0 = own_rows && un.active == 2 ? group : 0;
-        const int step = own_rows && un.active == 2 ? 2 : 1;
-        const int end = own_rows && un.active == 1 && group == 1 ? 0 : un.units;
+        int since = 0;                               // units since the start or the last flush
+        bool flushed = false;
+        // own rows: whole tiles; shared: this group's 64 positions of every tile
+        const int end = own_rows && group >= tree_active<D>(p, w) ? 0 : w.n;
         const int columns = own_rows ? C::kN : 64, col0 = shared_rows ? 64 * group : 0;
         const int flush_every = own_rows ? C::kFlush : C::kFlushShared;
         uint64_t *pvdone = &m.pvdone[C::kGroups == 2 ? group : 0];
-        for (int u = u0; u < end; u += step, ++mine) {
-            const int tile = un.tile(u), buf = un.buf(u);
-            const int t0 = (w.j0 + tile) * C::kN + col0;   // the first position of this group's
+        for (int u = 0; u < end; ++u, ++since) {   // tiles
+            const int buf = own_rows ? group : u & 1;
+            const int t0 = (w.j0 + u) * C::kN + col0;   // the first position of this group's
             const uint32_t t_s = t_lane + buf * C::kN + col0;
             const bool tail = t0 + columns > base;
             if (!(ok = wait(&m.sfull[buf], (sph >> buf) & 1u)))
                 break;
             sph ^= 1u << buf;
             tc_fence_after();
-            const bool flush = mine > 0 && mine % flush_every == 0;
+            const bool flush = since == flush_every;
             if (!own_rows && flush && !(ok = wait(pvdone, pvph ^ 1u)))
                 break;
-            if (flush && warp_live) {
+            if (flush) {
                 tc_fence_after();
-                flush_sums(mine == flush_every, mx);
+                if (warp_live)
+                    flush_sums(!flushed, mx);
+                since = 0;
+                flushed = true;
             }
             float mx_off = 0.f;
             if (warp_live) {
-                // Two passes over the row's scores, 32 columns at a time, the next
-                // ones on their way: the maximum, then the weights.  The loops
-                // stay small for the instruction cache (with a tile unrolled and
-                // its scores in registers, a third of the cycles went to
-                // fetching instructions).  What the row does not see becomes
-                // -inf in tensor memory, so the second pass needs no mask.
-                float top[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
-                auto upper = [&](const uint32_t (&s)[32]) {
-#pragma unroll
-                    for (int k = 0; k < 32; k += 2)   // a three-way maximum each
-                        top[k / 2 & 3] = fmaxf(fmaxf(top[k / 2 & 3], __uint_as_float(s[k])), __uint_as_float(s[k + 1]));
-                };
+                // Two passes over the row's scores: the maximum, which the loads
+                // form, then the weights, 32 columns at a time.  The loops stay
+                // small for the instruction cache (with a tile unrolled and its
+                // scores in registers, a third of the cycles went to fetching
+                // instructions).  What the row does not see becomes -inf in
+                // tensor memory, so neither pass needs a mask.
                 if (tail) {
 #pragma unroll 1
                     for (int c = 0; c < columns / 32; ++c) {
@@ -1022,31 +1062,24 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
                         for (int k = 0; k < 32; ++k)
                             s[k] = bits >> k & 1u ? s[k] : 0xff800000u;
                         tmem_st32(t_s + 32 * c, s);
-                        upper(s);
                     }
                     tmem_wait_st();
-                } else {
-                    uint32_t s0[32], s1[32];
-                    tmem_ld32(t_s, s0);
-#pragma unroll 1
-                    for (int c = 0; c < columns; c += 64) {
-                        tmem_wait_ld32(s0);
-                        tmem_ld32(t_s + c + 32, s1);
-                        upper(s0);
-                        tmem_wait_ld32(s1);
-                        if (c + 64 < columns)
-                            tmem_ld32(t_s + c + 64, s0);
-                        upper(s1);
-                    }
                 }
-                const float tm = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                float tm = kNegInf;
+#pragma unroll 1
+                for (int c = 0; c < columns; c += 64) {
+                    uint32_t s0[32], s1[32];
+                    float m0 = tmem_ld32_max(t_s + c, s0), m1 = tmem_ld32_max(t_s + c + 32, s1);
+                    tmem_wait_max(m0, m1);
+                    tm = fmaxf(tm, fmaxf(m0, m1));
+                }
                 const bool grow = tm > mx && (mx == kNegInf || (tm - mx) * sl > kSlack);
                 if (__any_sync(0xffffffffu, grow)) {
                     const float corr = grow ? (mx == kNegInf ? 0.f : exp2_approx((mx - tm) * sl)) : 1.f;
                     if (grow)
                         mx = tm;
                     l *= corr;
-                    if (mine > 0 && !flush) {   // after a flush there is nothing to rescale
+                    if (since > 0) {   // at the start, and after a flush there is nothing to rescale
                         // with own rows the score that was waited for follows this
                         // accumulator's last MMAs; with two score buffers the last unit's
                         // may still run
@@ -1069,8 +1102,8 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
             }
             if (tail && (!own_rows || group == 0)) {
                 // the V rows of these weights (with own rows the first group cleans for both)
-                const int vs = (vcount + tile) % p.v_slots;
-                if (!(ok = wait(&m.vfull[vs], ((vcount + tile) / p.v_slots) & 1)))
+                const int vs = (vcount + u) % p.v_slots;
+                if (!(ok = wait(&m.vfull[vs], ((vcount + u) / p.v_slots) & 1)))
                     break;
                 tree_clean_v<D, F16, LOAD>(v_ring + vs * C::kSlotBytes, col0 + max(0, base - t0), col0 + columns,
                                            L - t0 + col0, t0 - col0 - base, m.bad[odd], tid);
@@ -1080,7 +1113,7 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
             // A barrier's phases are told apart by parity alone: each has to be waited
             // for before the next but one can end.  The last unit's MMAs are waited
             // for below; those before them here, as long as the last cannot run.
-            if (!own_rows && mine > 0 && u + step >= end && !(ok = wait(pvdone, pvph ^ 1u)))
+            if (!own_rows && u > 0 && u + 1 == end && !(ok = wait(pvdone, pvph ^ 1u)))
                 break;
             // The weights, 64 positions at a time: the MMAs of the first half
             // run beside the exponentials of the second.
@@ -1099,7 +1132,7 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
                 for (int k = 0; k < 16; ++k) {
                     sum[k & 1] = fma2(x[k], one2, sum[k & 1]);
                     s[k] = pack_x2<F16>(x[k].x, x[k].y);
-                    const float2 rest = fma2(x2_to_float2<F16>(s[k]), neg2, x[k]);
+                    const float2 rest = kMixed ? minus_x2<F16>(x[k], s[k]) : fma2(x2_to_float2<F16>(s[k]), neg2, x[k]);
                     s[16 + k] = pack_x2<F16>(rest.x, rest.y);
                 }
                 tmem_st32(t_s + 32 * c, s);
@@ -1126,7 +1159,7 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
             break;
         // the accumulator's last MMAs (those before: with own rows the last score
         // followed them, else they were waited for)
-        if (mine > 0 && !(ok = wait(pvdone, pvph ^ 1u)))
+        if (end > 0 && !(ok = wait(pvdone, pvph ^ 1u)))
             break;
         tc_fence_after();
         vcount += w.n;
@@ -1136,7 +1169,7 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
             fetch_q(next);
 
         // the segment's result: O / l and the log-sum-exp (base 2), final or partial
-        if (mine > flush_every && warp_live) {
+        if (flushed && warp_live) {
             flush_sums(false, mx);   // the segment's whole sum, relative to ref
             if (mx != kNegInf) {
                 l *= exp2_approx((mx - ref) * sl);
@@ -1186,7 +1219,7 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
 #pragma unroll
             for (int k = 0; k < 32; ++k)
                 v[k] = 0.f;
-            if (mine > 0 && warp_live) {
+            if (end > 0 && warp_live) {
                 // columns c .. c + 31 of a group's sum: in the workspace once it was flushed
                 auto add = [&](int of, bool flushed, float weight) {
                     if (flushed) {
@@ -1211,10 +1244,10 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
                     }
                 };
                 if (shared_rows) {
-                    add(0, mine > flush_every, a0);
-                    add(1, mine > flush_every, a1);
+                    add(0, flushed, a0);
+                    add(1, flushed, a1);
                 } else
-                    add(C::kGroups == 1 ? 0 : group, mine > flush_every, 1.f);
+                    add(C::kGroups == 1 ? 0 : group, flushed, 1.f);
 #pragma unroll
                 for (int k = 0; k < 32; ++k)
                     v[k] = any ? v[k] * inv : 0.f;
