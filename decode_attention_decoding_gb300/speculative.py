@@ -77,7 +77,7 @@ def _status(t, gpu):
 
 def _launch(gpu, f, *args):
     """Call f with the GPU's current stream as its last argument and the GPU current (kernels launch on the current one)."""
-    s = torch.cuda.current_stream(gpu).cuda_stream
+    s = torch._C._cuda_getCurrentRawStream(gpu)   # torch.cuda.current_stream(gpu).cuda_stream without the object: 0.1 us, not 1.1
     if torch.cuda.current_device() == gpu:
         return f(*args, s)
     with torch.cuda.device(gpu):
