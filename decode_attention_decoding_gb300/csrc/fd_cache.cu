@@ -28,9 +28,9 @@ struct TablesParams {
 constexpr int kTablesThreads = 256;
 constexpr int kTablesTokensPerThread = 4;
 // CTAs an SM: more hide the slots' chains of loads, and each scans the lengths
-// once more.  1.6 M tokens of 384 requests: 2, 4, 8, 16 an SM 15.5, 12.1, 14.0,
-// 15.5 us; 512 threads a CTA are slower at either end (64 tokens of 64
-// requests 4.4 -> 4.8 us).
+// once more.  1.6 M tokens of 384 requests: 2, 4, 8, 16 an SM 15.1, 11.8, 13.6,
+// 15.0 us; 512 threads a CTA are slower at either end (15.4 us, and 64 tokens
+// of 64 requests 4.7 instead of 4.5).
 constexpr int kTablesCtasPerSm = 4;
 
 // Sum of v over the threads before this one, and over all of them in *total.

@@ -31,9 +31,9 @@ constexpr int kMaxTreeRows = 4096;   // nodes x query heads of a kv head
 constexpr int kTreeMaxCtas = 256;    // split CTAs (sizes the workspace)
 
 // Cost of a segment start in tiles of the split (below).  Measured on GB300
-// with 3, 4, 5, 7: 16 ragged GQA-4 requests of up to 8192 tokens 74, 70, 72, 73
-// us, 64 of up to 16384 364, 362, 361, 363, one of 2048 tokens 17.7, 17.8, 18.7,
-// 18.7.
+// with 3, 4, 5, 7: 16 ragged GQA-4 requests of up to 8192 tokens 72, 69, 73, 75
+// us, 64 of up to 16384 371, 370, 368, 371, one of 2048 tokens 17.4, 17.4, 18.2,
+// 18.2.
 constexpr int kTreeSegCost = 4;
 
 // A scale of 0 becomes this one, so that a hidden score (-inf) keeps its
