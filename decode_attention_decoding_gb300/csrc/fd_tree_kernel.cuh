@@ -42,7 +42,10 @@
 // What a row must not see must not reach it: a score outside the row's mask is
 // dropped before the maximum, and V rows behind the last position are zeroed
 // in shared memory.  Among the nodes, a V element that is not finite is zeroed
-// too and added afterwards, to the rows that see its node (fix_up).
+// too and added afterwards, to the rows that see its node (the end of
+// tree_softmax).  In the context it goes through the MMAs: every row sees it.
+// NaN comes out as NaN, but an infinity as itself or as NaN, by the signs of
+// the weights' remainders and by what is rescaled by 0 (tree_infinities).
 #pragma once
 
 #include <atomic>
@@ -884,6 +887,52 @@ __device__ __forceinline__ float tree_element(const uint8_t *cache, long long e)
         return x2_to_float2<F16>(reinterpret_cast<const uint16_t *>(cache)[e]).x;
 }
 
+// Infinities of the context.  An infinite V element takes an infinite amount
+// into its dim, whatever its weight; in the MMAs that is infinity times a
+// weight's two parts, one of which may be 0 or of the other sign, and NaN then.
+// So when an output is NaN though no score was, a warp looks through the V rows
+// [from, to) of its CTA's part of the context for what is not finite, and the
+// rows' outputs in those dims (c0 to c1) are set to what all of it adds up to.
+// Nothing is read otherwise; when it is, a warp reads 512 bytes a step.
+template <int D, bool F16, int KV>
+__device__ __forceinline__ void tree_infinities(const TreeParams &p, int b, int g, int from, int to, int c0, int c1,
+                                                bool mine, float *dst, int stride, int lane)
+{
+    constexpr int kBytes = kv_is_fp8(KV) ? 1 : 2, kPer = 16 / kBytes, kPieces = D / kPer, kRows = 32 / kPieces;
+    constexpr uint32_t kExp = kv_is_fp8(KV) ? 0x7cu : F16 ? 0x7c00u : 0x7f80u, kSign = kv_is_fp8(KV) ? 0x80u : 0x8000u;
+    static_assert(KV != kKvE4m3 && kPieces <= 32, "E4M3 has no infinities");
+    uint32_t plus = 0, minus = 0, nan = 0;   // a bit for each element of this lane's piece of a row
+#pragma unroll 4
+    for (int n = from; n < to; n += kRows) {
+        const int pos = n + lane / kPieces;
+        if (pos >= to)
+            continue;
+        const long long row = tree_row(p, b, pos, false);
+        const uint4 v = *reinterpret_cast<const uint4 *>(p.v + ((row * p.hkv + g) * D + lane % kPieces * kPer) * kBytes);
+        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+            const uint32_t y = x[e * kBytes / 4] >> (e * kBytes % 4 * 8) & (kSign * 2 - 1);
+            if ((y & kExp) == kExp)
+                (y & (kExp ^ (kSign - 1)) ? nan : y & kSign ? minus : plus) |= 1u << e;
+        }
+    }
+    __syncwarp();
+    for (int off = kPieces; off < 32; off <<= 1) {
+        plus |= __shfl_xor_sync(0xffffffffu, plus, off);
+        minus |= __shfl_xor_sync(0xffffffffu, minus, off);
+        nan |= __shfl_xor_sync(0xffffffffu, nan, off);
+    }
+    for (int k = c0 / kPer; k < c1 / kPer; ++k) {
+        const uint32_t up = __shfl_sync(0xffffffffu, plus, k), down = __shfl_sync(0xffffffffu, minus, k),
+                       none = __shfl_sync(0xffffffffu, nan, k) | (up & down);
+        for (uint32_t left = up | down | none; mine && left; left &= left - 1) {
+            const int e = __ffs(left) - 1, d = k * kPer + e;
+            dst[(d / 4) * stride + d % 4] = __uint_as_float(none >> e & 1u ? 0x7fffffffu : up >> e & 1u ? 0x7f800000u : 0xff800000u);
+        }
+    }
+}
+
 // A group of 128 threads, one query row each.
 template <int D, bool F16, int KV, int LOAD>
 __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, uint32_t q_smem, uint32_t v_ring,
@@ -1212,6 +1261,10 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
         const int slot = 2 * (int)blockIdx.x + (w.j0 > 0 ? 0 : 1);
         const int srow = (own_rows ? group * 128 : 0) + tid;   // row of the partial
         const int c0 = shared_rows ? group * (D / 2) : 0, c1 = shared_rows ? c0 + D / 2 : D;
+        // dim d of this row's output, or partial: out[d / 4 * stride + d % 4]
+        float *out = whole ? p.o + o_row * D : p.ws_o + ((long long)slot * (D / 4) * p.slot_rows + srow) * 4;
+        const int stride = whole ? 4 : p.slot_rows * 4;
+        [[maybe_unused]] float2 every = make_float2(0.f, 0.f);   // the outputs' sums: NaN if an output is
         __syncwarp();
         for (int c = c0; c < c1; c += 32) {
             float v[32];
@@ -1251,14 +1304,15 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
 #pragma unroll
                 for (int k = 0; k < 32; ++k)
                     v[k] = any ? v[k] * inv : 0.f;
+                if constexpr (KV != kKvE4m3)
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2)
+                        every = fma2(make_float2(v[k], v[k + 1]), make_float2(1.f, 1.f), every);
             }
             if (in_call && (whole || any)) {
-                float *dst = whole ? p.o + o_row * D + c
-                                   : p.ws_o + (((long long)slot * (D / 4) + c / 4) * p.slot_rows + srow) * 4;
-                const int stride = whole ? 4 : p.slot_rows * 4;
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    *reinterpret_cast<float4 *>(dst + k * stride) = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                    *reinterpret_cast<float4 *>(out + (c / 4 + k) * stride) = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
             }
             __syncwarp();
         }
@@ -1270,7 +1324,14 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
             else if (p.lse)
                 p.lse[o_row] = any ? lse2 * 0.6931471805599453f : kNegInf;
         }
-        // values that are not finite, of nodes in this CTA's tiles
+        // values that are not finite: of the context, then of nodes in this CTA's tiles
+        if constexpr (KV != kKvE4m3) {
+            const float all = every.x + every.y;
+            const bool mine = any && l == l && all != all;
+            if (__any_sync(0xffffffffu, mine))
+                tree_infinities<D, F16, KV>(p, w.b, g, w.j0 * C::kN, min((w.j0 + w.n) * C::kN, base), c0, c1, mine, out, stride,
+                                            threadIdx.x & 31);
+        }
         for (int wd = 0; wd < kMaxTree / 32; ++wd) {
             uint32_t nodes = m.bad[odd][wd];
             for (; nodes; nodes &= nodes - 1) {
@@ -1282,13 +1343,13 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
                 for (int d = 0; d < D; ++d)
                     s = fmaf(p.q_f16 ? f16x2_to_float2(p.q[o_row * D + d]).x : bf16x2_to_float2(p.q[o_row * D + d]).x,
                              tree_element<F16, KV>(p.k, at + d), s);
-                const float weight = exp2_approx((p.negate_q ? -s : s) * p.scale_log2 - lse2);
+                // an infinity stays one when its weight is too small for fp32 (a weight of NaN has made the row NaN)
+                const float weight = fmaxf(exp2_approx((p.negate_q ? -s : s) * p.scale_log2 - lse2), 1.1754944e-38f);
                 for (int d = c0; d < c1; ++d) {
                     const float x = tree_element<F16, KV>(p.v, at + d);
                     if (fabsf(x) <= 3.4028235e38f)
                         continue;
-                    float *dst = whole ? p.o + o_row * D + d
-                                       : p.ws_o + (((long long)slot * (D / 4) + d / 4) * p.slot_rows + srow) * 4 + d % 4;
+                    float *dst = out + (d / 4) * stride + d % 4;
                     *dst = fmaf(weight, x, *dst);
                 }
             }

@@ -93,7 +93,10 @@ __global__ void __launch_bounds__(32 * merge_warps(D)) tree_merge_kernel(const _
 #pragma unroll
                 for (int n = 0; n < kTogether; ++n)
                     higher = fmaxf(higher, x[n]);
-                const float ref = higher == kNegInf ? 0.f : higher, down = exp2_approx(top - ref);
+                // at least fp32's least normal number: an infinite sum stays infinite however small
+                // its weight is, and 10^-38 of a finite one does not matter
+                auto weight = [](float y) { return y < -126.f ? 1.1754944e-38f : exp2_approx(y); };   // NaN: NaN
+                const float ref = higher == kNegInf ? 0.f : higher, down = weight(top - ref);
                 sum *= down;
 #pragma unroll
                 for (int k = 0; k < kCols; ++k)
@@ -103,7 +106,7 @@ __global__ void __launch_bounds__(32 * merge_warps(D)) tree_merge_kernel(const _
                 for (int n = 0; n < kTogether; ++n) {
                     if (x[n] == kNegInf)
                         continue;   // no partial, or one that saw nothing and wrote nothing
-                    const float w = exp2_approx(x[n] - ref);
+                    const float w = weight(x[n] - ref);
                     sum += w;
 #pragma unroll
                     for (int k = 0; k < kCols; ++k) {

@@ -584,7 +584,9 @@ size_t fd_tree_workspace_size(int batch, int tree_len, int num_q_heads, int num_
  * <= 4096; head_dim 64, 128 or 256; bf16, fp16 or FP8 caches.  What the cache
  * holds at positions that no row sees (behind L_b, nodes without a set bit in
  * any row) does not matter, and what a node holds does not reach the rows that
- * do not see it, not-a-numbers included.
+ * do not see it, not-a-numbers included.  An infinite V element makes its dim of
+ * every row that sees it infinite, however small the weight; together with one
+ * of the other sign, or a NaN, it makes it NaN.
  */
 fd_status fd_tree_decode(const void *q, const void *k, const void *v, const uint64_t *tree_mask,
                          long long mask_stride, const int32_t *tree_lens_dev,
