@@ -33,6 +33,9 @@ constexpr int kTablesTokensPerThread = 4;
 // of 64 requests 4.7 instead of 4.5).
 constexpr int kTablesCtasPerSm = 4;
 
+// Shared memory of the kernel: cu and pages [batch + 1], old and held [batch].
+constexpr size_t tables_smem(int batch) { return sizeof(int) * (4 * (size_t)batch + 2); }
+
 // Sum of v over the threads before this one, and over all of them in *total.
 template <class T>
 __device__ __forceinline__ T block_exclusive_scan(T v, T *tmp, T *total)
@@ -520,9 +523,11 @@ fd_status fd_build_tables(const int32_t *seq_lens, const int32_t *new_lens, cons
     p.status = device_status;
     const long long want = pieces(max_tokens, kTablesThreads * kTablesTokensPerThread);
     const int grid = (int)(want < 1 ? 1 : want > kTablesCtasPerSm * sms ? kTablesCtasPerSm * sms : want);
-    const size_t smem = sizeof(int) * (4 * (size_t)batch + 2);
-    if (smem > 48 * 1024 - 256 &&   // beside the kernel's static part: large batches only
-        cudaFuncSetAttribute(build_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    // beside the kernel's static part, large batches only: the limit is the
+    // largest batch's, so that no call lowers it under another thread's launch
+    const size_t smem = tables_smem(batch);
+    if (smem > 48 * 1024 - 256 &&
+        cudaFuncSetAttribute(build_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)tables_smem(kMaxBatch)) != cudaSuccess)
         return FD_ERR_CUDA;
     build_tables_kernel<<<grid, kTablesThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(p);
     return cudaGetLastError() == cudaSuccess ? FD_OK : FD_ERR_CUDA;
