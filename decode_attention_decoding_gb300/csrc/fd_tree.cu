@@ -91,11 +91,14 @@ struct TreeWorkspace {
 };
 TreeWorkspace tree_workspace(int batch, int tree_rows, int d)
 {
-    const size_t rows = (size_t)slot_rows_of(segment_rows(tree_rows, d), tree_rows) * 2 * kTreeMaxCtas;
+    const size_t partials = 2 * kTreeMaxCtas, rows = partials * slot_rows_of(segment_rows(tree_rows, d), tree_rows);
+    // the statistics of as many rows as any head dim's segment has, so that the
+    // size grows with the head dim too
+    const size_t lse_rows = partials * slot_rows_of(256, tree_rows);
     TreeWorkspace w;
     w.cost = 256;
     w.lse = align_up(w.cost + sizeof(long long) * ((size_t)batch + 1), 256);
-    w.o = align_up(w.lse + sizeof(float) * rows, 256);
+    w.o = align_up(w.lse + sizeof(float) * lse_rows, 256);
     w.sums = align_up(w.o + sizeof(float) * rows * d, 256);
     w.total = align_up(w.sums + sizeof(float) * kTreeMaxCtas * tree_groups(d) * slot_rows_of(128, tree_rows) * d, 256);
     return w;

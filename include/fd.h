@@ -543,8 +543,9 @@ fd_status fd_cache_compact(void *k_cache, void *v_cache, const int32_t *block_ta
 /* Bytes of workspace that fd_tree_decode / fd_tree_decode_paged need for a
  * shape (the CTAs' partial outputs and running sums, whatever the lengths: up
  * to 101 MB for more than 128 query rows a kv head); initialise it once with
- * fd_workspace_init.  A workspace of one shape serves every smaller one.  Pure
- * host function; 0 for shapes that no call accepts. */
+ * fd_workspace_init.  A workspace of one shape serves every shape with no more
+ * requests, no more query rows a kv head (tree_len * Hq/Hkv) and no larger
+ * head_dim.  Pure host function; 0 for shapes that no call accepts. */
 size_t fd_tree_workspace_size(int batch, int tree_len, int num_q_heads, int num_kv_heads, int head_dim);
 
 /*
