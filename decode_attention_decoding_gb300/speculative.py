@@ -10,7 +10,8 @@ fd_cache_compact (include/fd.h).
 Like the package's other functions these only check and marshal arguments;
 tensors live on one GPU, outputs are allocated unless they are given.  A call
 runs on that GPU's current stream, whatever device is current, or on the
-stream given as `stream=`, which then owns what the call allocates.  These
+stream given as `stream=`, one of that GPU, which then owns what the call
+allocates.  These
 calls take a few microseconds on the GPU, so the checks are kept to a few
 attribute reads a tensor.
 """
@@ -44,11 +45,13 @@ class Tables(NamedTuple):
     free_count: torch.Tensor    # [1] int32
 
 
-def _gpu(t, name):
-    """Index of the GPU that t is on."""
+def _gpu(t, name, stream):
+    """Index of the GPU that t, and the stream if one is given, is on."""
     index = t.get_device()
     if index < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
+    if stream is not None and stream.device.index != index:
+        raise ValueError(f"stream is on {stream.device}, {name} on cuda:{index}")
     return index
 
 
@@ -91,20 +94,20 @@ def _on_stream(f):
         if stream is None:
             return f(*args, **kw)
         with torch.cuda.stream(stream):
-            return f(*args, **kw)
+            return f(*args, stream=stream, **kw)
     return call
 
 
 @_on_stream
 def fd_build_tables(seq_lens, new_lens, block_table, free_pages, free_count, page_size, num_pages, max_tokens,
-                    held_pages=None, slot_map=None, device_status=None, check=True):
+                    held_pages=None, slot_map=None, device_status=None, check=True, *, stream=None):
     """Give requests pages and slots for their new tokens (see fd_build_tables in include/fd.h).
 
     seq_lens, new_lens and held_pages int32 [B]; block_table int32 [B,
     max_blocks], updated in place; free_pages int32 [n], a stack whose first
     free_count (int32 [1]) entries are free; max_tokens the length of the slot
     map (entries behind the last token are -1).  Returns a Tables."""
-    gpu = _gpu(block_table, "block_table")
+    gpu = _gpu(block_table, "block_table", stream)
     B = seq_lens.shape[0]
     per_request, n = (B,), int(max_tokens)
     table, blocks = _table_of(block_table, B, gpu)
@@ -139,7 +142,7 @@ def _token_rows(t, name, gpu):
 
 @_on_stream
 def fd_cache_write(k_new, v_new, slot_map, k_cache, v_cache, kv_dtype=None, k_scale=1.0, v_scale=1.0,
-                   device_status=None, check=True):
+                   device_status=None, check=True, *, stream=None):
     """Write new K/V rows into the cache's slots (see fd_cache_write in include/fd.h).
 
     k_new, v_new bf16 or fp16 [n, Hkv, D], any token stride that is a multiple
@@ -147,7 +150,7 @@ def fd_cache_write(k_new, v_new, slot_map, k_cache, v_cache, kv_dtype=None, k_sc
     (pages [num_pages, P, Hkv, D], a contiguous cache [B, S, Hkv, D], or flat
     slots) of the same type, or FP8: float8 tensors, or uint8 codes with
     kv_dtype 'e4m3' / 'e5m2', quantised by k_scale / v_scale."""
-    gpu = _gpu(k_cache, "k_cache")
+    gpu = _gpu(k_cache, "k_cache", stream)
     ks, vs = _token_rows(k_new, "k_new", gpu), _token_rows(v_new, "v_new", gpu)
     kv = _kv_code(k_cache, v_cache, kv_dtype)
     n, h, d = shape = k_new.shape
@@ -167,7 +170,7 @@ def fd_cache_write(k_new, v_new, slot_map, k_cache, v_cache, kv_dtype=None, k_sc
 
 @_on_stream
 def fd_cache_compact(k_cache, v_cache, seq_lens, accepted, accept_lens, tree_len, block_table=None, tree_lens=None,
-                     seq_lens_out=None, device_status=None, check=True):
+                     seq_lens_out=None, device_status=None, check=True, *, stream=None):
     """Move the accepted path's rows to the front of the drafted tail, in place
     (see fd_cache_compact in include/fd.h).
 
@@ -176,7 +179,7 @@ def fd_cache_compact(k_cache, v_cache, seq_lens, accepted, accept_lens, tree_len
     [B] with the drafted tokens; accepted int32 [B, max_accept], ascending node
     indices; accept_lens int32 [B]; tree_lens int32 [B] or None (tree_len for
     every request).  Returns the new lengths int32 [B]."""
-    gpu = _gpu(k_cache, "k_cache")
+    gpu = _gpu(k_cache, "k_cache", stream)
     B = seq_lens.shape[0]
     per_request = (B,)
     size = k_cache.element_size()
@@ -224,9 +227,9 @@ def make_tree_workspace(batch, tree_len, num_q_heads, num_kv_heads, head_dim=128
 
 
 def _tree(name, q, k, v, block_table, seq_lens, tree_mask, tree_lens, seq_lens_host, scale, out, lse, workspace, num_ctas,
-          flags, wait_timeout_ns, split_events, check, dtype, kv_dtype, k_scale, v_scale):
+          flags, wait_timeout_ns, split_events, check, dtype, kv_dtype, k_scale, v_scale, stream):
     """Both layouts: checks, outputs, and the call `name`."""
-    gpu = _gpu(q, "q")
+    gpu = _gpu(q, "q", stream)
     if q.dim() != 4 or not q.is_contiguous() or q.element_size() != 2:
         raise ValueError("q must be a contiguous bf16 or fp16 tensor [B, tree_len, Hq, D]")
     kv = _kv_code(k, v, kv_dtype)
@@ -283,7 +286,7 @@ def _tree(name, q, k, v, block_table, seq_lens, tree_mask, tree_lens, seq_lens_h
 @_on_stream
 def fd_tree_decode(q, k, v, seq_lens=None, tree_mask=None, tree_lens=None, seq_lens_host=None, scale=None, out=None,
                    lse=None, workspace=None, num_ctas=0, flags=0, wait_timeout_ns=0, split_events=None, check=True,
-                   dtype=None, kv_dtype=None, k_scale=1.0, v_scale=1.0):
+                   dtype=None, kv_dtype=None, k_scale=1.0, v_scale=1.0, *, stream=None):
     """Attention of a drafted tree over a contiguous cache (see fd_tree_decode in include/fd.h).
 
     q [B, T, Hq, D]; k/v [B, S, Hkv, D] with the T nodes as the last positions
@@ -292,17 +295,17 @@ def fd_tree_decode(q, k, v, seq_lens=None, tree_mask=None, tree_lens=None, seq_l
     None: a causal chain); tree_lens int32 [B] (None: T nodes each).  The other
     arguments are fd_decode's.  Returns (out fp32 [B, T, Hq, D], lse [B, T, Hq])."""
     return _tree("fd_tree_decode", q, k, v, None, seq_lens, tree_mask, tree_lens, seq_lens_host, scale, out, lse,
-                 workspace, num_ctas, flags, wait_timeout_ns, split_events, check, dtype, kv_dtype, k_scale, v_scale)
+                 workspace, num_ctas, flags, wait_timeout_ns, split_events, check, dtype, kv_dtype, k_scale, v_scale, stream)
 
 
 @_on_stream
 def fd_tree_decode_paged(q, k_pages, v_pages, block_table, seq_lens, tree_mask=None, tree_lens=None,
                          seq_lens_host=None, scale=None, out=None, lse=None, workspace=None, num_ctas=0, flags=0,
                          wait_timeout_ns=0, split_events=None, check=True, dtype=None, kv_dtype=None,
-                         k_scale=1.0, v_scale=1.0):
+                         k_scale=1.0, v_scale=1.0, *, stream=None):
     """fd_tree_decode over pages [num_pages, P, Hkv, D] behind block_table int32 [B, max_blocks]."""
     if seq_lens is None or block_table is None:
         raise ValueError("a paged cache needs its block_table and seq_lens")
     return _tree("fd_tree_decode_paged", q, k_pages, v_pages, block_table, seq_lens, tree_mask, tree_lens,
                  seq_lens_host, scale, out, lse, workspace, num_ctas, flags, wait_timeout_ns, split_events, check,
-                 dtype, kv_dtype, k_scale, v_scale)
+                 dtype, kv_dtype, k_scale, v_scale, stream)
