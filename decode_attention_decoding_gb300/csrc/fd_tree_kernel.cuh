@@ -28,7 +28,7 @@
 //     tile: one group's exponentials run beside the other's MMAs.
 //
 // P is taken as a 16-bit part and its 16-bit remainder (two MMAs): outputs are
-// fp32, and one bf16 part alone would leave an error of 2^-9.  The two parts
+// fp32, and one bf16 part alone would leave an error of 2^-8.  The two parts
 // of 32 positions, 16 + 16 columns, overwrite those positions' 32 columns of S.
 //
 // The accumulator is rescaled only when a row's maximum grew by more than

@@ -578,7 +578,10 @@ size_t fd_tree_workspace_size(int batch, int tree_len, int num_q_heads, int num_
  *                (tree_len replaces it), and no user flag changes the call.
  *   The other arguments are fd_decode's.
  * Runs on the tcgen05 tensor cores with fp32 scores, sums and accumulation; each
- * softmax weight is taken as a 16-bit part plus its 16-bit remainder.  Results
+ * softmax weight is taken as a 16-bit part plus its 16-bit remainder, and a bf16
+ * query against an FP8 cache as fp16 over a power of two a row.  Measured against
+ * 64 bits, for scores of a few units: an error of at most 6.1e-6 of O by norm
+ * (40000 positions; 2.5e-6 over 300).  Results
  * are bitwise the same from call to call (with the same num_ctas).  The first
  * call of a shape on a device sets a kernel attribute: make it before a capture.
  * Any whole group Hq/Hkv; tree_len 1 .. 256; tree_len * Hq/Hkv <= 4096; batch
