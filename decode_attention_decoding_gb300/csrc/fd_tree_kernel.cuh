@@ -893,28 +893,51 @@ __device__ __forceinline__ float tree_element(const uint8_t *cache, long long e)
 // So when an output is NaN though no score was, a warp looks through the V rows
 // [from, to) of its CTA's part of the context for what is not finite, and the
 // rows' outputs in those dims (c0 to c1) are set to what all of it adds up to.
-// Nothing is read otherwise; when it is, a warp reads 512 bytes a step.
+// cache: V's rows of the kv head, of the whole pool with the request's blocks in
+// table, of the request without.
+// Nothing is read otherwise; when it is (or for a NaN), each warp reads it all,
+// 4 KB at a time: 1 M positions in one CTA take 84 ms instead of 9.  Not inlined,
+// so that the code that every segment runs stays together (one short request 17.4
+// us, inlined 17.65).
 template <int D, bool F16, int KV>
-__device__ __forceinline__ void tree_infinities(const TreeParams &p, int b, int g, int from, int to, int c0, int c1,
-                                                bool mine, float *dst, int stride, int lane)
+__device__ __noinline__ void tree_infinities(const uint8_t *cache, long long row_bytes, const int32_t *table, int page_size,
+                                             int num_pages, int from, int to, int c0, int c1, bool mine, float *dst, int stride)
 {
     constexpr int kBytes = kv_is_fp8(KV) ? 1 : 2, kPer = 16 / kBytes, kPieces = D / kPer, kRows = 32 / kPieces;
     constexpr uint32_t kExp = kv_is_fp8(KV) ? 0x7cu : F16 ? 0x7c00u : 0x7f80u, kSign = kv_is_fp8(KV) ? 0x80u : 0x8000u;
+    // in every element of a word: its sign bit; what carries an exponent of ones into it
+    constexpr uint32_t kOnes = kv_is_fp8(KV) ? 0x01010101u : 0x00010001u, kSigns = kOnes * kSign, kCarry = kOnes * (kSign - kExp);
+    constexpr int kBatch = 8;   // steps whose loads are in flight together
     static_assert(KV != kKvE4m3 && kPieces <= 32, "E4M3 has no infinities");
     uint32_t plus = 0, minus = 0, nan = 0;   // a bit for each element of this lane's piece of a row
-#pragma unroll 4
-    for (int n = from; n < to; n += kRows) {
-        const int pos = n + lane / kPieces;
-        if (pos >= to)
-            continue;
-        const long long row = tree_row(p, b, pos, false);
-        const uint4 v = *reinterpret_cast<const uint4 *>(p.v + ((row * p.hkv + g) * D + lane % kPieces * kPer) * kBytes);
-        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+    const int lane = threadIdx.x & 31;
+    const uint8_t *piece = cache + lane % kPieces * 16;
+    const unsigned end = max(to, 0);
+#pragma unroll 1
+    for (unsigned n = from + lane / kPieces; n < end; n += kRows * kBatch) {
+        uint4 v[kBatch];
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-            const uint32_t y = x[e * kBytes / 4] >> (e * kBytes % 4 * 8) & (kSign * 2 - 1);
-            if ((y & kExp) == kExp)
-                (y & (kExp ^ (kSign - 1)) ? nan : y & kSign ? minus : plus) |= 1u << e;
+        for (int k = 0; k < kBatch; ++k) {
+            const unsigned pos = min(n + k * kRows, end - 1);   // the last row more than once does no harm
+            long long row = pos;
+            if (table) {
+                const unsigned blk = pos / (unsigned)page_size, page = (unsigned)table[blk];
+                row = (long long)(page < (unsigned)num_pages ? page : 0u) * page_size + (pos - blk * (unsigned)page_size);
+            }
+            v[k] = ldg128_nc(piece + row * row_bytes);
+        }
+        auto odd = [&](uint32_t x) { return (x & ~kSigns) + kCarry; };
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const uint32_t x[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+            if (!((odd(x[0]) | odd(x[1]) | odd(x[2]) | odd(x[3])) & kSigns))
+                continue;
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) {
+                const uint32_t y = x[e * kBytes / 4] >> (e * kBytes % 4 * 8) & (kSign * 2 - 1);
+                if ((y & kExp) == kExp)
+                    (y & (kExp ^ (kSign - 1)) ? nan : y & kSign ? minus : plus) |= 1u << e;
+            }
         }
     }
     __syncwarp();
@@ -1337,9 +1360,12 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
         if constexpr (KV != kKvE4m3) {
             const float all = every.x + every.y;
             const bool mine = any && l == l && all != all;
-            if (__builtin_expect(__any_sync(0xffffffffu, mine), 0))
-                tree_infinities<D, F16, KV>(p, w.b, g, w.j0 * C::kN, min((w.j0 + w.n) * C::kN, base), c0, c1, mine, out, stride,
-                                            threadIdx.x & 31);
+            if (__builtin_expect(__any_sync(0xffffffffu, mine), 0)) {
+                const long long row_bytes = (long long)p.hkv * D * (kv_is_fp8(KV) ? 1 : 2), row0 = p.block_table ? 0 : (long long)w.b * p.page_size;
+                tree_infinities<D, F16, KV>(p.v + (row0 * p.hkv + g) * D * (kv_is_fp8(KV) ? 1 : 2), row_bytes,
+                                            p.block_table ? p.block_table + (long long)w.b * p.max_blocks : nullptr, p.page_size,
+                                            p.num_pages, w.j0 * C::kN, min((w.j0 + w.n) * C::kN, base), c0, c1, mine, out, stride);
+            }
         }
         for (int wd = 0; wd < kMaxTree / 32; ++wd) {
             uint32_t nodes = m.bad[odd][wd];

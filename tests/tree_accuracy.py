@@ -13,8 +13,9 @@ of random signs, roundings add up as the outputs themselves do:
   - scores of a few units are off by less than 2^-20 (D / 16 fp32 steps), the
     exponential by 2^-22: 0.1 2^-16.
 Weights of one 16-bit part alone are off by up to 2^-8 (bf16) or 2^-11 (fp16), and
-by some 0.4 of that as they fall: 100 or 13 times the bound.  An accumulator of 40000 positions that is never
-flushed loses some 4e-5, nearly three times the bound."""
+by some 0.4 of that as they fall: 100 or 13 times the bound.  An accumulator of
+40000 positions that is never flushed loses some 4e-5, nearly three times the
+bound."""
 import numpy as np
 import torch
 
