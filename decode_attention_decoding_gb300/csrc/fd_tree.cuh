@@ -109,7 +109,7 @@ __device__ __forceinline__ TreeSeg tree_seg(const TreeParams &p, TreeReq r)
 {
     TreeSeg s = {0, 0, 0};
     if (r.L > 0 && r.t > 0) {
-        s.nb = (r.L + tree_tile(D) - 1) / tree_tile(D);
+        s.nb = (r.L - 1) / tree_tile(D) + 1;   // L may be close to 2^31
         s.groups = (r.t * p.group + p.rows - 1) / p.rows;
         s.segs = p.hkv * s.groups;
     }

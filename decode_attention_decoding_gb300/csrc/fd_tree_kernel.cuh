@@ -1099,7 +1099,7 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
             const int buf = own_rows ? group : u & 1;
             const int t0 = (w.j0 + u) * C::kN + col0;   // the first position of this group's
             const uint32_t t_s = t_lane + buf * C::kN + col0;
-            const bool tail = t0 + columns > base;
+            const bool tail = columns > base - t0;   // t0 + columns may be 2^31
             if (!(ok = wait(&m.sfull[buf], (sph >> buf) & 1u)))
                 break;
             sph ^= 1u << buf;
@@ -1364,7 +1364,7 @@ __device__ __forceinline__ void tree_softmax(const TreeParams &p, TreeMisc &m, u
                 const long long row_bytes = (long long)p.hkv * D * (kv_is_fp8(KV) ? 1 : 2), row0 = p.block_table ? 0 : (long long)w.b * p.page_size;
                 tree_infinities<D, F16, KV>(p.v + (row0 * p.hkv + g) * D * (kv_is_fp8(KV) ? 1 : 2), row_bytes,
                                             p.block_table ? p.block_table + (long long)w.b * p.max_blocks : nullptr, p.page_size,
-                                            p.num_pages, w.j0 * C::kN, min((w.j0 + w.n) * C::kN, base), c0, c1, mine, out, stride);
+                                            p.num_pages, w.j0 * C::kN, (int)min((long long)(w.j0 + w.n) * C::kN, (long long)base), c0, c1, mine, out, stride);
             }
         }
         for (int wd = 0; wd < kMaxTree / 32; ++wd) {

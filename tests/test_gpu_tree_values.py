@@ -1,5 +1,5 @@
 """Tree attention on values that its other tests do not hold: infinities among
-the context's V."""
+the context's V, and a length next to 2^31."""
 import numpy as np
 import pytest
 import torch
@@ -69,3 +69,27 @@ def test_infinities_in_the_context(fd, D, T, dtype, kv, page, ctas, std):
             for pos in range(0, base, 3):
                 put(c, "v", b, pos, head, D // 2, INF)
     check_tree(*run(fd, c, 0.1, num_ctas=ctas), tree_attention(c["q64"], c["k64"], c["v64"], c["vis"], lens, c["trees"], 0.1))
+
+
+def test_a_length_next_to_2_31(fd):
+    """2^31 - 64 positions behind a table that names 8 pages again and again: the positions of a page
+    weigh as often as it is named.  A thread adds up to 2^31 / 128 / 152 = 110000 tiles' sums in fp32, 2^-24
+    each, in the sum of the weights and in O: 2 x 110000 x 2^-24 = 1.3e-2 at most, with the rest 1.4e-2; V is
+    positive, so the bound is relative."""
+    D, T, page, pages, blocks = 64, 2, 64, 9, (1 << 25) - 1
+    g = torch.Generator(device="cuda").manual_seed(5)
+    q = torch.randn(1, T, 1, D, generator=g, device="cuda").to(torch.bfloat16)
+    k = torch.randn(pages, page, 1, D, generator=g, device="cuda").to(torch.bfloat16)
+    v = torch.randn(pages, page, 1, D, generator=g, device="cuda").abs().to(torch.bfloat16)
+    table = torch.randint(0, 8, (1, blocks), generator=g, device="cuda", dtype=torch.int32)
+    table[0, -1] = 8                                          # the nodes' page: its last two positions
+    lens = i32([blocks * page])
+    ws = fd.make_tree_workspace(1, T, 1, 1, D)
+    o, lse = fd.fd_tree_decode_paged(q, k, v, table, lens, workspace=ws, scale=0.125)
+    assert fd.fd_get_device_error(ws) == fd.FD_OK
+    often = torch.bincount(table[0], minlength=pages).double().repeat_interleave(page).repeat(T, 1)
+    often[0, -1] = 0                                          # node 0 does not see node 1
+    s = (q[0, :, 0].double() @ k.view(-1, D).double().T) * 0.125 + often.log()
+    ref = torch.softmax(s, -1) @ v.view(-1, D).double()
+    assert float(((o[0, :, 0].double() - ref).abs() / ref).max()) <= 1.4e-2
+    assert float((lse[0, :, 0].double() - torch.logsumexp(s, -1)).abs().max()) <= 1.4e-2
