@@ -29,7 +29,9 @@ __all__ = [
     "fd_decode_noalloc", "fd_decode_partial", "fd_decode_paged_partial", "fd_merge_partials",
     "KV_END", "fd_build_tables", "fd_cache_write", "fd_cache_compact", "fd_tree_workspace_size",
     "make_tree_workspace", "fd_tree_decode", "fd_tree_decode_paged", "Tables", "FD_DEVICE_STATUS_BAD_LENGTH",
-    "FD_DEVICE_STATUS_NO_PAGES", "FD_DEVICE_STATUS_BAD_SLOT",
+    "FD_DEVICE_STATUS_NO_PAGES", "FD_DEVICE_STATUS_BAD_SLOT", "Cache4", "make_cache4", "fd_cache_write4", "fd_cache_read4",
+    "fd_decode4", "fd_decode4_paged", "fd_window_decode", "fd_window_decode_paged", "fd_window_workspace_size",
+    "make_window_workspace",
 ]
 
 FD_OK, FD_ERR_INVALID_ARG, FD_ERR_UNSUPPORTED, FD_ERR_WORKSPACE_TOO_SMALL = 0, 1, 2, 3
@@ -56,6 +58,11 @@ class FdOptions(ctypes.Structure):
                 ("split_start_event", ctypes.c_void_p), ("split_end_event", ctypes.c_void_p),
                 ("dtype", ctypes.c_int), ("kv_dtype", ctypes.c_int), ("k_scale", ctypes.c_float),
                 ("v_scale", ctypes.c_float), ("q_len", ctypes.c_int)]
+
+
+class FdCache4(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p)]
 
 
 def library_path() -> str:
@@ -105,6 +112,19 @@ def _load():
     lib.fd_tree_decode_paged.argtypes = [_P, _P, _P, _P, _I, _P, _LL, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F,
                                          _P, _P, _P, _SZ, ctypes.POINTER(FdOptions), _P]
     lib.fd_tree_decode_paged.restype = _I
+    cache4, opts = ctypes.POINTER(FdCache4), ctypes.POINTER(FdOptions)
+    lib.fd_cache_write4.argtypes = [_P, _P, _LL, _LL, _P, _I, _I, _I, cache4, _I, _LL, opts, _P, _P]
+    lib.fd_cache_read4.argtypes = [_P, _I, _I, _I, cache4, _I, _LL, _P, _P, _LL, _LL, opts, _P, _P]
+    lib.fd_window_workspace_size.argtypes = [_I, _I, _I, _I, _I]
+    lib.fd_window_workspace_size.restype = _SZ
+    lib.fd_window_decode.argtypes = [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _SZ, opts, _P]
+    lib.fd_window_decode_paged.argtypes = [_P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _SZ,
+                                           opts, _P]
+    lib.fd_decode4.argtypes = [_P, cache4, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _SZ, opts, _P]
+    lib.fd_decode4_paged.argtypes = [_P, cache4, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _SZ, opts, _P]
+    for f in (lib.fd_cache_write4, lib.fd_cache_read4, lib.fd_window_decode, lib.fd_window_decode_paged, lib.fd_decode4,
+              lib.fd_decode4_paged):
+        f.restype = _I
     lib.fd_get_device_error.argtypes = [_P, _P]
     lib.fd_get_device_error.restype = _I
     lib.fd_status_string.argtypes = [_I]
@@ -450,3 +470,6 @@ def fd_get_device_error(workspace, stream=None) -> int:
 from .speculative import (FD_DEVICE_STATUS_BAD_LENGTH, FD_DEVICE_STATUS_BAD_SLOT,  # noqa: E402
                           FD_DEVICE_STATUS_NO_PAGES, Tables, fd_build_tables, fd_cache_compact, fd_cache_write,
                           fd_tree_decode, fd_tree_decode_paged, fd_tree_workspace_size, make_tree_workspace)
+from .longcontext import (Cache4, fd_cache_read4, fd_cache_write4, fd_decode4, fd_decode4_paged,  # noqa: E402
+                          fd_window_decode, fd_window_decode_paged, fd_window_workspace_size, make_cache4,
+                          make_window_workspace)

@@ -4,8 +4,9 @@ Usage: ``python -m decode_attention_decoding_gb300.build`` or call :func:`build`
 Each translation unit is compiled by its own nvcc process, in parallel, then
 linked into ``decode_attention_decoding_gb300/libfd.so``.  ``fd_split_inst.cu``
 is compiled once per split-kernel variant (layout x K/V element type x head_dim)
-and ``fd_tree_inst.cu`` once per tree-kernel variant (how the cache is loaded x
-head_dim), each with its own defines.  Objects go to ``decode_attention_decoding_gb300/_build/``.
+``fd_tree_inst.cu`` once per tree-kernel variant (how the cache is loaded x
+head_dim) and ``fd_window_inst.cu`` once per window-kernel variant (K/V element
+type x head_dim), each with its own defines.  Objects go to ``decode_attention_decoding_gb300/_build/``.
 """
 from __future__ import annotations
 
@@ -40,6 +41,9 @@ KV_NAMES = ("bf16", "f16", "e4m3", "e5m2")
 TREE_INST = "fd_tree_inst.cu"
 TREE_LOADS = ("tma", "convert", "copy", "copy_fp8")   # fd_tree_inst.cu's FD_TREE_LOAD
 TREE_VARIANTS = [(load, d) for load in range(4) for d in (64, 128, 256)]
+WINDOW_INST = "fd_window_inst.cu"
+WINDOW_KV_NAMES = KV_NAMES + ("e2m1",)
+WINDOW_VARIANTS = [(kv, d) for kv in range(5) for d in (64, 128, 256)]
 SPLIT_VARIANTS = [(paged, kv, d) for paged in (0, 1) for kv in range(4) for d in (64, 128, 256)]
 
 
@@ -61,6 +65,9 @@ def _units():
             for load, d in TREE_VARIANTS:
                 units.append((src, f"{stem}_{TREE_LOADS[load]}_d{d}",
                               [f"-DFD_TREE_LOAD={load}", f"-DFD_TREE_D={d}"]))
+        elif os.path.basename(src) == WINDOW_INST:
+            for kv, d in WINDOW_VARIANTS:
+                units.append((src, f"{stem}_{WINDOW_KV_NAMES[kv]}_d{d}", [f"-DFD_WINDOW_KV={kv}", f"-DFD_WINDOW_D={d}"]))
         else:
             units.append((src, stem, []))
     return units

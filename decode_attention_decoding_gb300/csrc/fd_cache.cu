@@ -236,23 +236,6 @@ constexpr int kWriteUnitsPerThread = 4;
 
 enum : int { kWriteCopy = 0, kWriteE4m3 = 1, kWriteE5m2 = 2 };
 
-// x / scale as IEEE fp32 division rounds it.  FAST: from the rounded reciprocal
-// r of the scale, by one correction (Markstein 1990): q = x r, q + (x - q
-// scale) r with both steps fused is the correctly rounded quotient, for every
-// fp32 scale and every x of up to 11 significant bits (all mantissas of both
-// were tried; the exponents do not matter while nothing under- or overflows,
-// which scales in [2^-60, 2^60] see to for quotients that an FP8 type can tell
-// from 0 and from its largest value).  Quotients past 2^20 are cut to that
-// first, so that infinities reach the end as infinities.
-template <bool FAST>
-__device__ __forceinline__ float quotient(float x, float scale, float r)
-{
-    if constexpr (!FAST)
-        return __fdiv_rn(x, scale);
-    const float q = fminf(fmaxf(x * r, -1048576.f), 1048576.f);
-    return copysignf(fmaf(fmaf(-q, scale, x), r, q), x);   // -0 stays -0
-}
-
 // Four fp32 values to four FP8 codes, nearest even, saturating, NaN kept.
 template <int MODE, bool FAST>
 __device__ __forceinline__ uint32_t quantise4(float2 a, float2 b, float scale, float r)

@@ -228,6 +228,23 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b)
     return d;
 }
 
+// x / scale as IEEE fp32 division rounds it.  FAST: from the rounded reciprocal
+// r of the scale, by one correction (Markstein 1990): q = x r, q + (x - q
+// scale) r with both steps fused is the correctly rounded quotient, for every
+// fp32 scale and every x of up to 11 significant bits (all mantissas of both
+// were tried; the exponents do not matter while nothing under- or overflows,
+// which scales in [2^-60, 2^60] see to for quotients that an FP8 or 4-bit
+// type can tell from 0 and from its largest value).  Quotients past 2^20 are cut to that
+// first, so that infinities reach the end as infinities.
+template <bool FAST>
+__device__ __forceinline__ float quotient(float x, float scale, float r)
+{
+    if constexpr (!FAST)
+        return __fdiv_rn(x, scale);
+    const float q = fminf(fmaxf(x * r, -1048576.f), 1048576.f);
+    return copysignf(fmaf(fmaf(-q, scale, x), r, q), x);   // -0 stays -0
+}
+
 // Two bf16 values packed in a 32-bit word (element 0 in the low half) to fp32.
 __device__ __forceinline__ float2 bf16x2_to_float2(uint32_t w)
 {

@@ -1,0 +1,117 @@
+// fd_window.cuh -- decode attention through a sliding window with sinks, over
+// 16-bit, FP8 and 4-bit caches (sm_103a): parameters, and how the work is
+// divided among warps.
+//
+// The T = q_len new tokens of a request of length L sit at positions L - T + i.
+// Position t is visible to the token at position p when t <= p and
+// (t < sinks or t > p - window).  What some new token sees is
+//     [0, head) and [first, L),
+//     first = min(L, max(sinks, L - T - window + 1)), head = min(sinks, first),
+// and that is all a call reads: "row" v < head + L - first is position v if
+// v < head, else v - head + first.  Without a window first = head = 0.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "fd_device.cuh"
+#include "fd_sched.h"
+
+namespace fd {
+
+constexpr int kKvE2m1 = 4;           // 4-bit cache (after fd_device.cuh's kKv*)
+constexpr int kWindowMaxCtas = 160;  // split CTAs (sizes the workspace)
+constexpr int kWindowMaxWarps = 16;  // warps of a split CTA
+constexpr int kWindowMaxColumns = 16;
+
+// Cost of a segment start, in tiles (fd_sched.h): a warp loads the query and
+// flushes its outputs there.
+constexpr int kWindowSegCost = 1;
+
+// Shape of the split kernel for head dim D and a cache of type KV.
+template <int D_, int KV_>
+struct WindowCfg {
+    static constexpr int D = D_, KV = KV_;
+    static constexpr bool kFp4 = KV == kKvE2m1, kFp8 = KV == kKvE4m3 || KV == kKvE5m2;
+    static constexpr bool kF16 = KV != kKvBf16;              // type of the MMAs
+    static constexpr bool kInf = KV == kKvBf16 || KV == kKvF16 || KV == kKvE5m2;   // types with infinities
+    static constexpr int kParts = kF16 ? 2 : 3;              // 16-bit parts of a softmax weight
+    // weights are at most 2^kShift, so that fp16 remainders of small ones keep their bits
+    static constexpr float kShift = kF16 ? 14.f : 0.f;
+    static constexpr int kRow = kFp4 ? D / 2 : kFp8 ? D : 2 * D;   // bytes of a row
+    static constexpr int kGran = kRow / 16;                  // 16-byte pieces of a row
+    static constexpr int kScaleRow = kFp4 ? D / 16 : 0;      // bytes of a row's block scales
+    static constexpr int kTile = kRow <= 64 || (kRow <= 128 && !kFp4) ? 32 : 16;   // rows of a tile
+    static constexpr int kStage = 2 * kTile * (kRow + kScaleRow);
+    static constexpr int kWarps = kStage <= 2400 ? 16 : kStage <= 4800 && D < 256 ? 12 : kStage <= 8192 ? 8 : 4;
+    static constexpr int kStages = kStage <= 2400 || (kStage <= 4800 && D == 256) ? 4 : 3;
+    static constexpr int kRing = kStage * kStages;           // bytes of a warp's tiles
+};
+
+struct WindowParams {
+    const uint16_t *q;
+    const uint8_t *k, *v, *ks, *vs;    // cache rows; block scales of a 4-bit cache
+    const int32_t *block_table, *seq_lens;
+    float *o, *lse;
+    float *ws_o;                       // partials [slots][cols][D]: sums of weight * V ...
+    float2 *ws_ml;                     // ... and [slots][cols]: their reference exponent and sum of weights
+    int32_t *ws_prefix;                // [2 (batch + 1)]: the schedule, for the merge
+    unsigned int *ws_err;
+    int batch, q_len, hq, hkv, group, cols, cap;
+    int page_size, max_blocks, num_pages;   // contiguous: block_table null, page_size = s_max, num_pages = batch
+    uint32_t row_page, row_token, row_head; // cache row = page * row_page + slot * row_token + head * row_head
+    int window, sinks;                 // window 0: none
+    int team;                          // adjacent kv heads that a team of as many warps reads side by side
+    float scale_log2, v_scale;         // scale_log2 includes k_scale
+    int q_f16;
+};
+
+// What a request's new tokens see together.
+struct WindowReq {
+    int L, head, first, rows;
+};
+__device__ __forceinline__ WindowReq window_req(const WindowParams &p, int b, unsigned int *err)
+{
+    const int l = p.seq_lens ? p.seq_lens[b] : p.cap;
+    WindowReq r;
+    r.L = min(max(l, 0), p.cap);
+    if (err && r.L != l)
+        atomicOr(err, kErrLength);
+    r.head = r.first = 0;
+    if (p.window) {
+        const long long back = (long long)r.L - p.q_len - p.window + 1;
+        r.first = (int)min((long long)r.L, max((long long)p.sinks, back));
+        r.head = min(p.sinks, r.first);
+    }
+    r.rows = r.L - r.first + r.head;
+    return r;
+}
+__device__ __forceinline__ int window_pos(const WindowReq &r, int row) { return row < r.head ? row : row - r.head + r.first; }
+
+// Workers (teams of p.team warps) of a CTA of a call of this cost: no more
+// than there is work for, so that a short call spreads over all SMs.
+__device__ __forceinline__ int window_workers(long long cost, int grid, int most)
+{
+    const long long want = (cost + grid - 1) / grid;
+    return want < 1 ? 1 : want < most ? (int)want : most;
+}
+
+// Host side.
+struct WindowLaunch {
+    int grid;
+    size_t smem_optin;
+    cudaStream_t stream;
+};
+
+template <int D, int KV>
+cudaError_t launch_window_variant(const WindowParams &p, const WindowLaunch &c);
+
+#define FD_WINDOW_VARIANTS_D(X, D) X(D, kKvBf16) X(D, kKvF16) X(D, kKvE4m3) X(D, kKvE5m2) X(D, kKvE2m1)
+#define FD_WINDOW_VARIANTS(X) FD_WINDOW_VARIANTS_D(X, 64) FD_WINDOW_VARIANTS_D(X, 128) FD_WINDOW_VARIANTS_D(X, 256)
+#define FD_EXTERN_WINDOW(D, KV) extern template cudaError_t launch_window_variant<D, KV>(const WindowParams &, const WindowLaunch &);
+FD_WINDOW_VARIANTS(FD_EXTERN_WINDOW)
+#undef FD_EXTERN_WINDOW
+
+cudaError_t launch_window_merge(int head_dim, const WindowParams &p, int grid_ctas, int warps, float shift, cudaStream_t stream);
+
+}  // namespace fd

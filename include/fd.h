@@ -613,6 +613,138 @@ fd_status fd_tree_decode_paged(const void *q, const void *k_pages, const void *v
                                size_t workspace_bytes, const fd_options *opts, fd_stream_t stream);
 
 /*
+ * ---- Long contexts: a sliding window with sinks, and caches in 4 bits ----
+ *
+ * Decoding reads the whole cache for every token.  fd_window_decode reads less
+ * of it: the last `window` positions and the first `sinks` ones.  A 4-bit cache
+ * (fd_cache_write4, fd_decode4) makes what is read smaller: 9/16 byte an
+ * element.  Both can be had together.  The sources this library follows have no
+ * counterpart to these calls; the arithmetic of the attention is fd_decode's.
+ * They follow the conventions at the top of this file, and may be captured and
+ * replayed.
+ */
+
+/*
+ * A 4-bit cache.  Each row (one token's K or V of one kv head) is cut into
+ * blocks of 16 consecutive dims; an element is
+ *     code * s * t,
+ * code in E2M1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives), s the block's
+ * scale in E4M3 and t the tensor's scale (fd_options.k_scale or v_scale; 0
+ * means 1).  A byte holds two codes, the even dim in its low half.  The rows of
+ * a kv head lie together, so that short rows make long reads:
+ *     codes  [num_pages, num_kv_heads, page_size, head_dim / 2]
+ *     scales [num_pages, num_kv_heads, page_size, head_dim / 16]
+ * for pages, and for a contiguous cache the same with a page a request:
+ * [batch, num_kv_heads, s_max, ..].  Slots are numbered as for fd_cache_write
+ * (page * page_size + t, or b * s_max + t).  All four are device pointers,
+ * 16-byte aligned.
+ */
+typedef struct fd_cache4 {
+    uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+} fd_cache4;
+
+/*
+ * Write num_tokens new K and V rows into the slots of a 4-bit cache.  For a
+ * block with elements x_i, in fp32 arithmetic rounded to nearest:
+ *     s = E4M3(max |x_i| / (6 t))            nearest even, at most 448
+ *     code_i = E2M1(x_i / (s t))             nearest even, at most 6 in magnitude
+ * and all codes 0 where s is 0.  A block with a NaN gets s = NaN and codes 0,
+ * so every element of it reads as NaN; infinities become the largest code.
+ *   k_new, v_new, k_stride, v_stride, slot_map, device_status: as for
+ *                fd_cache_write (opts->dtype their type; negative slots are
+ *                skipped, slots >= num_slots too and reported).  Slots >= 0 must
+ *                differ: the row of a slot given twice is a mix of both.
+ *   page_size    tokens of a page (s_max for a contiguous cache); num_slots is a
+ *                multiple of it.
+ *   opts         NULL or options; dtype, k_scale and v_scale are used, kv_dtype
+ *                must be FD_KV_AS_Q.
+ * head_dim 64, 128 or 256.
+ */
+fd_status fd_cache_write4(const void *k_new, const void *v_new, long long k_stride, long long v_stride,
+                          const int64_t *slot_map, int num_tokens, int num_kv_heads, int head_dim,
+                          const fd_cache4 *cache, int page_size, long long num_slots, const fd_options *opts,
+                          unsigned int *device_status, fd_stream_t stream);
+
+/*
+ * Read rows of a 4-bit cache back into 16 bits: row i of k_out and v_out
+ * [num_tokens, Hkv, D] (type opts->dtype, token rows k_stride and v_stride
+ * elements apart, as for fd_cache_write's k_new) becomes the row of slot_map[i],
+ * code * s * t in fp32 rounded to nearest even.  The rows of negative slots, and
+ * of slots >= num_slots (reported), keep what they hold; a slot may be named
+ * more than once.  Other arguments as for fd_cache_write4.
+ */
+fd_status fd_cache_read4(const int64_t *slot_map, int num_tokens, int num_kv_heads, int head_dim,
+                         const fd_cache4 *cache, int page_size, long long num_slots, void *k_out, void *v_out,
+                         long long k_stride, long long v_stride, const fd_options *opts,
+                         unsigned int *device_status, fd_stream_t stream);
+
+/* Bytes of workspace that fd_window_decode, fd_decode4 and their paged forms
+ * need for a shape, whatever the lengths and the cache's type (21 MB for 8 query
+ * columns Hq/Hkv x q_len of head_dim 128); initialise it once with
+ * fd_workspace_init.  A workspace of one shape serves every shape with no more
+ * requests, no more columns and no larger head_dim.  Pure host function; 0 for
+ * shapes that no call accepts. */
+size_t fd_window_workspace_size(int batch, int num_q_heads, int num_kv_heads, int head_dim, int q_len);
+
+/*
+ * Decode attention through a sliding window with sinks over a contiguous
+ * cache.  The new token at position p (p = L_b - q_len + i for new token i)
+ * attends to position t when
+ *     t <= p  and  (t < sinks or t > p - window),
+ * that is to the last `window` positions with its own, and to the first `sinks`.
+ * O, LSE and the arguments are fd_decode's, and:
+ *   window       >= 1; sinks >= 0 (they may overlap, and pass the length).
+ *   workspace    at least fd_window_workspace_size(...) bytes (its error word is
+ *                read with fd_get_device_error).
+ *   opts         as for fd_decode; num_ctas is at most 160, and neither flags nor
+ *                wait_timeout_ns change the call (nothing in it waits).
+ * Positions that no new token of a request sees are not read: they may hold
+ * anything.  What a position holds does not reach the tokens that do not see it,
+ * not-a-numbers included.  A visible V element that is infinite makes its dim of
+ * the rows that see it infinite (NaN beside one of the other sign, or a NaN).
+ * Head groups, q_len, head_dim and batch as for fd_decode: G * q_len <= 16, but
+ * any of them with any cache.  Rows of the cache (positions x kv heads) are
+ * limited to 2^32 - 2, and num_kv_heads * batch * (visible positions / 16 + 2)
+ * to 2^31 (FD_ERR_UNSUPPORTED).  Results are bitwise the same from call to call
+ * (with the same num_ctas).  The first call of a shape on a device sets a kernel
+ * attribute: make it before a capture.
+ */
+fd_status fd_window_decode(const void *q, const void *k, const void *v, const int32_t *seq_lens_dev,
+                           const int32_t *seq_lens_host, int batch, int num_q_heads, int num_kv_heads, int head_dim,
+                           int s_max, int window, int sinks, float scale, float *o, float *lse, void *workspace,
+                           size_t workspace_bytes, const fd_options *opts, fd_stream_t stream);
+
+/* fd_window_decode over a paged cache: k_pages, v_pages, block_table,
+ * max_blocks_per_seq and num_pages as for fd_decode_paged, any page_size >= 1.
+ * Only the entries of pages that hold a visible position are read, so the pages
+ * behind the window can be given back and their entries hold anything. */
+fd_status fd_window_decode_paged(const void *q, const void *k_pages, const void *v_pages, const int32_t *block_table,
+                                 int max_blocks_per_seq, const int32_t *seq_lens_dev, const int32_t *seq_lens_host,
+                                 int batch, int num_q_heads, int num_kv_heads, int head_dim, int page_size,
+                                 int num_pages, int window, int sinks, float scale, float *o, float *lse,
+                                 void *workspace, size_t workspace_bytes, const fd_options *opts, fd_stream_t stream);
+
+/*
+ * Decode attention over a contiguous 4-bit cache (fd_cache4, s_max tokens a
+ * request): fd_window_decode's arguments and results, except that window 0 means
+ * every position up to the token's own (sinks is then ignored), and that
+ * opts->kv_dtype must be FD_KV_AS_Q.  opts->k_scale and v_scale are the tensors'
+ * scales t.  The codes' values enter the products exactly.
+ */
+fd_status fd_decode4(const void *q, const fd_cache4 *cache, const int32_t *seq_lens_dev, const int32_t *seq_lens_host,
+                     int batch, int num_q_heads, int num_kv_heads, int head_dim, int s_max, int window, int sinks,
+                     float scale, float *o, float *lse, void *workspace, size_t workspace_bytes, const fd_options *opts,
+                     fd_stream_t stream);
+
+/* fd_decode4 over a paged 4-bit cache: block_table, max_blocks_per_seq and
+ * num_pages as for fd_decode_paged, any page_size >= 1. */
+fd_status fd_decode4_paged(const void *q, const fd_cache4 *cache, const int32_t *block_table, int max_blocks_per_seq,
+                           const int32_t *seq_lens_dev, const int32_t *seq_lens_host, int batch, int num_q_heads,
+                           int num_kv_heads, int head_dim, int page_size, int num_pages, int window, int sinks,
+                           float scale, float *o, float *lse, void *workspace, size_t workspace_bytes,
+                           const fd_options *opts, fd_stream_t stream);
+
+/*
  * Read and clear the sticky device-error word of a workspace: FD_OK,
  * FD_ERR_TIMEOUT or FD_ERR_DEVICE_INPUT (timeout wins if both happened).
  * After FD_ERR_TIMEOUT the outputs of the failed call are undefined; the
