@@ -17,15 +17,16 @@ bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 
 bool scale_ok(float x) { return x == 0.f || (x > 0.f && x < __builtin_huge_valf()); }
 
+// The counts lie at the same place for every shape: each call leaves them at 0.
 struct WindowWorkspace {
-    size_t prefix, ml, o, total;
+    size_t counts, ml, o, total;
 };
-WindowWorkspace window_workspace(int batch, int cols, int d)
+WindowWorkspace window_workspace(int cols, int d)
 {
     const size_t slots = 2 * (size_t)kWindowMaxCtas * kWindowMaxWarps;
     WindowWorkspace w;
-    w.prefix = 256;
-    w.ml = align_up(w.prefix + 2 * sizeof(int32_t) * ((size_t)batch + 1), 256);
+    w.counts = 256;
+    w.ml = align_up(w.counts + sizeof(unsigned int) * slots / 2, 256);
     w.o = align_up(w.ml + sizeof(float2) * slots * cols, 256);
     w.total = align_up(w.o + sizeof(float) * slots * cols * d, 256);
     return w;
@@ -107,6 +108,7 @@ fd_status run(const WindowCall &a)
     p.cols = p.group * q_len;
     p.cap = (int)cap;
     p.page_size = a.page_size;
+    p.page_shift = a.page_size > 0 && (a.page_size & (a.page_size - 1)) == 0 ? __builtin_ctz((unsigned)a.page_size) : -1;
     p.max_blocks = a.max_blocks;
     p.num_pages = a.num_pages;
     p.row_page = (uint32_t)a.page_size * (uint32_t)a.hkv;
@@ -115,7 +117,11 @@ fd_status run(const WindowCall &a)
     p.window = a.window;
     p.sinks = a.window ? a.sinks : 0;
     const bool scaled = kv >= kKvE4m3;
-    p.scale_log2 = a.scale * (scaled && opts && opts->k_scale != 0.f ? opts->k_scale : 1.f) * 1.4426950408889634f;
+    const float scale = a.scale * (scaled && opts && opts->k_scale != 0.f ? opts->k_scale : 1.f);
+    p.negate_q = scale < 0.f;
+    p.scale_log2 = (p.negate_q ? -scale : scale) * 1.4426950408889634f;
+    if (p.scale_log2 < kWindowLeastScale)
+        p.scale_log2 = kWindowLeastScale;
     p.v_scale = scaled && opts && opts->v_scale != 0.f ? opts->v_scale : 1.f;
     p.q_f16 = f16;
     // Rows of a kv head are hkv rows apart unless the cache is in 4 bits: where they are short, adjacent
@@ -128,34 +134,25 @@ fd_status run(const WindowCall &a)
         else if (row <= 128 && a.hkv % 2 == 0)
             p.team = 2;
     }
-    const WindowWorkspace w = window_workspace(a.batch, p.cols, a.d);
+    const WindowWorkspace w = window_workspace(p.cols, a.d);
     uint8_t *ws = static_cast<uint8_t *>(a.ws);
     p.ws_err = reinterpret_cast<unsigned int *>(ws);
-    p.ws_prefix = reinterpret_cast<int32_t *>(ws + w.prefix);
+    p.ws_counts = reinterpret_cast<unsigned int *>(ws + w.counts);
     p.ws_ml = reinterpret_cast<float2 *>(ws + w.ml);
     p.ws_o = reinterpret_cast<float *>(ws + w.o);
     WindowLaunch c;
     c.grid = opts && opts->num_ctas > 0 ? opts->num_ctas : dev.sms < kWindowMaxCtas ? dev.sms : kWindowMaxCtas;
     c.smem_optin = (size_t)dev.smem_optin;
     c.stream = a.stream;
-    cudaEvent_t ev0 = opts ? static_cast<cudaEvent_t>(opts->split_start_event) : nullptr;
-    cudaEvent_t ev1 = opts ? static_cast<cudaEvent_t>(opts->split_end_event) : nullptr;
-    if (ev0 && !record_event(ev0, c.stream))
-        return FD_ERR_CUDA;
+    c.start_event = opts ? static_cast<cudaEvent_t>(opts->split_start_event) : nullptr;
+    c.end_event = opts ? static_cast<cudaEvent_t>(opts->split_end_event) : nullptr;
     cudaError_t e = cudaErrorInvalidValue;
-    int warps = 0;
-    float shift = 0.f;
 #define FD_PICK_WINDOW(D, KV)                       \
-    if (a.d == D && kv == KV) {                     \
-        e = launch_window_variant<D, KV>(p, c);     \
-        warps = WindowCfg<D, KV>::kWarps;           \
-        shift = WindowCfg<D, KV>::kShift;           \
-    }
+    if (a.d == D && kv == KV)                       \
+        e = launch_window_variant<D, KV>(p, c);
     FD_WINDOW_VARIANTS(FD_PICK_WINDOW)
 #undef FD_PICK_WINDOW
-    if (e != cudaSuccess || (ev1 && !record_event(ev1, c.stream)))
-        return FD_ERR_CUDA;
-    return launch_window_merge(a.d, p, c.grid, warps, shift, c.stream) == cudaSuccess ? FD_OK : FD_ERR_CUDA;
+    return e == cudaSuccess ? FD_OK : FD_ERR_CUDA;
 }
 
 }  // namespace
@@ -171,7 +168,7 @@ size_t fd_window_workspace_size(int batch, int num_q_heads, int num_kv_heads, in
         num_kv_heads > 65535 || q_len < 1 || (long long)(num_q_heads / num_kv_heads) * q_len > kWindowMaxColumns ||
         (head_dim != 64 && head_dim != 128 && head_dim != 256))
         return 0;
-    return window_workspace(batch, num_q_heads / num_kv_heads * q_len, head_dim).total;
+    return window_workspace(num_q_heads / num_kv_heads * q_len, head_dim).total;
 }
 
 fd_status fd_window_decode(const void *q, const void *k, const void *v, const int32_t *seq_lens_dev,

@@ -28,24 +28,27 @@ constexpr int kWindowMaxColumns = 16;
 // flushes its outputs there.
 constexpr int kWindowSegCost = 1;
 
-// Shape of the split kernel for head dim D and a cache of type KV.
-template <int D_, int KV_>
+// Shape of the split kernel for head dim D, a cache of type KV and MMAs of 8 NT
+// query columns.
+template <int D_, int KV_, int NT_>
 struct WindowCfg {
-    static constexpr int D = D_, KV = KV_;
+    static constexpr int D = D_, KV = KV_, NT = NT_;
     static constexpr bool kFp4 = KV == kKvE2m1, kFp8 = KV == kKvE4m3 || KV == kKvE5m2;
     static constexpr bool kF16 = KV != kKvBf16;              // type of the MMAs
     static constexpr bool kInf = KV == kKvBf16 || KV == kKvF16 || KV == kKvE5m2;   // types with infinities
     static constexpr int kParts = kF16 ? 2 : 3;              // 16-bit parts of a softmax weight
-    // weights are at most 2^kShift, so that fp16 remainders of small ones keep their bits
-    static constexpr float kShift = kF16 ? 14.f : 0.f;
+    // The reference of a column's weights is a score of the column; scores may pass it by kSlack (in log2) before it is
+    // moved, and it has the weight 2^kShift: fp16 remainders of small weights keep their bits, and 2^15 is not passed.
+    static constexpr float kShift = kF16 ? 14.f : 0.f, kSlack = 1.f;
     static constexpr int kRow = kFp4 ? D / 2 : kFp8 ? D : 2 * D;   // bytes of a row
     static constexpr int kGran = kRow / 16;                  // 16-byte pieces of a row
     static constexpr int kScaleRow = kFp4 ? D / 16 : 0;      // bytes of a row's block scales
     static constexpr int kTile = kRow <= 64 || (kRow <= 128 && !kFp4) ? 32 : 16;   // rows of a tile
     static constexpr int kStage = 2 * kTile * (kRow + kScaleRow);
-    static constexpr int kWarps = kStage <= 2400 ? 16 : kStage <= 4800 && D < 256 ? 12 : kStage <= 8192 ? 8 : 4;
-    static constexpr int kStages = kStage <= 2400 || (kStage <= 4800 && D == 256) ? 4 : 3;
-    static constexpr int kRing = kStage * kStages;           // bytes of a warp's tiles
+    static constexpr int kWarps = kStage <= 4800 && D < 256 && NT == 1 ? 12 : kStage <= 8192 ? 8 : 4;
+    static constexpr int kSums = (int)sizeof(float) * NT * 8 * (D + 2);   // bytes of a warp's sums, left in its ring at the end
+    static constexpr int kStages = kSums <= 2 * kStage ? 2 : (kSums + kStage - 1) / kStage;
+    static constexpr int kRing = (kStage + 16) * kStages;    // bytes of a warp's tiles, and what each is
 };
 
 struct WindowParams {
@@ -55,15 +58,16 @@ struct WindowParams {
     float *o, *lse;
     float *ws_o;                       // partials [slots][cols][D]: sums of weight * V ...
     float2 *ws_ml;                     // ... and [slots][cols]: their reference exponent and sum of weights
-    int32_t *ws_prefix;                // [2 (batch + 1)]: the schedule, for the merge
+    unsigned int *ws_counts;           // of a segment that several CTAs have: partials written; by its first worker, 0 between calls
     unsigned int *ws_err;
     int batch, q_len, hq, hkv, group, cols, cap;
     int page_size, max_blocks, num_pages;   // contiguous: block_table null, page_size = s_max, num_pages = batch
+    int page_shift;                    // page_size = 2^page_shift, or -1
     uint32_t row_page, row_token, row_head; // cache row = page * row_page + slot * row_token + head * row_head
     int window, sinks;                 // window 0: none
     int team;                          // adjacent kv heads that a team of as many warps reads side by side
-    float scale_log2, v_scale;         // scale_log2 includes k_scale
-    int q_f16;
+    float scale_log2, v_scale;         // scale_log2 includes k_scale; > 0 (a negative scale's sign goes to q)
+    int q_f16, negate_q;
 };
 
 // What a request's new tokens see together.
@@ -96,11 +100,28 @@ __device__ __forceinline__ int window_workers(long long cost, int grid, int most
     return want < 1 ? 1 : want < most ? (int)want : most;
 }
 
+// A scale of 0 becomes this one, so that a hidden score (-inf) keeps its
+// weight of 0; scores below 1e30 are still 0.
+constexpr float kWindowLeastScale = 1e-37f;
+
+// fd_sched.h's Schedule with divisions of 32 bits where they do: a short call
+// waits for them (a 64-bit division costs some 100 instructions).
+struct WindowSchedule : Schedule {
+    __device__ __forceinline__ static long long quotient(long long x, long long y)
+    {
+        return (unsigned long long)x >> 32 == 0 && (unsigned long long)y >> 32 == 0 ? (long long)((uint32_t)x / (uint32_t)y) : x / y;
+    }
+    __device__ __forceinline__ int cta_at(long long pos) const { return (int)quotient(pos * ctas(), cost()); }
+    // cost position at which CTA c's tiles begin
+    __device__ __forceinline__ long long begin(int c) const { return quotient(cost() * c + ctas() - 1, ctas()); }
+};
+
 // Host side.
 struct WindowLaunch {
     int grid;
     size_t smem_optin;
     cudaStream_t stream;
+    cudaEvent_t start_event, end_event;   // recorded around the split kernel, or null
 };
 
 template <int D, int KV>
@@ -112,6 +133,6 @@ cudaError_t launch_window_variant(const WindowParams &p, const WindowLaunch &c);
 FD_WINDOW_VARIANTS(FD_EXTERN_WINDOW)
 #undef FD_EXTERN_WINDOW
 
-cudaError_t launch_window_merge(int head_dim, const WindowParams &p, int grid_ctas, int warps, float shift, cudaStream_t stream);
+bool record_event(cudaEvent_t ev, cudaStream_t stream);   // fd_api.cu
 
 }  // namespace fd

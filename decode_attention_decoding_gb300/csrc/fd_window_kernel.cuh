@@ -33,16 +33,13 @@ __device__ __forceinline__ void cp_async_wait()
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
-// Copy BYTES from src, or write zeros (size 0).
 template <int BYTES>
-__device__ __forceinline__ void cp_async_or_zero(uint32_t dst, const void *src, uint32_t size, uint64_t policy)
+__device__ __forceinline__ void cp_async_small(uint32_t dst, const void *src, uint64_t policy)
 {
     if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src), "r"(size), "l"(policy)
-                     : "memory");
+        cp_async_16(dst, src, policy);
     else
-        asm volatile("cp.async.ca.shared.global.L2::cache_hint [%0], [%1], %4, %2, %3;" ::"r"(dst), "l"(src), "r"(size), "l"(policy),
-                     "n"(BYTES)
+        asm volatile("cp.async.ca.shared.global.L2::cache_hint [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "l"(policy), "n"(BYTES)
                      : "memory");
 }
 
@@ -65,15 +62,24 @@ __device__ __forceinline__ uint32_t lds8(uint32_t addr)
     return v;
 }
 
-// The four bytes of w, each two E2M1 codes (the first in the low half), as
-// four pairs of fp16.
-__device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t w, uint32_t (&r)[4])
+// Byte I of w, two E2M1 codes (the first in the low half), as a pair of fp16.
+template <int I>
+__device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t w)
 {
-    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-        : "r"(w));
+    uint32_t r;
+    if constexpr (I == 0)
+        asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\t}" : "=r"(r) : "r"(w));
+    else if constexpr (I == 1)
+        asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}" : "=r"(r) : "r"(w));
+    else if constexpr (I == 2)
+        asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, c;\n\t}" : "=r"(r) : "r"(w));
+    else
+        asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, d;\n\t}" : "=r"(r) : "r"(w));
+    return r;
+}
+__device__ __forceinline__ uint32_t e2m1x2_at(uint32_t w, int i)   // i known to the compiler
+{
+    return i == 0 ? e2m1x2_to_f16x2<0>(w) : i == 1 ? e2m1x2_to_f16x2<1>(w) : i == 2 ? e2m1x2_to_f16x2<2>(w) : e2m1x2_to_f16x2<3>(w);
 }
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b)
 {
@@ -90,6 +96,19 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b)
     else
         asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
+}
+// As mma_16816 with C = 0.
+template <bool F16>
+__device__ __forceinline__ void mma_16816_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    if constexpr (F16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+                     : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+                     : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 // Two fp32 values rounded towards zero to 16 bits.
 template <bool F16>
@@ -113,29 +132,65 @@ __device__ __forceinline__ int window_row(int g) { return g & 1 ? 4 + ((g >> 1) 
 template <int GRAN>
 __device__ __forceinline__ int window_swizzle(int r) { return (((r & 1) << 2) | (r & 2)) & (GRAN - 1); }
 
-// One warp's place in the schedule.
-struct WindowCursor {
-    int b, h, j, nb;     // request, launch head, tile of the segment, tiles of a segment
-    WindowReq req;
+// Where a lane finds its pieces in a tile, in bytes: of K row window_row(g), the even pieces x (place ke + 64 x) and the
+// odd ones (ko + 64 x); of V the rows c and 4 + (c ^ 1) (v[] + 128 x); of the block scales of either.  Rows 8 further are
+// 8 rows of bytes further.
+template <class C>
+struct WindowPlaces {
+    uint32_t ke, ko, ks, v[2], vs[2];
+    __device__ __forceinline__ WindowPlaces(int g, int c)
+    {
+        constexpr int kRow = C::kRow, kLane = kRow / 8;
+        const int r = window_row(g), sw = window_swizzle<C::kGran>(r);
+        ke = ko = r * kRow + (kRow >= 64 ? (c ^ (sw & 3)) << 4 : 8 * c);
+        if (kRow >= 128) {
+            ke += 16 * (sw & 4);
+            ko -= 16 * (sw & 4);
+        }
+        ks = r * C::kScaleRow + (kRow >= 64 ? 2 * c : c);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int row = i ? 4 + (c ^ 1) : c, s = window_swizzle<C::kGran>(row);
+            v[i] = row * kRow + (kLane >= 16 ? (g ^ s) << 4 : kLane == 8 ? (((g >> 1) ^ s) << 4) + 8 * (g & 1) : 4 * g);
+            vs[i] = row * C::kScaleRow + (C::D == 256 ? 2 * g : C::D == 128 ? g : g >> 1);
+        }
+    }
 };
 
-template <class C, int NT, bool PACK>
+// A tile's flags; above them its rows.
+enum : int { kTilePlain = 1, kTileFirst = 2, kTileLast = 4, kTileN = 8 };   // kTileN: a shift
+
+__device__ __forceinline__ void sts128(uint32_t addr, int x, int y, int z, int w)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+// One warp's place in the schedule.
+struct WindowCursor {
+    int b, h, j, nb;        // request, launch head, tile of the segment, tiles of a segment
+    int rows, head, skip;   // row v of the request is position v, + skip from row head on
+    const int32_t *pages;   // the request's block table
+};
+
+template <class C, bool PACK>
 struct WindowWarp {
-    static constexpr int D = C::D, KV = C::KV, kTile = C::kTile, kRow = C::kRow, kGran = C::kGran;
+    static constexpr int NT = C::NT, D = C::D, KV = C::KV, kTile = C::kTile, kRow = C::kRow, kGran = C::kGran;
     static constexpr int KT = kTile / 16;          // k steps of a tile
     static constexpr int kSteps = D / 16;          // k steps of a row, and 16-dim blocks of the output
     static constexpr int kParts = PACK ? 1 : C::kParts;   // MMAs a block (PACK: both parts in one)
-    static constexpr float kShift = C::kShift;
+    static constexpr float kShift = C::kShift, kSlack = C::kSlack;
     static constexpr int kColMask = PACK ? 3 : 8 * NT - 1;
 
     uint32_t qf[NT][kSteps][2];
     float mult[NT][2];         // score of column 2c, 2c + 1 of an MMA's eight -> log2 units
     float acc[kSteps][NT][4];
-    float m[NT][2], l[NT][2];
+    // of columns 2c, 2c + 1: what a score (log2 units) may not pass, kShift - the reference, and the sum of weights
+    float limit[NT][2], offset[NT][2], l[NT][2];
 
     // Load the query of segment (b, head) as the B operand of S^T.
     __device__ __forceinline__ void start(const WindowParams &p, int b, int head, int g, int c)
     {
+        const uint32_t sign = p.negate_q ? 0x80008000u : 0u;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int col = (nt * 8 + g) & kColMask;
@@ -150,8 +205,8 @@ struct WindowWarp {
                 uint2 w = make_uint2(0u, 0u);
                 if (real)
                     w = *reinterpret_cast<const uint2 *>(src + dim);
-                qf[nt][s][0] = w.x;
-                qf[nt][s][1] = w.y;
+                qf[nt][s][0] = w.x ^ sign;
+                qf[nt][s][1] = w.y ^ sign;
             }
             float f = p.scale_log2;
             if (KV >= kKvE4m3 && !p.q_f16) {
@@ -177,11 +232,12 @@ struct WindowWarp {
                         const float2 x = bf16x2_to_float2(qf[nt][s][w]);
                         qf[nt][s][w] = pack_f16x2(x.x * up, x.y * up);
                     }
-                f *= down;
+                f = fmaxf(f * down, 1.1754944e-38f);
             }
             mult[nt][0] = __shfl_sync(0xffffffffu, f, 8 * c);
             mult[nt][1] = __shfl_sync(0xffffffffu, f, 8 * c + 4);
-            m[nt][0] = m[nt][1] = -__builtin_huge_valf();
+            limit[nt][0] = limit[nt][1] = -__builtin_huge_valf();
+            offset[nt][0] = offset[nt][1] = kShift;
             l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
             for (int s = 0; s < kSteps; ++s)
@@ -191,10 +247,10 @@ struct WindowWarp {
         }
     }
 
-    // S^T of a tile in log2 units: sc[kt][nt] = rows window_row(g), + 8 of 16-row step kt times columns 2c, 2c + 1.
-    __device__ __forceinline__ void scores(uint32_t k, uint32_t ks, int g, int c, float (&sc)[KT][NT][4]) const
+    // S^T of a tile, without the scale: sc[kt][nt] = rows window_row(g), + 8 of 16-row step kt times columns 2c, 2c + 1.
+    __device__ __forceinline__ void scores(const WindowPlaces<C> &at, uint32_t k, uint32_t ks, float (&sc)[KT][NT][4]) const
     {
-        const int r = window_row(g), sw = window_swizzle<kGran>(r);
+        const uint32_t ke = k + at.ke, ko = k + at.ko, kscale = ks + at.ks;
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt) {
 #pragma unroll
@@ -208,44 +264,37 @@ struct WindowWarp {
                 uint32_t a[2][4], s16[2][2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const uint32_t row = (uint32_t)(kt * 16 + r + 8 * i);
+                    const uint32_t from = (x & 1 ? ko : ke) + (kt * 16 + 8 * i) * kRow + 64 * x;
                     if constexpr (kRow >= 64) {
-                        const uint4 w = lds128(k + row * kRow + (((c + 4 * x) ^ sw) << 4));
+                        const uint4 w = lds128(from);
                         a[i][0] = w.x; a[i][1] = w.y; a[i][2] = w.z; a[i][3] = w.w;
                     } else {
-                        const uint2 w = lds64(k + row * kRow + 8 * c);
+                        const uint2 w = lds64(from);
                         a[i][0] = w.x; a[i][1] = w.y;
                     }
                     if constexpr (C::kFp4) {
-                        if constexpr (kRow >= 64) {
-                            const uint32_t b = fp8x2_to_f16x2<kKvE4m3>((uint16_t)lds16(ks + row * C::kScaleRow + 2 * (c + 4 * x)));
-                            s16[i][0] = prmt(b, b, 0x1010);
-                            s16[i][1] = prmt(b, b, 0x3232);
-                        } else {
-                            const uint32_t b = fp8x2_to_f16x2<kKvE4m3>((uint16_t)lds8(ks + row * C::kScaleRow + c));
-                            s16[i][0] = prmt(b, b, 0x1010);
-                        }
+                        const uint32_t place = kscale + (kt * 16 + 8 * i) * C::kScaleRow + 8 * x;
+                        const uint32_t b = fp8x2_to_f16x2<kKvE4m3>((uint16_t)(kRow >= 64 ? lds16(place) : lds8(place)));
+                        s16[i][0] = prmt(b, b, 0x1010);
+                        s16[i][1] = prmt(b, b, 0x3232);
                     }
                 }
                 if constexpr (C::kFp4) {
 #pragma unroll
-                    for (int w = 0; w < kWords; ++w) {
-                        uint32_t f[2][4];
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            e2m1x8_to_f16x2(a[i][w], f[i]);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                f[i][e] = hmul2(f[i][e], s16[i][w / 2]);
-                        }
+                    for (int w = 0; w < kWords; ++w)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const int s = (x * kWords + w) * 2 + e;
+                            uint32_t f[2][2];
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                                for (int y = 0; y < 2; ++y)
+                                    f[i][y] = hmul2(e2m1x2_at(a[i][w], 2 * e + y), s16[i][w / 2]);
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
-                                mma_16816<C::kF16>(sc[kt][nt], f[0][2 * e], f[1][2 * e], f[0][2 * e + 1], f[1][2 * e + 1], qf[nt][s][0], qf[nt][s][1]);
+                                mma_16816<C::kF16>(sc[kt][nt], f[0][0], f[1][0], f[0][1], f[1][1], qf[nt][s][0], qf[nt][s][1]);
                         }
-                    }
                 } else if constexpr (C::kFp8) {
 #pragma unroll
                     for (int w = 0; w < 4; ++w) {
@@ -264,14 +313,21 @@ struct WindowWarp {
                                                qf[nt][x * 2 + w][0], qf[nt][x * 2 + w][1]);
                 }
             }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    sc[kt][nt][e] *= mult[nt][e & 1];
         }
     }
 
+    // Hide the rows from n on.
+    __device__ __forceinline__ void cut(int n, int g, float (&sc)[KT][NT][4]) const
+    {
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (kt * 16 + window_row(g) + 8 * (e / 2) >= n)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        sc[kt][nt][e] = -__builtin_huge_valf();
+    }
     // Hide what a column's token does not see in the tile from row `row0` of the request.
     __device__ __forceinline__ void mask(const WindowParams &p, const WindowReq &req, int row0, int g, int c, float (&sc)[KT][NT][4]) const
     {
@@ -297,36 +353,61 @@ struct WindowWarp {
         return v < req.rows && pos <= own && (!p.window || pos < p.sinks || own - pos < p.window);
     }
 
-    // The scores' softmax weights against the running maximum, in parts, as the B operand of O^T: pf[kt][part][nt][2];
-    // alpha: the factor of what was summed before.
-    __device__ __forceinline__ void weights(float (&sc)[KT][NT][4], int c, uint32_t (&pf)[KT][kParts][NT][2], float (&alpha)[NT][2])
+    // Move the references up to the tile's scores if one passes its limit, which is rare after the first tiles.
+    __device__ __forceinline__ void rescale(const float (&sc)[KT][NT][4])
+    {
+        float top[NT][2];
+        bool over = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float x = fmaxf(sc[0][nt][e], sc[0][nt][e + 2]);
+#pragma unroll
+                for (int kt = 1; kt < KT; ++kt)
+                    x = fmaxf(x, fmaxf(sc[kt][nt][e], sc[kt][nt][e + 2]));
+                top[nt][e] = x * mult[nt][e];
+                over = over || top[nt][e] > limit[nt][e];
+            }
+        if (!__any_sync(0xffffffffu, over))
+            return;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float x = top[nt][e];
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1)
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
+                const float was = limit[nt][e] - kSlack, now = fmaxf(was, x);
+                const float ref = now == -__builtin_huge_valf() ? 0.f : now;
+                // at least fp32's least normal number: an infinite sum stays infinite
+                const float alpha = fmaxf(exp2_approx(was - ref), 1.1754944e-38f);
+                limit[nt][e] = now + kSlack;
+                offset[nt][e] = kShift - ref;
+                l[nt][e] *= alpha;
+#pragma unroll
+                for (int s = 0; s < kSteps; ++s) {
+                    acc[s][nt][e] *= alpha;
+                    acc[s][nt][e + 2] *= alpha;
+                }
+            }
+    }
+    // The reference of a column, -inf if nothing was seen.
+    __device__ __forceinline__ float reference(int nt, int e) const { return limit[nt][e] - kSlack; }
+
+    // The scores' softmax weights in parts, as the B operand of O^T: pf[kt][part][nt][2].  Where V may hold infinities,
+    // no part is less than `least`: an infinity times a part that is 0 would be NaN.
+    __device__ __forceinline__ void weights(const float (&sc)[KT][NT][4], uint32_t least, int c, uint32_t (&pf)[KT][kParts][NT][2])
     {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            float ref[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float top = -__builtin_huge_valf();
-#pragma unroll
-                for (int kt = 0; kt < KT; ++kt) {
-                    top = fmaxf(top, fmaxf(sc[kt][nt][e], sc[kt][nt][e + 2]));
-                }
-#pragma unroll
-                for (int off = 4; off < 32; off <<= 1)
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-                const float now = fmaxf(m[nt][e], top);
-                ref[e] = now == -__builtin_huge_valf() ? 0.f : now;
-                // at least fp32's least normal number: an infinite sum stays infinite
-                alpha[nt][e] = fmaxf(exp2_approx(m[nt][e] - ref[e]), 1.1754944e-38f);
-                m[nt][e] = now;
-                l[nt][e] *= alpha[nt][e];
-                ref[e] -= kShift;
-            }
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
                 for (int a = 0; a < 2; ++a) {
-                    float x = exp2_approx(sc[kt][nt][2 * a] - ref[0]), y = exp2_approx(sc[kt][nt][2 * a + 1] - ref[1]);
+                    float x = exp2_approx(fmaf(sc[kt][nt][2 * a], mult[nt][0], offset[nt][0]));
+                    float y = exp2_approx(fmaf(sc[kt][nt][2 * a + 1], mult[nt][1], offset[nt][1]));
                     l[nt][0] += x;
                     l[nt][1] += y;
                     if constexpr (PACK) {
@@ -336,7 +417,7 @@ struct WindowWarp {
                         const uint32_t rest = pack_f16x2(x - top.x, y - top.y);
                         w = c & 2 ? rest : w;
                         if constexpr (C::kInf)
-                            w = max2<true>(w, 0x00010001u);
+                            w = max2<true>(w, least);
                         pf[kt][0][nt][a] = movmatrix_trans(w);
                     } else {
 #pragma unroll
@@ -350,10 +431,8 @@ struct WindowWarp {
                                 x -= top.x;
                                 y -= top.y;
                             }
-                            // an infinite V element times a part that is 0 would be NaN: parts of what is seen
-                            // are at least 2^-38 (fp16) or 2^-126 of the largest weight
                             if constexpr (C::kInf)
-                                w = max2<C::kF16>(w, C::kF16 ? 0x00010001u : 0x00800080u);
+                                w = max2<C::kF16>(w, least);
                             pf[kt][part][nt][a] = movmatrix_trans(w);
                         }
                     }
@@ -361,36 +440,13 @@ struct WindowWarp {
         }
     }
 
-    // acc = acc * alpha + V^T P^T.  TOKEN: only the weights of token `token`'s columns, and of V only the rows that it
-    // sees, whatever the others hold.
-    template <bool TOKEN>
-    __device__ __forceinline__ void values(const WindowParams &p, const WindowReq &req, int row0, int token, uint32_t v, uint32_t vs,
-                                           int g, int c, const uint32_t (&pin)[KT][kParts][NT][2], const float (&alpha)[NT][2])
+    // acc += V^T P^T
+    __device__ __forceinline__ void values(const WindowPlaces<C> &at, uint32_t v, uint32_t vs, const uint32_t (&pf)[KT][kParts][NT][2])
     {
+        const uint32_t from[2] = {v + at.v[0], v + at.v[1]}, scale[2] = {vs + at.vs[0], vs + at.vs[1]};
         constexpr int kLane = kRow / 8;                        // bytes of a row that a lane takes
         constexpr int kLoad = kLane < 16 ? kLane : 16, kPieces = kLane / kLoad, kWords = kLoad / 4;
         constexpr int kBlocks = C::kFp4 ? 4 : C::kFp8 ? 2 : 1; // 16-dim output blocks of a word
-        const int r[4] = {c, 4 + (c ^ 1), 8 + c, 12 + (c ^ 1)};
-        uint32_t pf[KT][kParts][NT][2], keep[KT][2];
-#pragma unroll
-        for (int kt = 0; kt < KT; ++kt) {
-#pragma unroll
-            for (int part = 0; part < kParts; ++part)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const bool mine = !TOKEN || ((nt * 8 + g) & kColMask) / p.group == token;
-                    pf[kt][part][nt][0] = mine ? pin[kt][part][nt][0] : 0u;
-                    pf[kt][part][nt][1] = mine ? pin[kt][part][nt][1] : 0u;
-                }
-            if constexpr (TOKEN) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int own = req.L - p.q_len + token;
-                    keep[kt][i] = (visible(p, req, row0 + kt * 16 + r[2 * i], own) ? 0x0000FFFFu : 0u) |
-                                  (visible(p, req, row0 + kt * 16 + r[2 * i + 1], own) ? 0xFFFF0000u : 0u);
-                }
-            }
-        }
 #pragma unroll
         for (int x = 0; x < kPieces; ++x) {
             uint32_t w[KT][4][kWords];
@@ -399,99 +455,155 @@ struct WindowWarp {
             for (int kt = 0; kt < KT; ++kt) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const uint32_t at = v + (uint32_t)(kt * 16 + r[i]) * kRow;
-                    const int sw = window_swizzle<kGran>(r[i]);
+                    const uint32_t place = from[i & 1] + (kt * 16 + 8 * (i / 2)) * kRow + 128 * x;
                     if constexpr (kLoad == 16) {
-                        const uint4 y = lds128(at + (((g + 8 * x) ^ sw) << 4));
+                        const uint4 y = lds128(place);
                         w[kt][i][0] = y.x; w[kt][i][1] = y.y; w[kt][i][2] = y.z; w[kt][i][3] = y.w;
                     } else if constexpr (kLoad == 8) {
-                        const uint2 y = lds64(at + ((((g >> 1)) ^ sw) << 4) + 8 * (g & 1));
+                        const uint2 y = lds64(place);
                         w[kt][i][0] = y.x; w[kt][i][1] = y.y;
                     } else
-                        w[kt][i][0] = lds32(at + 4 * g);
+                        w[kt][i][0] = lds32(place);
                 }
                 if constexpr (C::kFp4) {
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const uint32_t a = vs + (uint32_t)(kt * 16 + r[2 * i]) * C::kScaleRow, b = vs + (uint32_t)(kt * 16 + r[2 * i + 1]) * C::kScaleRow;
+                        const uint32_t a = scale[0] + (kt * 16 + 8 * i) * C::kScaleRow, b = scale[1] + (kt * 16 + 8 * i) * C::kScaleRow;
                         if constexpr (D == 256) {
-                            const uint32_t y = prmt(lds16(a + 2 * g), lds16(b + 2 * g), 0x5140);
+                            const uint32_t y = prmt(lds16(a), lds16(b), 0x5140);
                             s16[kt][i][0] = fp8x2_to_f16x2<kKvE4m3>(lo16(y));
                             s16[kt][i][1] = fp8x2_to_f16x2<kKvE4m3>(hi16(y));
                         } else {
-                            const int blk = D == 128 ? g : g >> 1;
-                            s16[kt][i][0] = fp8x2_to_f16x2<kKvE4m3>((uint16_t)(lds8(a + blk) | lds8(b + blk) << 8));
+                            s16[kt][i][0] = fp8x2_to_f16x2<kKvE4m3>((uint16_t)(lds8(a) | lds8(b) << 8));
                         }
                     }
                 }
             }
 #pragma unroll
             for (int j = 0; j < kWords; ++j) {
-                uint32_t a[KT][kBlocks][4];
+                // the words of two rows each, paired row by row: even and odd dims apart (4 bits), or as bytes and halves
+                uint32_t y[KT][4];
 #pragma unroll
-                for (int kt = 0; kt < KT; ++kt) {
-                    const uint32_t w0 = w[kt][0][j], w1 = w[kt][1][j], w2 = w[kt][2][j], w3 = w[kt][3][j];
-                    if constexpr (C::kFp4) {
-                        // even and odd dims of two rows side by side, then to fp16
-                        constexpr uint32_t kLo = 0x0F0F0F0Fu;
-                        uint32_t f[4];
+                for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const uint32_t y = i ? w2 : w0, z = i ? w3 : w1, s = s16[kt][i][D == 256 ? j / 2 : 0];
-                            e2m1x8_to_f16x2((y & kLo) | ((z << 4) & ~kLo), f);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                a[kt][e][2 * i] = hmul2(f[e], s);
-                            e2m1x8_to_f16x2(((y >> 4) & kLo) | (z & ~kLo), f);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                a[kt][e][2 * i + 1] = hmul2(f[e], s);
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t a = w[kt][2 * i][j], b = w[kt][2 * i + 1][j];
+                        if constexpr (C::kFp4) {
+                            constexpr uint32_t kLo = 0x0F0F0F0Fu;
+                            y[kt][2 * i] = (a & kLo) | ((b << 4) & ~kLo);
+                            y[kt][2 * i + 1] = ((a >> 4) & kLo) | (b & ~kLo);
+                        } else {
+                            y[kt][2 * i] = prmt(a, b, C::kFp8 ? 0x5140 : 0x5410);
+                            y[kt][2 * i + 1] = prmt(a, b, C::kFp8 ? 0x7362 : 0x7632);
                         }
-                    } else if constexpr (C::kFp8) {
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const uint32_t y = i ? w2 : w0, z = i ? w3 : w1;
-                            const uint32_t lo = prmt(y, z, 0x5140), hi = prmt(y, z, 0x7362);
-                            a[kt][0][2 * i] = fp8x2_to_f16x2<KV>(lo16(lo));
-                            a[kt][0][2 * i + 1] = fp8x2_to_f16x2<KV>(hi16(lo));
-                            a[kt][1][2 * i] = fp8x2_to_f16x2<KV>(lo16(hi));
-                            a[kt][1][2 * i + 1] = fp8x2_to_f16x2<KV>(hi16(hi));
-                        }
-                    } else {
-                        a[kt][0][0] = prmt(w0, w1, 0x5410);
-                        a[kt][0][1] = prmt(w0, w1, 0x7632);
-                        a[kt][0][2] = prmt(w2, w3, 0x5410);
-                        a[kt][0][3] = prmt(w2, w3, 0x7632);
                     }
-                    if constexpr (TOKEN) {
-#pragma unroll
-                        for (int e = 0; e < kBlocks; ++e)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                a[kt][e][i] &= keep[kt][i / 2];
-                    }
-                }
-                // The tile's sums start from 0 and are added in fp32: the tensor cores' additions truncate.
 #pragma unroll
                 for (int e = 0; e < kBlocks; ++e) {
+                    uint32_t a[KT][4];
+#pragma unroll
+                    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            if constexpr (C::kFp4) {
+                                const uint32_t s = s16[kt][i][D == 256 ? j / 2 : 0];
+                                a[kt][2 * i] = hmul2(e2m1x2_at(y[kt][2 * i], e), s);
+                                a[kt][2 * i + 1] = hmul2(e2m1x2_at(y[kt][2 * i + 1], e), s);
+                            } else if constexpr (C::kFp8) {
+                                a[kt][2 * i] = fp8x2_to_f16x2<KV>(lo16(y[kt][2 * i + e]));
+                                a[kt][2 * i + 1] = fp8x2_to_f16x2<KV>(hi16(y[kt][2 * i + e]));
+                            } else {
+                                a[kt][2 * i] = y[kt][2 * i];
+                                a[kt][2 * i + 1] = y[kt][2 * i + 1];
+                            }
+                        }
                     const int blk = (x * kWords + j) * kBlocks + e;
+                    // The tile's sums start from 0 and are added in fp32: the tensor cores' additions truncate.
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        float t[4] = {0.f, 0.f, 0.f, 0.f};
+                        float t[4];
 #pragma unroll
                         for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
                             for (int part = 0; part < kParts; ++part)
-                                mma_16816<C::kF16>(t, a[kt][e][0], a[kt][e][1], a[kt][e][2], a[kt][e][3], pf[kt][part][nt][0], pf[kt][part][nt][1]);
+                                if (kt == 0 && part == 0)
+                                    mma_16816_zero<C::kF16>(t, a[kt][0], a[kt][1], a[kt][2], a[kt][3], pf[kt][part][nt][0], pf[kt][part][nt][1]);
+                                else
+                                    mma_16816<C::kF16>(t, a[kt][0], a[kt][1], a[kt][2], a[kt][3], pf[kt][part][nt][0], pf[kt][part][nt][1]);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            // 0 times a row that only `token` sees may be NaN
-                            const bool mine = !TOKEN || ((nt * 8 + 2 * c + (i & 1)) & kColMask) / p.group == token;
-                            acc[blk][nt][i] = fmaf(acc[blk][nt][i], alpha[nt][i & 1], mine ? t[i] : 0.f);
-                        }
+                        for (int i = 0; i < 4; ++i)
+                            acc[blk][nt][i] += t[i];
                     }
                 }
             }
+        }
+    }
+
+    // Of a tile that some columns see in part: what V holds that is not finite goes to the sums of the columns that see
+    // it (whose other terms do not matter) and becomes 0 in the tile, so that weights of 0 do not make it NaN.
+    __device__ __forceinline__ void screen(const WindowParams &p, const WindowReq &req, int row0, uint32_t v, uint32_t vs, int lane)
+    {
+        constexpr int kBytes = C::kFp4 ? kTile * C::kScaleRow : kTile * kRow;
+        const uint32_t at = C::kFp4 ? vs : v;
+        bool bad = false;
+        for (int i = 4 * lane; i < kBytes; i += 128)
+            bad = bad || not_finite(lds32(at + i));
+        if (!__any_sync(0xffffffffu, bad))
+            return;
+        const int g = lane >> 2, c = lane & 3;
+        for (int r = 0; r < kTile; ++r) {
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const float x = element(v, vs, r, block_dim(s, g) + y);
+                    if (fabsf(x) < __builtin_huge_valf())
+                        continue;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int i = min(((nt * 8 + 2 * c + e) & kColMask) / p.group, p.q_len - 1);
+                            if (visible(p, req, row0 + r, req.L - p.q_len + i))
+                                acc[s][nt][2 * y + e] += x;
+                        }
+                }
+        }
+        __syncwarp();
+        for (int i = 4 * lane; i < kBytes; i += 128) {
+            uint32_t w = lds32(at + i);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t keep = C::kFp4 || C::kFp8 ? 0xFFu << 8 * e : 0xFFFFu << 16 * (e & 1);
+                if (not_finite(w & keep))
+                    w &= ~keep;
+            }
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + i), "r"(w) : "memory");
+        }
+        __syncwarp();
+    }
+    // Whether one of the elements (scales of a 4-bit cache) in w is an infinity or NaN.
+    __device__ __forceinline__ static bool not_finite(uint32_t w)
+    {
+        constexpr uint32_t kMask = C::kFp4 || KV == kKvE4m3 ? 0x7Fu : KV == kKvE5m2 ? 0x7Cu : KV == kKvF16 ? 0x7C00u : 0x7F80u;
+        bool bad = false;
+#pragma unroll
+        for (int e = 0; e < 32; e += C::kFp4 || C::kFp8 ? 8 : 16)
+            bad = bad || (w >> e & kMask) == kMask;
+        return bad;
+    }
+    // V's element of row r and dim d of the tile.
+    __device__ __forceinline__ static float element(uint32_t v, uint32_t vs, int r, int d)
+    {
+        const int byte = d * kRow / D;
+        const uint32_t w = lds8(v + r * kRow + (((byte >> 4) ^ window_swizzle<kGran>(r)) << 4) + (byte & 15));
+        if constexpr (C::kFp4) {
+            const float s = fp8x2_to_float2<kKvE4m3>((uint16_t)lds8(vs + r * C::kScaleRow + d / 16)).x;
+            return f16x2_to_float2(e2m1x2_to_f16x2<0>(d & 1 ? w >> 4 : w)).x * s;
+        } else if constexpr (C::kFp8) {
+            return fp8x2_to_float2<KV>((uint16_t)w).x;
+        } else {
+            const uint32_t hi = lds8(v + r * kRow + (((byte >> 4) ^ window_swizzle<kGran>(r)) << 4) + (byte & 15) + 1);
+            return x2_to_float2<C::kF16>(w | hi << 8).x;
         }
     }
 
@@ -586,116 +698,195 @@ __device__ __forceinline__ void window_schedule(const WindowParams &p, int *pref
     __syncthreads();
 }
 
-// Shared memory: the warps' rings, then prefix and non-empty [batch + 1], then scratch.
-constexpr int kWindowScratch = 2 * kWindowMaxWarps + 2 * kWindowMaxWarps;   // ints: the scan's sums; the warps' last segments
+// The partials of a segment that workers w0 .. w1 share: one of each CTA, and one more of w1 if it went on to another
+// segment.  n is 1 if one CTA (or worker) has it whole.
+struct WindowParts {
+    int w0, w1, c0, c1, n;
+    bool apart;
+    WindowParts() = default;
+    __device__ __forceinline__ WindowParts(const WindowSchedule &s, int teams, int seg)
+    {
+        const int b = seg / s.hkv;
+        const long long pos = s.seg_pos(b, seg - b * s.hkv), end = pos + (s.prefix[b + 1] - s.prefix[b]) / s.hkv;
+        w0 = s.cta_at(pos);
+        w1 = s.cta_at(end - 1);
+        apart = w0 != w1 && end + s.w < s.cost() && s.cta_at(end + s.w) == w1;
+        c0 = w0 / teams;
+        c1 = (apart ? w1 - 1 : w1) / teams;
+        n = c1 - c0 + 1 + (apart ? 1 : 0);
+    }
+    // Where partial k lies (in units of a team).
+    __device__ __forceinline__ int slot(int teams, int k) const
+    {
+        return c0 + k > c1 ? 2 * w1 : 2 * max(w0, (c0 + k) * teams) + 1;
+    }
+};
+
+// Shared memory: the warps' rings, then prefix and non-empty [batch + 1], then scratch: the scan's sums,
+// and what the warps hold at the end.
+constexpr int kWindowScratch = 2 * kWindowMaxWarps * (3 + (int)(sizeof(WindowParts) / sizeof(int)));
 template <class C>
 constexpr size_t window_smem(int batch)
 {
     return (size_t)C::kWarps * C::kRing + sizeof(int) * (2 * ((size_t)batch + 1) + kWindowScratch);
 }
 
-template <class C, int NT, bool PACK>
-__global__ void __launch_bounds__(32 * C::kWarps) window_kernel(const __grid_constant__ WindowParams p)
+constexpr int kWindowTogether = 4;   // partials whose loads a thread has in flight
+
+// Sums of weights and of weighted V rows (4 dims) against the reference exponent `top`.
+struct WindowSum {
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    float top = -__builtin_huge_valf(), l = 0.f;
+    __device__ __forceinline__ void add(float2 ml, float4 x)
+    {
+        const float higher = fmaxf(top, ml.x), ref = higher == -__builtin_huge_valf() ? 0.f : higher;
+        // at least fp32's least normal number: an infinite sum stays infinite
+        const float f = fmaxf(exp2_approx(top - ref), 1.1754944e-38f), w = fmaxf(exp2_approx(ml.x - ref), 1.1754944e-38f);
+        top = higher;
+        l = fmaf(w, ml.y, l * f);
+        sum.x = fmaf(w, x.x, sum.x * f);
+        sum.y = fmaf(w, x.y, sum.y * f);
+        sum.z = fmaf(w, x.z, sum.z * f);
+        sum.w = fmaf(w, x.w, sum.w * f);
+    }
+    template <int D>
+    __device__ __forceinline__ void store(const WindowParams &p, int b, int head, int col, int d, float shift) const
+    {
+        const long long row = window_out_row(p, b, head, col);
+        const float f = l == 0.f ? 0.f : p.v_scale / l;
+        *reinterpret_cast<float4 *>(p.o + row * D + d) = make_float4(sum.x * f, sum.y * f, sum.z * f, sum.w * f);
+        if (d == 0 && p.lse)
+            p.lse[row] = window_lse(top - shift, l);
+    }
+};
+
+template <class C, bool PACK>
+__global__ void __launch_bounds__(32 * C::kWarps, 1) window_kernel(const __grid_constant__ WindowParams p)
 {
-    using Warp = WindowWarp<C, NT, PACK>;
-    constexpr int D = C::D, kTile = C::kTile, kRow = C::kRow, kGran = C::kGran, kStages = C::kStages;
+    using Warp = WindowWarp<C, PACK>;
+    constexpr int NT = C::NT, D = C::D, kTile = C::kTile, kRow = C::kRow, kGran = C::kGran, kStages = C::kStages;
     constexpr int kMl = NT * 8 * 2;   // floats of (m, l) in front of a warp's sums
-    static_assert(C::kRing >= (int)sizeof(float) * (kMl + NT * 8 * D), "the ring holds a warp's sums at the end");
+    static_assert(C::kRing >= C::kSums, "the ring holds a warp's sums at the end");
     extern __shared__ __align__(128) uint8_t smem[];
     int *prefix = reinterpret_cast<int *>(smem + C::kWarps * C::kRing);
-    int *nonempty = prefix + p.batch + 1, *tmp = nonempty + p.batch + 1, *s_last = tmp + 2 * kWindowMaxWarps;
+    int *nonempty = prefix + p.batch + 1, *tmp = nonempty + p.batch + 1;
+    int *s_seg = tmp + 2 * kWindowMaxWarps, *s_size = s_seg + 2 * kWindowMaxWarps;
+    WindowParts *s_parts = reinterpret_cast<WindowParts *>(s_size + 2 * kWindowMaxWarps);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
 
     pdl_launch_dependents();
     pdl_wait_prior_grid();
     window_schedule<kTile>(p, prefix, nonempty, tmp, blockIdx.x == 0);
-    if (blockIdx.x == 0)
-        for (int i = threadIdx.x; i < 2 * (p.batch + 1); i += blockDim.x)
-            p.ws_prefix[i] = prefix[i];
-
     const int heads = p.hkv / p.team;
-    Schedule sch = {prefix, nonempty, p.batch, heads, kWindowSegCost, 0};
+    for (int b = blockIdx.x; b < p.batch; b += gridDim.x)   // requests that see nothing
+        if (prefix[b] == prefix[b + 1])
+            for (int i = threadIdx.x; i < p.q_len * p.hq * (D / 4); i += blockDim.x) {
+                const long long row = (long long)b * p.q_len * p.hq + i / (D / 4);
+                *reinterpret_cast<float4 *>(p.o + row * D + i % (D / 4) * 4) = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (p.lse && i % (D / 4) == 0)
+                    p.lse[row] = -__builtin_huge_valf();
+            }
+    WindowSchedule sch = {{prefix, nonempty, p.batch, heads, kWindowSegCost, 0}};
     const int teams = window_workers(sch.cost(), gridDim.x, C::kWarps / p.team);
     sch.P = gridDim.x * teams;
     const int team = warp / p.team, lead = warp - team * p.team;   // the warp's kv head of the team's
     const int worker = blockIdx.x * teams + team;
     int t0 = 0, t1 = 0;
-    if (team < teams)
-        sch.range(worker, &t0, &t1);
+    if (team < teams && worker < sch.ctas()) {
+        // odd lanes find the run's end
+        const int t = sch.tile_at(sch.begin(worker + (lane & 1)));
+        t0 = __shfl_sync(0xffffffffu, t, 0);
+        t1 = __shfl_sync(0xffffffffu, t, 1);
+    }
 
     Warp w;
-    int last = -1;   // the segment of the sums that the warp still holds
+    int last = -1, begun = -1;   // the segment of the sums that the warp still holds; the one that it found begun and ended
     if (t0 < t1) {
         const uint32_t ring = smem_addr(smem) + warp * C::kRing;
+        const uint32_t meta = ring + kStages * C::kStage;   // of each tile: request, launch head, first row, kTile* and its rows
         const uint64_t policy = l2_policy_evict_first();
 
-        // A tile's rows of the cache: lane r has row r's number, or none.
-        constexpr uint32_t kNone = 0xFFFFFFFFu;
         WindowCursor ld;
-        ld.b = request_of_tile(prefix, p.batch, t0);
-        ld.nb = (prefix[ld.b + 1] - prefix[ld.b]) / heads;
+        auto request = [&](int b) {
+            const WindowReq r = window_req(p, b, nullptr);
+            ld.b = b;
+            ld.nb = (prefix[b + 1] - prefix[b]) / heads;
+            ld.rows = r.rows;
+            ld.head = r.head;
+            ld.skip = r.first - r.head;
+            ld.pages = p.block_table + (long long)b * p.max_blocks;
+        };
+        request(request_of_tile(prefix, p.batch, t0));
         ld.h = (t0 - prefix[ld.b]) / ld.nb;
         ld.j = t0 - prefix[ld.b] - ld.h * ld.nb;
-        ld.req = window_req(p, ld.b, nullptr);
-        WindowCursor use = ld;
-        auto advance = [&](WindowCursor &x) {
-            if (++x.j < x.nb)
+        auto advance = [&]() {
+            if (++ld.j < ld.nb)
                 return;
-            x.j = 0;
-            if (++x.h < heads)
+            ld.j = 0;
+            if (++ld.h < heads)
                 return;
-            x.h = 0;
-            do
-                ++x.b;
-            while (prefix[x.b + 1] == prefix[x.b]);
-            x.nb = (prefix[x.b + 1] - prefix[x.b]) / heads;
-            x.req = window_req(p, x.b, nullptr);
+            ld.h = 0;
+            int b = ld.b + 1;
+            while (prefix[b + 1] == prefix[b])
+                ++b;
+            request(b);
         };
-        // The page and slot of lane's row of the tile at ld; one tile ahead of the copies, which wait for them.
-        int page = -1, slot = 0, head = 0;
+        // Lane's row of the tile at ld: its page, and its number within the page's rows.  Looked up one tile ahead of the
+        // copies, which wait for it.  Rows behind the last are copies of it: their weights are 0.
+        int page = 0;
+        uint32_t in_page = 0;
+        auto position = [&](int row) { return row < ld.head ? row : row + ld.skip; };
         auto look_up = [&]() {
-            const int v = ld.j * kTile + lane;
-            page = -1;
-            head = ld.h * p.team + lead;
-            if (lane < kTile && v < ld.req.rows) {
-                const int pos = window_pos(ld.req, v);
-                if (p.block_table) {
-                    const int blk = (unsigned)pos / (unsigned)p.page_size;
-                    slot = pos - blk * p.page_size;
-                    page = p.block_table[(long long)ld.b * p.max_blocks + blk];
-                    if ((unsigned)page >= (unsigned)p.num_pages) {
-                        page = 0;
-                        atomicOr(p.ws_err, kErrPage);
-                    }
-                } else {
-                    page = ld.b;
-                    slot = pos;
+            int slot = position(min(ld.j * kTile + (lane & (kTile - 1)), ld.rows - 1));
+            page = ld.b;
+            if (p.block_table) {
+                const int blk = p.page_shift >= 0 ? slot >> p.page_shift : (int)((unsigned)slot / (unsigned)p.page_size);
+                slot -= blk * p.page_size;
+                page = ld.pages[blk];
+            }
+            in_page = (uint32_t)slot * p.row_token + (uint32_t)(ld.h * p.team + lead) * p.row_head;
+        };
+        // Places of the lane's pieces: the first of a copy, and of every other copy.
+        constexpr int kCopies = kTile * kGran / 32, kRows = 32 / kGran;   // copies of a lane, rows of a copy
+        const uint8_t *from_k = p.k + 16 * (lane % kGran), *from_v = p.v + 16 * (lane % kGran);
+        const uint32_t to_even = lane / kGran * kRow + ((lane % kGran ^ window_swizzle<kGran>(lane / kGran)) << 4);
+        const uint32_t to_odd = lane / kGran * kRow + ((lane % kGran ^ window_swizzle<kGran>(lane / kGran + kRows)) << 4);
+        auto copy = [&](int stage) {
+            if ((unsigned)page >= (unsigned)p.num_pages) {
+                page = 0;
+                atomicOr(p.ws_err, kErrPage);
+            }
+            const int row0 = ld.j * kTile, n = min(kTile, ld.rows - row0);
+            // is every row visible to every new token?
+            bool plain = n == kTile;
+            if (p.q_len > 1) {
+                plain = plain && position(row0 + kTile - 1) <= ld.rows + ld.skip - p.q_len;
+                if (p.window) {
+                    const int behind = max(position(row0), ld.head + ld.skip);   // the first row behind the sinks
+                    plain = plain && (row0 + kTile <= ld.head || ld.rows + ld.skip - 1 - behind < p.window);
                 }
             }
-        };
-        auto copy = [&](int stage) {
-            const uint32_t row = page < 0 ? kNone : (uint32_t)page * p.row_page + (uint32_t)slot * p.row_token + (uint32_t)head * p.row_head;
-            const uint32_t k = ring + stage * C::kStage, v = k + kTile * kRow;
-            constexpr int kCopies = kTile * kGran / 32, kRows = 32 / kGran;   // copies of a lane, rows of a copy
+            sts128(meta + 16 * stage, ld.b, ld.h, row0, n << kTileN | (plain ? kTilePlain : 0) | (ld.j == 0 ? kTileFirst : 0) |
+                                                            (ld.j + 1 == ld.nb ? kTileLast : 0));
+            const uint32_t row = (uint32_t)page * p.row_page + in_page;
+            const uint32_t k = ring + stage * C::kStage, even = k + to_even, odd = k + to_odd;
 #pragma unroll
             for (int i = 0; i < kCopies; ++i) {
-                const int r = i * kRows + lane / kGran, x = lane % kGran;
-                const uint32_t from = __shfl_sync(0xffffffffu, row, r);
-                const uint32_t size = from == kNone ? 0u : 16u;
-                const size_t at = from == kNone ? 0 : (size_t)from * kRow + 16 * x;
-                const uint32_t to = r * kRow + ((x ^ window_swizzle<kGran>(r)) << 4);
-                cp_async_or_zero<16>(k + to, p.k + at, size, policy);
-                cp_async_or_zero<16>(v + to, p.v + at, size, policy);
+                const size_t at = (size_t)__shfl_sync(0xffffffffu, row, i * kRows + lane / kGran) * kRow;
+                // the swizzle has a period of 4 rows: of 1, 2 or 4 copies
+                const uint32_t to = kRows >= 4 ? even + i * kRows * kRow : kRows == 2 ? (i & 1 ? odd : even) + i * kRows * kRow
+                                               : k + i * kRow + ((lane % kGran ^ window_swizzle<kGran>(i)) << 4);
+                cp_async_16(to, from_k + at, policy);
+                cp_async_16(to + kTile * kRow, from_v + at, policy);
             }
             if constexpr (C::kFp4) {
                 constexpr int kS = C::kScaleRow;
-                const uint32_t ks = v + kTile * kRow, vs = ks + kTile * kS;
-                if (kTile == 32 || lane < kTile) {
-                    const uint32_t size = row == kNone ? 0u : (uint32_t)kS;
-                    const size_t at = row == kNone ? 0 : (size_t)row * kS;
-                    cp_async_or_zero<kS>(ks + lane * kS, p.ks + at, size, policy);
-                    cp_async_or_zero<kS>(vs + lane * kS, p.vs + at, size, policy);
-                }
+                const uint32_t ks = k + 2 * kTile * kRow, vs = ks + kTile * kS;
+                if constexpr (kTile == 32) {
+                    cp_async_small<kS>(ks + lane * kS, p.ks + (size_t)row * kS, policy);
+                    cp_async_small<kS>(vs + lane * kS, p.vs + (size_t)row * kS, policy);
+                } else   // rows of K for half the lanes, of V for the others
+                    cp_async_small<kS>((lane < 16 ? ks : vs - 16 * kS) + lane * kS, (lane < 16 ? p.ks : p.vs) + (size_t)row * kS, policy);
             }
         };
 
@@ -705,58 +896,55 @@ __global__ void __launch_bounds__(32 * C::kWarps) window_kernel(const __grid_con
             if (ahead < t1) {
                 copy(stage);
                 if (++ahead < t1) {
-                    advance(ld);
+                    advance();
                     look_up();
                 }
             }
             cp_async_commit();
         };
+        const bool first = ld.j == 0;
+        const int b0 = ld.b, h0 = ld.h;
 #pragma unroll
         for (int i = 0; i < kStages - 1; ++i)
             fetch(i);
+        w.start(p, b0, h0 * p.team + lead, g, c);   // while the first tile is on its way
+        last = b0 * heads + h0;
 
+        const WindowPlaces<C> places(g, c);
         int stage = 0;
-        bool whole = false;   // the segment's first tile was the warp's
+        bool whole = first;   // the segment's first tile was the warp's
         for (int t = t0; t < t1; ++t) {
-            const int seg = use.b * heads + use.h, head_now = use.h * p.team + lead;
-            if (seg != last) {
-                w.start(p, use.b, head_now, g, c);
-                last = seg;
-                whole = use.j == 0;
-            }
             cp_async_wait<kStages - 2>();
             __syncwarp();
             fetch(stage == 0 ? kStages - 1 : stage - 1);
+            const uint4 tile = lds128(meta + 16 * stage);
+            const int b = (int)tile.x, h = (int)tile.y, row0 = (int)tile.z, flags = (int)tile.w;
+            const int seg = b * heads + h, head = h * p.team + lead;
+            if (seg != last) {
+                w.start(p, b, head, g, c);
+                last = seg;
+                whole = flags & kTileFirst;
+            }
             const uint32_t k = ring + stage * C::kStage, v = k + kTile * kRow, ks = v + kTile * kRow, vs = ks + kTile * C::kScaleRow;
             stage = stage + 1 == kStages ? 0 : stage + 1;
-            const int row0 = use.j * kTile;
-            // every row of the tile visible to every new token?
-            bool plain = row0 + kTile <= use.req.rows && window_pos(use.req, row0 + kTile - 1) <= use.req.L - p.q_len;
-            if (p.window && p.q_len > 1) {
-                const int from = max(window_pos(use.req, row0), use.req.first);   // the tile's first row behind the sinks
-                plain = plain && (row0 + kTile <= use.req.head || from < p.sinks || use.req.L - 1 - from < p.window);
-            }
-            float sc[Warp::KT][NT][4], alpha[NT][2];
+            float sc[Warp::KT][NT][4];
             uint32_t pf[Warp::KT][Warp::kParts][NT][2];
-            w.scores(k, ks, g, c, sc);
-            if (!plain)
-                w.mask(p, use.req, row0, g, c, sc);
-            w.weights(sc, c, pf, alpha);
-            if (plain || p.q_len == 1)
-                w.template values<false>(p, use.req, row0, 0, v, vs, g, c, pf, alpha);
-            else {
-                float one[NT][2];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    one[nt][0] = one[nt][1] = 1.f;
-                for (int i = 0; i < p.q_len; ++i) {
-                    w.template values<true>(p, use.req, row0, i, v, vs, g, c, pf, alpha);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        alpha[nt][0] = alpha[nt][1] = 1.f;
+            w.scores(places, k, ks, sc);
+            uint32_t least = C::kF16 ? 0x00010001u : 0x00800080u;   // 2^-38 or 2^-126 of a reference's weight
+            if (!(flags & kTilePlain)) {
+                if (p.q_len == 1)
+                    w.cut(flags >> kTileN, g, sc);
+                else {
+                    const WindowReq req = window_req(p, b, nullptr);
+                    w.mask(p, req, row0, g, c, sc);
+                    w.screen(p, req, row0, v, vs, lane);
+                    least = 0u;
                 }
             }
-            if (use.j + 1 == use.nb && (whole || t + 1 < t1)) {
+            w.rescale(sc);
+            w.weights(sc, least, c, pf);
+            w.values(places, v, vs, pf);
+            if ((flags & kTileLast) && (whole || t + 1 < t1)) {
                 // the segment ends inside the run: its output, or a partial of a segment that others began
                 w.finish();
                 const long long slot_o = (long long)(2 * worker) * p.team + lead;
@@ -770,25 +958,25 @@ __global__ void __launch_bounds__(32 * C::kWarps) window_kernel(const __grid_con
                         float *dst;
                         float f = 1.f;
                         if (whole) {
-                            const long long row = window_out_row(p, use.b, head_now, col);
+                            const long long row = window_out_row(p, b, head, col);
                             dst = p.o + row * D;
                             f = w.l[nt][e] == 0.f ? 0.f : p.v_scale / w.l[nt][e];
                             if (g == 0 && p.lse)
-                                p.lse[row] = window_lse(w.m[nt][e] - Warp::kShift, w.l[nt][e]);
+                                p.lse[row] = window_lse(w.reference(nt, e) - Warp::kShift, w.l[nt][e]);
                         } else {
                             dst = p.ws_o + (slot_o * p.cols + col) * D;
                             if (g == 0)
-                                p.ws_ml[slot_o * p.cols + col] = make_float2(w.m[nt][e], w.l[nt][e]);
+                                p.ws_ml[slot_o * p.cols + col] = make_float2(w.reference(nt, e), w.l[nt][e]);
                         }
 #pragma unroll
                         for (int s = 0; s < Warp::kSteps; s += 2)
                             *reinterpret_cast<float4 *>(dst + Warp::block_dim(s, g)) =
                                 make_float4(w.acc[s][nt][e] * f, w.acc[s][nt][e + 2] * f, w.acc[s + 1][nt][e] * f, w.acc[s + 1][nt][e + 2] * f);
                     }
+                if (!whole)
+                    begun = seg;
                 last = -1;
             }
-            if (t + 1 < t1)
-                advance(use);
         }
         cp_async_wait<0>();
         __syncwarp();
@@ -807,7 +995,7 @@ __global__ void __launch_bounds__(32 * C::kWarps) window_kernel(const __grid_con
                 if (col >= p.cols || (PACK && c >= 2))
                     continue;
                 if (g == 0) {
-                    ml[2 * col] = w.m[nt][e];
+                    ml[2 * col] = w.reference(nt, e);
                     ml[2 * col + 1] = w.l[nt][e];
                 }
 #pragma unroll
@@ -816,59 +1004,127 @@ __global__ void __launch_bounds__(32 * C::kWarps) window_kernel(const __grid_con
                         make_float4(w.acc[s][nt][e], w.acc[s][nt][e + 2], w.acc[s + 1][nt][e], w.acc[s + 1][nt][e + 2]);
             }
     }
-    if (lane == 0)
-        s_last[warp] = last;
+    if (lane == 0) {
+        s_seg[warp] = begun;
+        s_seg[C::kWarps + warp] = last;
+    }
     __syncthreads();
-    for (int a = 0; a < C::kWarps; ++a) {   // a: the group's first warp (of its kv head of the team's)
-        const int seg = s_last[a];
-        if (seg < 0 || (a >= p.team && s_last[a - p.team] == seg))
+    // What the CTA has of segments that others share: the partials of segments that its warps found begun (entries 0 ..
+    // kWarps - 1), and its groups of warps that hold sums of one segment (kWarps .. 2 kWarps - 1, at the group's first).
+    const int lead_of = threadIdx.x % C::kWarps % p.team;
+    if (threadIdx.x < 2 * C::kWarps) {
+        const int a = threadIdx.x, seg = s_seg[a];
+        s_size[a] = 0;
+        if (seg >= 0 && (a < C::kWarps || a < C::kWarps + p.team || s_seg[a - p.team] != seg)) {
+            int n = 1;
+            if (a >= C::kWarps)
+                while (a + n * p.team < 2 * C::kWarps && s_seg[a + n * p.team] == seg)
+                    ++n;
+            s_size[a] = n;
+            s_parts[a] = WindowParts(sch, teams, seg);
+        }
+    }
+    __syncthreads();
+    const int items = p.cols * (D / 4);   // 4 dims of a column
+    for (int a = C::kWarps + warp; a < 2 * C::kWarps; a += C::kWarps) {   // a warp adds up its group
+        const int n = s_size[a];
+        if (n == 0)
             continue;
-        int n = 1;
-        while (a + n * p.team < C::kWarps && s_last[a + n * p.team] == seg)
-            ++n;
-        const int b = seg / heads, head = (seg - b * heads) * p.team + a % p.team;
-        // did the group have the whole segment?
-        const long long pos = sch.seg_pos(b, seg - b * heads);
-        const int nb = (prefix[b + 1] - prefix[b]) / heads, w0 = blockIdx.x * teams + a / p.team;
-        const bool all = sch.cta_at(pos) == w0 && sch.cta_at(pos + nb - 1) == w0 + n - 1;
-        const long long slot_o = (long long)(2 * w0 + 1) * p.team + a % p.team;
-        for (int i = threadIdx.x; i < p.cols * (D / 4); i += blockDim.x) {
+        const int seg = s_seg[a], b = seg / heads, head = (seg - b * heads) * p.team + lead;
+        const bool all = s_parts[a].n == 1;
+        const long long slot = (long long)(2 * worker + 1) * p.team + lead;
+        for (int i = lane; i < items; i += 32) {
             const int col = i / (D / 4), d = 4 * (i - col * (D / 4));
-            float top = -__builtin_huge_valf();
-            for (int k = 0; k < n; ++k)
-                top = fmaxf(top, reinterpret_cast<const float *>(smem + (a + k * p.team) * C::kRing)[2 * col]);
-            const float ref = top == -__builtin_huge_valf() ? 0.f : top;
-            float sum = 0.f;
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            WindowSum x;
             for (int k = 0; k < n; ++k) {
-                const float *ml = reinterpret_cast<const float *>(smem + (a + k * p.team) * C::kRing);
-                const float4 y = *reinterpret_cast<const float4 *>(ml + kMl + col * D + d);
-                const float f = fmaxf(exp2_approx(ml[2 * col] - ref), 1.1754944e-38f);
-                sum = fmaf(f, ml[2 * col + 1], sum);
-                x.x = fmaf(f, y.x, x.x);
-                x.y = fmaf(f, y.y, x.y);
-                x.z = fmaf(f, y.z, x.z);
-                x.w = fmaf(f, y.w, x.w);
+                const float *ml = reinterpret_cast<const float *>(smem + (warp + k * p.team) * C::kRing);
+                x.add(make_float2(ml[2 * col], ml[2 * col + 1]), *reinterpret_cast<const float4 *>(ml + kMl + col * D + d));
             }
-            if (all) {
-                const long long row = window_out_row(p, b, head, col);
-                const float f = sum == 0.f ? 0.f : p.v_scale / sum;
-                *reinterpret_cast<float4 *>(p.o + row * D + d) = make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
-                if (d == 0 && p.lse)
-                    p.lse[row] = window_lse(top - Warp::kShift, sum);
-            } else {
-                *reinterpret_cast<float4 *>(p.ws_o + (slot_o * p.cols + col) * D + d) = x;
+            if (all)
+                x.store<D>(p, b, head, col, d, Warp::kShift);
+            else {
+                *reinterpret_cast<float4 *>(p.ws_o + (slot * p.cols + col) * D + d) = x.sum;
                 if (d == 0)
-                    p.ws_ml[slot_o * p.cols + col] = make_float2(top, sum);
+                    p.ws_ml[slot * p.cols + col] = make_float2(x.top, x.l);
             }
         }
     }
+
+    // The CTA that writes the last partial of a segment adds them up, in the order of the workers.
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x < 2 * C::kWarps) {
+        const int a = threadIdx.x;
+        bool merge = false;
+        if (s_size[a] > 0 && s_parts[a].n > 1) {
+            unsigned int *count = p.ws_counts + s_parts[a].w0 * p.team + lead_of;
+            merge = atomicAdd(count, 1u) == (unsigned)s_parts[a].n - 1;
+            if (merge)
+                *count = 0;
+        }
+        s_size[a] = merge ? 1 : 0;
+    }
+    __syncthreads();
+    int merges = 0;
+    for (int a = 0; a < 2 * C::kWarps; ++a)
+        merges += s_size[a];
+    if (merges == 0)
+        return;
+    __threadfence();
+    // Threads share the (segment, 4 dims) pairs, or several share the partials of one.
+    const int total = merges * items, per = min(total, (int)blockDim.x), split = blockDim.x / per, mine = threadIdx.x / per;
+    WindowSum *shared = reinterpret_cast<WindowSum *>(smem);
+    for (int i0 = 0; i0 < total; i0 += per) {
+        const int i = i0 + threadIdx.x - mine * per;
+        const bool active = mine < split && i < total;
+        int a = 0, b = 0, head = 0, col = 0, d = 0;
+        WindowSum x;
+        if (active) {
+            int which = i / items;
+            while (which > 0 || s_size[a] == 0)
+                which -= s_size[a++];
+            const WindowParts parts = s_parts[a];
+            const int seg = s_seg[a], of = a % C::kWarps % p.team;
+            b = seg / heads;
+            head = (seg - b * heads) * p.team + of;
+            col = i % items / (D / 4);
+            d = 4 * (i % (D / 4));
+            for (int k0 = mine; k0 < parts.n; k0 += split * kWindowTogether) {
+                float2 ml[kWindowTogether];
+                float4 y[kWindowTogether];
+#pragma unroll
+                for (int e = 0; e < kWindowTogether; ++e) {
+                    const int k = min(k0 + e * split, parts.n - 1);
+                    const long long slot = (long long)parts.slot(teams, k) * p.team + of;
+                    ml[e] = __ldcg(p.ws_ml + slot * p.cols + col);
+                    y[e] = __ldcg(reinterpret_cast<const float4 *>(p.ws_o + (slot * p.cols + col) * D + d));
+                }
+#pragma unroll
+                for (int e = 0; e < kWindowTogether; ++e)
+                    if (k0 + e * split < parts.n)
+                        x.add(ml[e], y[e]);
+            }
+        }
+        if (split > 1) {   // then total < blockDim: one pass
+            __syncthreads();
+            if (active)
+                shared[mine * per + i] = x;
+            __syncthreads();
+            if (active && mine == 0)
+                for (int k = 1; k < split; ++k) {
+                    const WindowSum &y = shared[k * per + i];
+                    x.add(make_float2(y.top, y.l), y.sum);
+                }
+        }
+        if (active && mine == 0)
+            x.store<D>(p, b, head, col, d, Warp::kShift);
+    }
 }
 
-template <class C, int NT, bool PACK>
+template <class C, bool PACK>
 cudaError_t launch_window_t(const WindowParams &p, const WindowLaunch &c)
 {
-    auto kernel = window_kernel<C, NT, PACK>;
+    auto kernel = window_kernel<C, PACK>;
     // Raise the kernel's shared-memory limit once per device, so that later calls may be captured; again if a launch
     // is refused (the device's context was reset since).
     static std::atomic<unsigned long long> configured{0};
@@ -885,6 +1141,8 @@ cudaError_t launch_window_t(const WindowParams &p, const WindowLaunch &c)
     };
     if (!(configured.load(std::memory_order_acquire) & bit) && (e = configure()) != cudaSuccess)
         return e;
+    if (c.start_event && !record_event(c.start_event, c.stream))
+        return cudaErrorInvalidValue;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -902,22 +1160,25 @@ cudaError_t launch_window_t(const WindowParams &p, const WindowLaunch &c)
             return e;
         e = cudaLaunchKernelEx(&cfg, kernel, p);
     }
-    return e;
+    if (e != cudaSuccess)
+        return e;
+    if (c.end_event && !record_event(c.end_event, c.stream))
+        return cudaErrorInvalidValue;
+    return cudaSuccess;
 }
 
 template <int D, int KV>
 cudaError_t launch_window_variant(const WindowParams &p, const WindowLaunch &c)
 {
-    using C = WindowCfg<D, KV>;
-    static_assert(window_smem<C>(kMaxBatch) <= 232448, "fits the 227 KB of a CTA");
-    cudaError_t e;
+    using One = WindowCfg<D, KV, 1>;
+    using Two = WindowCfg<D, KV, 2>;
+    static_assert(window_smem<One>(kMaxBatch) <= 232448 && window_smem<Two>(kMaxBatch) <= 232448, "fits the 227 KB of a CTA");
     if (p.cols > 8)
-        e = launch_window_t<C, 2, false>(p, c);
-    else if constexpr (C::kF16)
-        e = p.cols <= 4 ? launch_window_t<C, 1, true>(p, c) : launch_window_t<C, 1, false>(p, c);
-    else
-        e = launch_window_t<C, 1, false>(p, c);
-    return e;
+        return launch_window_t<Two, false>(p, c);
+    if constexpr (One::kF16)
+        if (p.cols <= 4)
+            return launch_window_t<One, true>(p, c);
+    return launch_window_t<One, false>(p, c);
 }
 
 }  // namespace fd
