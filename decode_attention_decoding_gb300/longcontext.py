@@ -11,22 +11,25 @@ Like the package's other functions these only check and marshal arguments;
 tensors live on one GPU, outputs are allocated unless they are given.  A call
 runs on that GPU's current stream, whatever device is current, or on the
 stream given as `stream=`, one of that GPU, which then owns what the call
-allocates.
+allocates.  Short calls take less time on the GPU than here, so the checks are
+kept to a few attribute reads a tensor.
 """
 from __future__ import annotations
 
+import functools
 import math
 from typing import NamedTuple
 
 import torch
 
 from . import FD_ERR_INVALID_ARG, FD_OK, FdCache4, FdError, FdOptions, _kv_code, _lib, _options, fd_workspace_init
-from .speculative import _BF16, _F16, _F32, _I32, _I64, _gpu, _launch, _on_stream, _ptr_of, _status, _table_of, _token_rows
+from .speculative import _BF16, _F16, _F32, _I32, _I64, _gpu, _on_stream, _ptr_of, _status, _table_of, _token_rows
 
 __all__ = ["Cache4", "make_cache4", "fd_cache_write4", "fd_cache_read4", "fd_decode4", "fd_decode4_paged",
            "fd_window_decode", "fd_window_decode_paged", "fd_window_workspace_size", "make_window_workspace"]
 
 _U8 = torch.uint8
+_SCALES = (torch.float8_e4m3fn, torch.uint8)
 
 
 class Cache4(NamedTuple):
@@ -48,18 +51,39 @@ def make_cache4(pages, num_kv_heads, page_size, head_dim, device="cuda") -> Cach
                   zeros(head_dim // 16, torch.float8_e4m3fn))
 
 
+_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
+def _call(gpu, f, *args):
+    """Call f with the GPU's current stream as its last argument and the GPU current (kernels launch on the current one)."""
+    if _current_device() == gpu:
+        return f(*args, _raw_stream(gpu))
+    with torch.cuda.device(gpu):
+        return f(*args, _raw_stream(gpu))
+
+
+@functools.lru_cache(maxsize=256)
+def _opts(num_ctas, dtype, kv, k_scale, v_scale, q_len):
+    """The options of these values; the library only reads them."""
+    return FdOptions(num_ctas, 0, 0, None, None, dtype, kv, k_scale, v_scale, q_len)
+
+
 def _cache(cache, d, gpu):
-    """(FdCache4, (pages, Hkv, page)) of a cache of head dim d on the call's GPU."""
+    """(FdCache4, pages, Hkv, page) of a cache of head dim d on the call's GPU."""
     kc, ks, vc, vs = cache
-    if kc.dim() != 4:
-        raise ValueError(f"k_codes must be [pages, Hkv, P, {d // 2}], got {list(kc.shape)}")
-    lead = kc.shape[:3]
-    codes, scales = (*lead, d // 2), (*lead, d // 16)
-    for t, name in ((ks, "k_scales"), (vs, "v_scales")):
-        if t.dtype is not torch.float8_e4m3fn and t.dtype is not _U8:
-            raise ValueError(f"{name} must be float8_e4m3fn or uint8, got {t.dtype}")
-    return FdCache4(_ptr_of(kc, "k_codes", _U8, codes, gpu), _ptr_of(ks, "k_scales", ks.dtype, scales, gpu),
-                    _ptr_of(vc, "v_codes", _U8, codes, gpu), _ptr_of(vs, "v_scales", vs.dtype, scales, gpu)), lead
+    codes, scales = kc.shape, ks.shape
+    ok = (kc.dtype is _U8 and vc.dtype is _U8 and len(codes) == 4 and 2 * codes[3] == d and vc.shape == codes and kc.get_device() == gpu
+          and vc.get_device() == gpu and kc.is_contiguous() and vc.is_contiguous())
+    if not ok:
+        raise ValueError(f"k_codes and v_codes must be contiguous uint8 [pages, Hkv, P, {d // 2}] on cuda:{gpu}, got {kc.dtype} "
+                         f"{list(kc.shape)} on {kc.device} and {vc.dtype} {list(vc.shape)} on {vc.device}")
+    pages, hkv, page, _ = codes
+    ok = (ks.dtype in _SCALES and vs.dtype in _SCALES and scales == (pages, hkv, page, d // 16) and vs.shape == scales
+          and ks.get_device() == gpu and vs.get_device() == gpu and ks.is_contiguous() and vs.is_contiguous())
+    if not ok:
+        raise ValueError(f"k_scales and v_scales must be contiguous float8_e4m3fn or uint8 {[pages, hkv, page, d // 16]} on cuda:{gpu}, got "
+                         f"{ks.dtype} {list(ks.shape)} on {ks.device} and {vs.dtype} {list(vs.shape)} on {vs.device}")
+    return FdCache4(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr()), pages, hkv, page
 
 
 def _rows4(name, call, k, v, kn, vn, slot_map, cache, k_scale, v_scale, device_status, check, stream, write):
@@ -69,16 +93,16 @@ def _rows4(name, call, k, v, kn, vn, slot_map, cache, k_scale, v_scale, device_s
     n, h, d = shape = k.shape
     if v.shape != shape or v.dtype is not k.dtype:
         raise ValueError(f"{kn} and {vn} must have one shape and type")
-    c, (pages, heads, page) = _cache(cache, d, gpu)
+    c, pages, heads, page = _cache(cache, d, gpu)
     if heads != h:
         raise ValueError(f"the cache has {heads} kv heads, the rows {h}")
-    opts = FdOptions(0, 0, 0, None, None, 1 if k.dtype is _F16 else 0, 0, k_scale, v_scale, 1)
+    opts = _opts(0, 1 if k.dtype is _F16 else 0, 0, float(k_scale), float(v_scale), 1)
     slots = _ptr_of(slot_map, "slot_map", _I64, (n,), gpu)
-    status = _status(device_status, gpu)
+    status = None if device_status is None else _status(device_status, gpu)
     if write:
-        st = _launch(gpu, call, k.data_ptr(), v.data_ptr(), ks, vs, slots, n, h, d, c, page, pages * page, opts, status)
+        st = _call(gpu, call, k.data_ptr(), v.data_ptr(), ks, vs, slots, n, h, d, c, page, pages * page, opts, status)
     else:
-        st = _launch(gpu, call, slots, n, h, d, c, page, pages * page, k.data_ptr(), v.data_ptr(), ks, vs, opts, status)
+        st = _call(gpu, call, slots, n, h, d, c, page, pages * page, k.data_ptr(), v.data_ptr(), ks, vs, opts, status)
     if check and st != FD_OK:
         raise FdError(st, name)
 
@@ -128,26 +152,35 @@ def make_window_workspace(batch, num_q_heads, num_kv_heads, head_dim=128, device
     return ws
 
 
-def _attend(name, call, q, cache, pages, page, hkv, block_table, seq_lens, window, sinks, seq_lens_host, scale, out, lse,
-            workspace, num_ctas, split_events, check, kv, k_scale, v_scale, gpu):
+def _attend(name, call, q, gpu, cache, pages, page, hkv, table, seq_lens, window, sinks, seq_lens_host, scale, out, lse,
+            workspace, num_ctas, split_events, check, kv, k_scale, v_scale):
     """Any cache: checks, outputs, and the call `name`; `cache`: its arguments in that call."""
-    dt = q.dtype
-    if q.dim() not in (3, 4) or not q.is_contiguous() or (dt is not _BF16 and dt is not _F16):
-        raise ValueError("q must be a contiguous bf16 or fp16 tensor [B, Hq, D] or [B, q_len, Hq, D]")
-    shape = q.shape
-    B, T, hq, d = shape if len(shape) == 4 else (shape[0], 1, *shape[1:])
-    per_request = (B,)
-    layout, cap = (), (page,)
-    if block_table is not None:
-        layout, cap = _table_of(block_table, B, gpu), (page, pages)
+    shape, dt = q.shape, q.dtype
+    if len(shape) == 4:
+        B, T, hq, d = shape
+    elif len(shape) == 3:
+        (B, hq, d), T = shape, 1
+    else:
+        raise ValueError(f"q must be [B, Hq, D] or [B, q_len, Hq, D], got {list(shape)}")
+    if (dt is not _BF16 and dt is not _F16) or not q.is_contiguous():
+        raise ValueError("q must be a contiguous bf16 or fp16 tensor")
+    if table is not None:
+        layout = (*_table_of(table, B, gpu),)
+        cap = (page, pages)
     elif pages != B:
         raise ValueError(f"a contiguous cache must hold {B} requests, got {pages}")
+    else:
+        layout, cap = (), (page,)
     if out is None:
         out = torch.empty(shape, dtype=_F32, device=q.device)
+    else:
+        _ptr_of(out, "out", _F32, shape, gpu)
     if lse is None:
         lse = torch.empty(shape[:-1], dtype=_F32, device=q.device)
     elif lse is False:
         lse = None
+    else:
+        _ptr_of(lse, "lse", _F32, shape[:-1], gpu)
     if workspace is None:
         workspace = make_window_workspace(B, hq, hkv, d, q.device, T)
     elif workspace.get_device() != gpu or not workspace.is_contiguous():
@@ -157,32 +190,42 @@ def _attend(name, call, q, cache, pages, page, hkv, block_table, seq_lens, windo
         host = seq_lens_host.to(_I32).contiguous().cpu()
         if host.numel() != B:
             raise ValueError(f"seq_lens_host must hold {B} lengths")
-    opts = _options(num_ctas, 0, 0, split_events, 1 if dt is _F16 else 0, kv, k_scale, v_scale, T)
-    st = _launch(gpu, call, q.data_ptr(), *cache, *layout,
-                 None if seq_lens is None else _ptr_of(seq_lens, "seq_lens", _I32, per_request, gpu),
-                 None if host is None else host.data_ptr(), B, hq, hkv, d, *cap, window, sinks,
-                 1.0 / math.sqrt(d) if scale is None else scale, _ptr_of(out, "out", _F32, shape, gpu),
-                 None if lse is None else _ptr_of(lse, "lse", _F32, shape[:-1], gpu), workspace.data_ptr(),
-                 workspace.numel() * workspace.element_size(), opts)
+    f16 = 1 if dt is _F16 else 0
+    if split_events is None:
+        opts = _opts(num_ctas, f16, kv, float(k_scale), float(v_scale), T)
+    else:
+        opts = _options(num_ctas, 0, 0, split_events, f16, kv, k_scale, v_scale, T)
+    st = _call(gpu, call, q.data_ptr(), *cache, *layout, None if seq_lens is None else _ptr_of(seq_lens, "seq_lens", _I32, (B,), gpu),
+               None if host is None else host.data_ptr(), B, hq, hkv, d, *cap, window, sinks,
+               1.0 / math.sqrt(d) if scale is None else scale, out.data_ptr(), None if lse is None else lse.data_ptr(),
+               workspace.data_ptr(), workspace.nbytes, opts)
     if check and st != FD_OK:
         raise FdError(st, name)
     return out, lse
 
 
-def _window(name, call, q, k, v, block_table, seq_lens, window, sinks, seq_lens_host, scale, out, lse, workspace, num_ctas,
+def _window(name, call, q, k, v, table, seq_lens, window, sinks, seq_lens_host, scale, out, lse, workspace, num_ctas,
             split_events, check, kv_dtype, k_scale, v_scale, stream):
-    gpu = _gpu(q, "q", stream)
-    kv = _kv_code(k, v, kv_dtype)
-    if k.dim() != 4 or k.shape != v.shape or k.get_device() != gpu or v.get_device() != gpu or k.shape[3] != q.shape[-1]:
-        raise ValueError(f"k and v must have one 4-d shape with head_dim {q.shape[-1]} on cuda:{gpu}")
-    if kv == 0 and (k.dtype is not q.dtype or v.dtype is not q.dtype):
-        raise TypeError("a 16-bit cache must be of q's type")
-    pages, page, hkv, _ = k.shape
-    return _attend(name, call, q, (k.data_ptr(), v.data_ptr()), pages, page, hkv, block_table, seq_lens, window, sinks,
-                   seq_lens_host, scale, out, lse, workspace, num_ctas, split_events, check, kv, k_scale, v_scale, gpu)
+    gpu = q.get_device()
+    if gpu < 0 or stream is not None:
+        _gpu(q, "q", stream)
+        with torch.cuda.stream(stream):
+            return _window(name, call, q, k, v, table, seq_lens, window, sinks, seq_lens_host, scale, out, lse, workspace,
+                           num_ctas, split_events, check, kv_dtype, k_scale, v_scale, None)
+    shape, dt = k.shape, k.dtype
+    if (len(shape) != 4 or v.shape != shape or shape[3] != q.shape[-1] or k.get_device() != gpu or v.get_device() != gpu
+            or not k.is_contiguous() or not v.is_contiguous()):
+        raise ValueError(f"k and v must be contiguous, of one 4-d shape with head_dim {q.shape[-1]}, on cuda:{gpu}")
+    kv = 0
+    if kv_dtype is not None or dt is not q.dtype or v.dtype is not dt:
+        kv = _kv_code(k, v, kv_dtype)
+        if kv == 0:
+            raise TypeError("a 16-bit cache must be of q's type")
+    pages, page, hkv, _ = shape
+    return _attend(name, call, q, gpu, (k.data_ptr(), v.data_ptr()), pages, page, hkv, table, seq_lens, window, sinks, seq_lens_host,
+                   scale, out, lse, workspace, num_ctas, split_events, check, kv, k_scale, v_scale)
 
 
-@_on_stream
 def fd_window_decode(q, k, v, seq_lens, window, sinks=0, seq_lens_host=None, scale=None, out=None, lse=None,
                      workspace=None, num_ctas=0, split_events=None, check=True, kv_dtype=None, k_scale=1.0,
                      v_scale=1.0, *, stream=None):
@@ -197,7 +240,6 @@ def fd_window_decode(q, k, v, seq_lens, window, sinks=0, seq_lens_host=None, sca
                    lse, workspace, num_ctas, split_events, check, kv_dtype, k_scale, v_scale, stream)
 
 
-@_on_stream
 def fd_window_decode_paged(q, k_pages, v_pages, block_table, seq_lens, window, sinks=0, seq_lens_host=None, scale=None,
                            out=None, lse=None, workspace=None, num_ctas=0, split_events=None, check=True, kv_dtype=None,
                            k_scale=1.0, v_scale=1.0, *, stream=None):
@@ -210,15 +252,19 @@ def fd_window_decode_paged(q, k_pages, v_pages, block_table, seq_lens, window, s
                    v_scale, stream)
 
 
-def _decode4(name, call, q, cache, block_table, seq_lens, window, sinks, seq_lens_host, scale, out, lse, workspace, num_ctas,
+def _decode4(name, call, q, cache, table, seq_lens, window, sinks, seq_lens_host, scale, out, lse, workspace, num_ctas,
              split_events, check, k_scale, v_scale, stream):
-    gpu = _gpu(q, "q", stream)
-    c, (pages, hkv, page) = _cache(cache, q.shape[-1], gpu)
-    return _attend(name, call, q, (c,), pages, page, hkv, block_table, seq_lens, window, sinks, seq_lens_host, scale, out, lse,
-                   workspace, num_ctas, split_events, check, 0, k_scale, v_scale, gpu)
+    gpu = q.get_device()
+    if gpu < 0 or stream is not None:
+        _gpu(q, "q", stream)
+        with torch.cuda.stream(stream):
+            return _decode4(name, call, q, cache, table, seq_lens, window, sinks, seq_lens_host, scale, out, lse, workspace,
+                            num_ctas, split_events, check, k_scale, v_scale, None)
+    c, pages, hkv, page = _cache(cache, q.shape[-1], gpu)
+    return _attend(name, call, q, gpu, (c,), pages, page, hkv, table, seq_lens, window, sinks, seq_lens_host, scale, out, lse,
+                   workspace, num_ctas, split_events, check, 0, k_scale, v_scale)
 
 
-@_on_stream
 def fd_decode4(q, cache, seq_lens=None, window=0, sinks=0, seq_lens_host=None, scale=None, out=None, lse=None,
                workspace=None, num_ctas=0, split_events=None, check=True, k_scale=1.0, v_scale=1.0, *, stream=None):
     """Decode attention over a contiguous 4-bit cache, a Cache4 of [B, Hkv, S, ..]
@@ -228,7 +274,6 @@ def fd_decode4(q, cache, seq_lens=None, window=0, sinks=0, seq_lens_host=None, s
                     workspace, num_ctas, split_events, check, k_scale, v_scale, stream)
 
 
-@_on_stream
 def fd_decode4_paged(q, cache, block_table, seq_lens, window=0, sinks=0, seq_lens_host=None, scale=None, out=None,
                      lse=None, workspace=None, num_ctas=0, split_events=None, check=True, k_scale=1.0, v_scale=1.0, *,
                      stream=None):
