@@ -26,10 +26,39 @@ struct Cache4Params {
     int num_tokens, tokens_per_cta, hkv, page_size;
     int blocks_log2;                  // blocks of a kv head's row: D / 16
     int units;                        // blocks of a token: hkv * D / 16
+    unsigned int units_magic;         // floor(2^32 / units) + 1: __umulhi(x, magic) = x / units for x * units < 2^32
+    int page_shift;                   // page_size = 2^page_shift, or -1
+    int wide;                         // rows of 32-byte pieces: base and stride are multiples of 32
 };
 
-constexpr int kCache4Threads = 256;
-constexpr int kCache4Units = 2;   // blocks a thread has in flight
+// Measured on GB300 (32768 rows of 8 heads into random slots, and back; us): 128 threads with one block each 35.5 and
+// 33.5; two blocks a thread 35.9 and 34.2, four 37.1 and 40.6; 256 threads 35.7 and 34.2, 64 35.7 and 35.9.  Two 16-byte
+// accesses in place of one of 32 bytes, and rows read after their slots, took the write to 73.
+constexpr int kCache4Threads = 128;
+
+// 32 bytes of a row, as one access where they are aligned.
+__device__ __forceinline__ void load_piece(const uint8_t *p, bool wide, uint32_t (&w)[8])
+{
+    if (wide) {
+        asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                     : "l"(p));
+    } else {
+        const uint4 a = ldg128_nc(p), b = ldg128_nc(p + 16);
+        w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w; w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+    }
+}
+__device__ __forceinline__ void store_piece(uint8_t *p, bool wide, const uint32_t (&w)[8])
+{
+    if (wide)
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                     "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    else {
+        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4 *>(p + 16) = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
 
 __device__ __forceinline__ uint32_t pack_e2m1x8(const float (&x)[8])
 {
@@ -50,39 +79,60 @@ __device__ __forceinline__ void e2m1x2_to_f16x2(uint32_t w, uint32_t (&r)[4])
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
         : "r"(w));
 }
-__device__ __forceinline__ float max_nan(float a, float b)
+template <bool F16>
+__device__ __forceinline__ uint32_t max_nan_x2(uint32_t a, uint32_t b)
 {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    uint32_t r;
+    if constexpr (F16)
+        asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 
-// One block of a row: 16 fp32 values to 8 bytes of codes and a scale.
-__device__ __forceinline__ uint2 quantise_block(const float (&x)[16], float t, uint32_t *scale_code)
+// One block of a row: 16 elements, two a word, to 8 bytes of codes and a scale.
+template <bool F16>
+__device__ __forceinline__ uint2 quantise_block(const uint32_t (&w)[8], float t, uint32_t *scale_code)
 {
-    float top = 0.f;
+    uint32_t m = w[0] & 0x7FFF7FFFu;
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-        top = max_nan(top, fabsf(x[i]));
+    for (int i = 1; i < 8; ++i)
+        m = max_nan_x2<F16>(m, w[i] & 0x7FFF7FFFu);
+    const float top = x2_to_float2<F16>(max_nan_x2<F16>(m, m >> 16)).x;
     const uint32_t code = pack_e4m3x2(__fdiv_rn(top, 6.f * t), 0.f) & 0xFFu;
     *scale_code = code;
     const float unit = fp8x2_to_float2<kKvE4m3>((uint16_t)code).x * t;
     if (!(unit > 0.f))   // 0, or NaN
         return make_uint2(0u, 0u);
-    float y[2][8];
-    if (unit >= 0x1p-60f && unit <= 0x1p60f) {
+    uint32_t out[2];
+    if (code < 0x7Eu && unit >= 0x1p-60f && unit <= 0x1p60f) {
+        // below the largest scale the quotients are at most 6.5: quotient<true> without its limits
         const float r = __frcp_rn(unit);
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            y[i / 8][i % 8] = quotient<true>(x[i], unit, r);
-    } else {
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2; ++h) {
+            float y[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                y[h][i] = quotient<false>(x[8 * h + i], unit, 0.f);
+            for (int i = 0; i < 8; ++i) {
+                const float2 x2 = x2_to_float2<F16>(w[4 * h + i / 2]);
+                const float x = i % 2 ? x2.y : x2.x, q = x * r;
+                y[i] = copysignf(fmaf(fmaf(-q, unit, x), r, q), x);
+            }
+            out[h] = pack_e2m1x8(y);
+        }
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float y[8];
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+                const float2 x = x2_to_float2<F16>(w[4 * h + i]);
+                y[2 * i] = quotient<false>(x.x, unit, 0.f);
+                y[2 * i + 1] = quotient<false>(x.y, unit, 0.f);
+            }
+            out[h] = pack_e2m1x8(y);
+        }
     }
-    return make_uint2(pack_e2m1x8(y[0]), pack_e2m1x8(y[1]));
+    return make_uint2(out[0], out[1]);
 }
 
 // A CTA takes tokens_per_cta tokens of K (blockIdx.y = 0) or V.
@@ -93,71 +143,44 @@ __global__ void __launch_bounds__(kCache4Threads) cache4_kernel(const __grid_con
     const unsigned total = (unsigned)n * (unsigned)p.units;
     const int which = blockIdx.y;
     const float scale = p.scale[which];
-    for (unsigned u0 = threadIdx.x; u0 < total; u0 += kCache4Threads * kCache4Units) {
-        uint4 x[kCache4Units][2];
-        uint2 codes[kCache4Units];
-        uint32_t s[kCache4Units];
-        long long blk[kCache4Units];      // the block's place in the cache, or -1
-        uint8_t *row[kCache4Units];
-#pragma unroll
-        for (int k = 0; k < kCache4Units; ++k) {
-            const unsigned u = u0 + k * kCache4Threads;
-            blk[k] = -1;
-            if (u < total) {
-                const unsigned t = u / (unsigned)p.units, c = u - t * (unsigned)p.units;
-                const long long slot = p.slots[t0 + t];
-                if (slot >= 0 && slot < p.num_slots) {
-                    const unsigned h = c >> p.blocks_log2, in = c & ((1u << p.blocks_log2) - 1);
-                    const long long page = slot < (1ll << 32) ? (long long)((unsigned)slot / (unsigned)p.page_size) : slot / p.page_size;
-                    const long long at = (page * p.hkv + h) * p.page_size + (slot - page * p.page_size);
-                    blk[k] = (at << p.blocks_log2) + in;
-                    row[k] = p.rows[which] + (long long)(t0 + t) * p.stride[which] + (size_t)c * 32;
-                    if constexpr (WRITE) {
-                        x[k][0] = ldg128_nc(row[k]);
-                        x[k][1] = ldg128_nc(row[k] + 16);
-                    } else {
-                        codes[k] = *reinterpret_cast<const uint2 *>(p.codes[which] + blk[k] * 8);
-                        s[k] = p.scales[which][blk[k]];
-                    }
-                } else if (slot >= 0 && p.status)
-                    atomicOr(p.status, FD_DEVICE_STATUS_BAD_SLOT);
-            }
+    uint8_t *all_codes = p.codes[which], *all_scales = p.scales[which], *rows = p.rows[which];
+    const long long stride = p.stride[which];
+    for (unsigned u = threadIdx.x; u < total; u += kCache4Threads) {
+        const unsigned t = p.tokens_per_cta == 1 ? 0u : __umulhi(u, p.units_magic);   // u / units
+        const unsigned unit = u - t * (unsigned)p.units, h = unit >> p.blocks_log2, in = unit & ((1u << p.blocks_log2) - 1);
+        const long long slot = p.slots[t0 + t];
+        uint8_t *row = rows + (long long)(t0 + t) * stride + (size_t)unit * 32;
+        uint32_t x[8];
+        if constexpr (WRITE)   // read while the slot is on its way
+            load_piece(row, p.wide, x);
+        if (slot < 0 || slot >= p.num_slots) {
+            if (slot >= 0 && p.status)
+                atomicOr(p.status, FD_DEVICE_STATUS_BAD_SLOT);
+            continue;
         }
+        const long long page = p.page_shift >= 0 ? slot >> p.page_shift
+                               : slot >> 32 == 0 ? (long long)((unsigned)slot / (unsigned)p.page_size) : slot / p.page_size;
+        const long long at = (((page * p.hkv + h) * p.page_size + (slot - page * p.page_size)) << p.blocks_log2) + in;   // the block's place
+        if constexpr (WRITE) {
+            uint32_t code;
+            *reinterpret_cast<uint2 *>(all_codes + at * 8) = quantise_block<F16>(x, scale, &code);
+            all_scales[at] = (uint8_t)code;
+        } else {
+            const uint2 codes = *reinterpret_cast<const uint2 *>(all_codes + at * 8);
+            const float s = fp8x2_to_float2<kKvE4m3>((uint16_t)all_scales[at]).x;
+            const uint32_t w[2] = {codes.x, codes.y};
 #pragma unroll
-        for (int k = 0; k < kCache4Units; ++k) {
-            if (blk[k] < 0)
-                continue;
-            if constexpr (WRITE) {
-                float v[16];
+            for (int i = 0; i < 2; ++i) {
+                uint32_t f[4];
+                e2m1x2_to_f16x2(w[i], f);
+                // code * s is exact; the product with t is rounded to fp32, and that to 16 bits
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint32_t w[4] = {x[k][i].x, x[k][i].y, x[k][i].z, x[k][i].w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 y = x2_to_float2<F16>(w[e]);
-                        v[8 * i + 2 * e] = y.x;
-                        v[8 * i + 2 * e + 1] = y.y;
-                    }
-                }
-                uint32_t code;
-                *reinterpret_cast<uint2 *>(p.codes[which] + blk[k] * 8) = quantise_block(v, scale, &code);
-                p.scales[which][blk[k]] = (uint8_t)code;
-            } else {
-                const float sc = fp8x2_to_float2<kKvE4m3>((uint16_t)s[k]).x;
-                const uint32_t w[2] = {codes[k].x, codes[k].y};
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    uint32_t f[4];
-                    e2m1x2_to_f16x2(w[i], f);
-                    // code * s is exact; the product with t is rounded to fp32, and that to 16 bits
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 y = f16x2_to_float2(f[e]);
-                        f[e] = pack_x2<F16>(y.x * sc * scale, y.y * sc * scale);
-                    }
-                    *reinterpret_cast<uint4 *>(row[k] + 16 * i) = make_uint4(f[0], f[1], f[2], f[3]);
+                for (int e = 0; e < 4; ++e) {
+                    const float2 y = f16x2_to_float2(f[e]);
+                    x[4 * i + e] = pack_x2<F16>(y.x * s * scale, y.y * s * scale);
                 }
             }
+            store_piece(row, p.wide, x);
         }
     }
 }
@@ -207,8 +230,10 @@ fd_status run(const fd_cache4 *cache, int page_size, long long num_slots, const 
     p.page_size = page_size;
     p.blocks_log2 = head_dim == 64 ? 2 : head_dim == 128 ? 3 : 4;
     p.units = hkv << p.blocks_log2;
-    const int per_pass = kCache4Threads * kCache4Units;
-    p.tokens_per_cta = p.units >= per_pass ? 1 : per_pass / p.units;
+    p.units_magic = (unsigned int)((1ull << 32) / (unsigned)p.units) + 1u;
+    p.page_shift = (page_size & (page_size - 1)) == 0 ? __builtin_ctz((unsigned)page_size) : -1;
+    p.wide = aligned(k, 32) && aligned(v, 32) && p.stride[0] % 32 == 0 && p.stride[1] % 32 == 0;
+    p.tokens_per_cta = p.units >= kCache4Threads ? 1 : kCache4Threads / p.units;
     const dim3 grid((unsigned)((num_tokens + (long long)p.tokens_per_cta - 1) / p.tokens_per_cta), 2);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (opts && opts->dtype == FD_DTYPE_F16)
