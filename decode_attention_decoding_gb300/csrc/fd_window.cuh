@@ -43,12 +43,15 @@ struct WindowCfg {
     static constexpr int kRow = kFp4 ? D / 2 : kFp8 ? D : 2 * D;   // bytes of a row
     static constexpr int kGran = kRow / 16;                  // 16-byte pieces of a row
     static constexpr int kScaleRow = kFp4 ? D / 16 : 0;      // bytes of a row's block scales
-    static constexpr int kTile = kRow <= 64 || (kRow <= 128 && !kFp4) ? 32 : 16;   // rows of a tile
+    static constexpr int kTile = kFp4 && D == 128 && NT == 1 ? 64 : kRow <= 64 || (kRow <= 128 && !kFp4) ? 32 : 16;   // rows of a tile
     static constexpr int kStage = 2 * kTile * (kRow + kScaleRow);
-    static constexpr int kWarps = kStage <= 4800 && D < 256 && NT == 1 ? 12 : kStage <= 8192 ? 8 : 4;
+    static constexpr int kWarps = kStage <= 4800 && D < 256 && NT == 1 ? 12 : kStage <= 9300 ? 8 : 4;
+    // Two words a lane of each k step of the query: in registers where there are some left.
+    static constexpr bool kQueryShared = NT == 2;
+    static constexpr int kQuery = kQueryShared ? 16 * D * NT : 0;
     static constexpr int kSums = (int)sizeof(float) * NT * 8 * (D + 2);   // bytes of a warp's sums, left in its ring at the end
-    static constexpr int kStages = kSums <= 2 * kStage ? 2 : (kSums + kStage - 1) / kStage;
-    static constexpr int kRing = (kStage + 16) * kStages;    // bytes of a warp's tiles, and what each is
+    static constexpr int kStages = kSums <= 2 * kStage + kQuery ? 2 : (kSums - kQuery + kStage - 1) / kStage;
+    static constexpr int kRing = (kStage + 16) * kStages + kQuery;   // bytes of a warp's tiles, of what each is, and of the query
 };
 
 struct WindowParams {

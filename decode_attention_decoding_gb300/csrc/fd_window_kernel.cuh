@@ -181,7 +181,10 @@ struct WindowWarp {
     static constexpr float kShift = C::kShift, kSlack = C::kSlack;
     static constexpr int kColMask = PACK ? 3 : 8 * NT - 1;
 
-    uint32_t qf[NT][kSteps][2];
+    // The query as the B operand of S^T, two words of each k step: in registers, or in shared memory (every lane its own).
+    static constexpr int kHeld = C::kQueryShared ? 1 : kSteps;
+    uint32_t qf[kHeld][NT][2];
+    uint32_t q_at;
     float mult[NT][2];         // score of column 2c, 2c + 1 of an MMA's eight -> log2 units
     float acc[kSteps][NT][4];
     // of columns 2c, 2c + 1: what a score (log2 units) may not pass, kShift - the reference, and the sum of weights
@@ -197,16 +200,17 @@ struct WindowWarp {
             const int i = col / p.group;
             const bool real = col < p.cols;
             const uint16_t *src = p.q + ((long long)(b * p.q_len + (real ? i : 0)) * p.hq + head * p.group + (real ? col - i * p.group : 0)) * D;
+            uint2 words[kSteps];
 #pragma unroll
             for (int s = 0; s < kSteps; ++s) {
                 // elements of a piece, and the lane's four in step s
                 constexpr int kEl = kRow >= 64 ? 16 * D / kRow : 16, kPer = kEl / 4;
                 const int dim = (c + 4 * (s / kPer)) * kEl + 4 * (s % kPer);
-                uint2 w = make_uint2(0u, 0u);
+                words[s] = make_uint2(0u, 0u);
                 if (real)
-                    w = *reinterpret_cast<const uint2 *>(src + dim);
-                qf[nt][s][0] = w.x ^ sign;
-                qf[nt][s][1] = w.y ^ sign;
+                    words[s] = *reinterpret_cast<const uint2 *>(src + dim);
+                words[s].x ^= sign;
+                words[s].y ^= sign;
             }
             float f = p.scale_log2;
             if (KV >= kKvE4m3 && !p.q_f16) {
@@ -214,25 +218,30 @@ struct WindowWarp {
                 // what fp16 cannot hold is below 2^-39 of it
                 float top = 0.f;
 #pragma unroll
-                for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float2 x = bf16x2_to_float2(qf[nt][s][e]);
-                        top = fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y)));
-                    }
+                for (int s = 0; s < kSteps; ++s) {
+                    const float2 x = bf16x2_to_float2(words[s].x), y = bf16x2_to_float2(words[s].y);
+                    top = fmaxf(top, fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(y.x), fabsf(y.y))));
+                }
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
                 int e = ((int)(__float_as_uint(top) >> 23) & 255) - 127;     // top in [2^e, 2^(e + 1))
                 e = top > 0.f && e < 128 ? min(max(14 - e, -126), 126) : 0;
                 const float up = __uint_as_float((uint32_t)(e + 127) << 23), down = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
-                for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-                    for (int w = 0; w < 2; ++w) {
-                        const float2 x = bf16x2_to_float2(qf[nt][s][w]);
-                        qf[nt][s][w] = pack_f16x2(x.x * up, x.y * up);
-                    }
+                for (int s = 0; s < kSteps; ++s) {
+                    const float2 x = bf16x2_to_float2(words[s].x), y = bf16x2_to_float2(words[s].y);
+                    words[s] = make_uint2(pack_f16x2(x.x * up, x.y * up), pack_f16x2(y.x * up, y.y * up));
+                }
                 f = fmaxf(f * down, 1.1754944e-38f);
+            }
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                if constexpr (C::kQueryShared)
+                    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(q_at + (s * NT + nt) * 256), "r"(words[s].x), "r"(words[s].y) : "memory");
+                else {
+                    qf[s][nt][0] = words[s].x;
+                    qf[s][nt][1] = words[s].y;
+                }
             }
             mult[nt][0] = __shfl_sync(0xffffffffu, f, 8 * c);
             mult[nt][1] = __shfl_sync(0xffffffffu, f, 8 * c + 4);
@@ -251,66 +260,71 @@ struct WindowWarp {
     __device__ __forceinline__ void scores(const WindowPlaces<C> &at, uint32_t k, uint32_t ks, float (&sc)[KT][NT][4]) const
     {
         const uint32_t ke = k + at.ke, ko = k + at.ko, kscale = ks + at.ks;
+        constexpr int kPieces = kRow >= 64 ? kRow / 64 : 1;
+        constexpr int kPer = kSteps / kPieces;   // k steps of a piece
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt) {
+        for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     sc[kt][nt][e] = 0.f;
-            constexpr int kPieces = kRow >= 64 ? kRow / 64 : 1, kWords = kRow >= 64 ? 4 : 2;
 #pragma unroll
-            for (int x = 0; x < kPieces; ++x) {
-                uint32_t a[2][4], s16[2][2];
+        for (int x = 0; x < kPieces; ++x) {
+            uint32_t a[KT][2][4], s16[KT][2][2];   // rows window_row(g) and + 8 of each 16: words; block scales as fp16 pairs
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const uint32_t from = (x & 1 ? ko : ke) + (kt * 16 + 8 * i) * kRow + 64 * x;
                     if constexpr (kRow >= 64) {
                         const uint4 w = lds128(from);
-                        a[i][0] = w.x; a[i][1] = w.y; a[i][2] = w.z; a[i][3] = w.w;
+                        a[kt][i][0] = w.x; a[kt][i][1] = w.y; a[kt][i][2] = w.z; a[kt][i][3] = w.w;
                     } else {
                         const uint2 w = lds64(from);
-                        a[i][0] = w.x; a[i][1] = w.y;
+                        a[kt][i][0] = w.x; a[kt][i][1] = w.y;
                     }
                     if constexpr (C::kFp4) {
                         const uint32_t place = kscale + (kt * 16 + 8 * i) * C::kScaleRow + 8 * x;
                         const uint32_t b = fp8x2_to_f16x2<kKvE4m3>((uint16_t)(kRow >= 64 ? lds16(place) : lds8(place)));
-                        s16[i][0] = prmt(b, b, 0x1010);
-                        s16[i][1] = prmt(b, b, 0x3232);
+                        s16[kt][i][0] = prmt(b, b, 0x1010);
+                        s16[kt][i][1] = prmt(b, b, 0x3232);
                     }
                 }
-                if constexpr (C::kFp4) {
 #pragma unroll
-                    for (int w = 0; w < kWords; ++w)
+            for (int s = 0; s < kPer; ++s) {
+                uint32_t q[NT][2];
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int s = (x * kWords + w) * 2 + e;
-                            uint32_t f[2][2];
-#pragma unroll
-                            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                                for (int y = 0; y < 2; ++y)
-                                    f[i][y] = hmul2(e2m1x2_at(a[i][w], 2 * e + y), s16[i][w / 2]);
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-                                mma_16816<C::kF16>(sc[kt][nt], f[0][0], f[1][0], f[0][1], f[1][1], qf[nt][s][0], qf[nt][s][1]);
-                        }
-                } else if constexpr (C::kFp8) {
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        const uint32_t a0 = fp8x2_to_f16x2<KV>(lo16(a[0][w])), a1 = fp8x2_to_f16x2<KV>(lo16(a[1][w]));
-                        const uint32_t a2 = fp8x2_to_f16x2<KV>(hi16(a[0][w])), a3 = fp8x2_to_f16x2<KV>(hi16(a[1][w]));
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma_16816<C::kF16>(sc[kt][nt], a0, a1, a2, a3, qf[nt][x * 4 + w][0], qf[nt][x * 4 + w][1]);
+                for (int nt = 0; nt < NT; ++nt) {
+                    if constexpr (C::kQueryShared) {
+                        const uint2 w = lds64(q_at + ((x * kPer + s) * NT + nt) * 256);
+                        q[nt][0] = w.x;
+                        q[nt][1] = w.y;
+                    } else {
+                        q[nt][0] = qf[x * kPer + s][nt][0];
+                        q[nt][1] = qf[x * kPer + s][nt][1];
                     }
-                } else {
+                }
 #pragma unroll
-                    for (int w = 0; w < 2; ++w)
+                for (int kt = 0; kt < KT; ++kt) {
+                    uint32_t f[2][2];   // [row][pair of the lane's four elements]
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma_16816<C::kF16>(sc[kt][nt], a[0][2 * w], a[1][2 * w], a[0][2 * w + 1], a[1][2 * w + 1],
-                                               qf[nt][x * 2 + w][0], qf[nt][x * 2 + w][1]);
+                    for (int i = 0; i < 2; ++i) {
+                        if constexpr (C::kFp4) {
+                            const uint32_t w = a[kt][i][s / 2], sc16 = s16[kt][i][s / 4];
+                            f[i][0] = hmul2(e2m1x2_at(w, 2 * (s & 1)), sc16);
+                            f[i][1] = hmul2(e2m1x2_at(w, 2 * (s & 1) + 1), sc16);
+                        } else if constexpr (C::kFp8) {
+                            f[i][0] = fp8x2_to_f16x2<KV>(lo16(a[kt][i][s]));
+                            f[i][1] = fp8x2_to_f16x2<KV>(hi16(a[kt][i][s]));
+                        } else {
+                            f[i][0] = a[kt][i][2 * s];
+                            f[i][1] = a[kt][i][2 * s + 1];
+                        }
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma_16816<C::kF16>(sc[kt][nt], f[0][0], f[1][0], f[0][1], f[1][1], q[nt][0], q[nt][1]);
                 }
             }
         }
@@ -800,6 +814,7 @@ __global__ void __launch_bounds__(32 * C::kWarps, 1) window_kernel(const __grid_
     }
 
     Warp w;
+    w.q_at = smem_addr(smem) + warp * C::kRing + C::kStages * (C::kStage + 16) + 8 * lane;
     int last = -1, begun = -1;   // the segment of the sums that the warp still holds; the one that it found begun and ended
     if (t0 < t1) {
         const uint32_t ring = smem_addr(smem) + warp * C::kRing;
@@ -831,20 +846,25 @@ __global__ void __launch_bounds__(32 * C::kWarps, 1) window_kernel(const __grid_
                 ++b;
             request(b);
         };
-        // Lane's row of the tile at ld: its page, and its number within the page's rows.  Looked up one tile ahead of the
-        // copies, which wait for it.  Rows behind the last are copies of it: their weights are 0.
-        int page = 0;
-        uint32_t in_page = 0;
+        // Lane's rows of the tile at ld: their pages, and their numbers within a page's rows.  Looked up one tile ahead of
+        // the copies, which wait for them.  Rows behind the last are copies of it: their weights are 0.
+        constexpr int kMine = kTile > 32 ? kTile / 32 : 1;
+        int page[kMine];
+        uint32_t in_page[kMine];
         auto position = [&](int row) { return row < ld.head ? row : row + ld.skip; };
         auto look_up = [&]() {
-            int slot = position(min(ld.j * kTile + (lane & (kTile - 1)), ld.rows - 1));
-            page = ld.b;
-            if (p.block_table) {
-                const int blk = p.page_shift >= 0 ? slot >> p.page_shift : (int)((unsigned)slot / (unsigned)p.page_size);
-                slot -= blk * p.page_size;
-                page = ld.pages[blk];
+            const uint32_t head_row = (uint32_t)(ld.h * p.team + lead) * p.row_head;
+#pragma unroll
+            for (int m = 0; m < kMine; ++m) {
+                int slot = position(min(ld.j * kTile + 32 * m + (lane & (kTile - 1)), ld.rows - 1));
+                page[m] = ld.b;
+                if (p.block_table) {
+                    const int blk = p.page_shift >= 0 ? slot >> p.page_shift : (int)((unsigned)slot / (unsigned)p.page_size);
+                    slot -= blk * p.page_size;
+                    page[m] = ld.pages[blk];
+                }
+                in_page[m] = (uint32_t)slot * p.row_token + head_row;
             }
-            in_page = (uint32_t)slot * p.row_token + (uint32_t)(ld.h * p.team + lead) * p.row_head;
         };
         // Places of the lane's pieces: the first of a copy, and of every other copy.
         constexpr int kCopies = kTile * kGran / 32, kRows = 32 / kGran;   // copies of a lane, rows of a copy
@@ -852,9 +872,14 @@ __global__ void __launch_bounds__(32 * C::kWarps, 1) window_kernel(const __grid_
         const uint32_t to_even = lane / kGran * kRow + ((lane % kGran ^ window_swizzle<kGran>(lane / kGran)) << 4);
         const uint32_t to_odd = lane / kGran * kRow + ((lane % kGran ^ window_swizzle<kGran>(lane / kGran + kRows)) << 4);
         auto copy = [&](int stage) {
-            if ((unsigned)page >= (unsigned)p.num_pages) {
-                page = 0;
-                atomicOr(p.ws_err, kErrPage);
+            uint32_t row[kMine];
+#pragma unroll
+            for (int m = 0; m < kMine; ++m) {
+                if ((unsigned)page[m] >= (unsigned)p.num_pages) {
+                    page[m] = 0;
+                    atomicOr(p.ws_err, kErrPage);
+                }
+                row[m] = (uint32_t)page[m] * p.row_page + in_page[m];
             }
             const int row0 = ld.j * kTile, n = min(kTile, ld.rows - row0);
             // is every row visible to every new token?
@@ -868,11 +893,10 @@ __global__ void __launch_bounds__(32 * C::kWarps, 1) window_kernel(const __grid_
             }
             sts128(meta + 16 * stage, ld.b, ld.h, row0, n << kTileN | (plain ? kTilePlain : 0) | (ld.j == 0 ? kTileFirst : 0) |
                                                             (ld.j + 1 == ld.nb ? kTileLast : 0));
-            const uint32_t row = (uint32_t)page * p.row_page + in_page;
             const uint32_t k = ring + stage * C::kStage, even = k + to_even, odd = k + to_odd;
 #pragma unroll
             for (int i = 0; i < kCopies; ++i) {
-                const size_t at = (size_t)__shfl_sync(0xffffffffu, row, i * kRows + lane / kGran) * kRow;
+                const size_t at = (size_t)__shfl_sync(0xffffffffu, row[i * kRows / 32], (i * kRows + lane / kGran) & 31) * kRow;
                 // the swizzle has a period of 4 rows: of 1, 2 or 4 copies
                 const uint32_t to = kRows >= 4 ? even + i * kRows * kRow : kRows == 2 ? (i & 1 ? odd : even) + i * kRows * kRow
                                                : k + i * kRow + ((lane % kGran ^ window_swizzle<kGran>(i)) << 4);
@@ -882,11 +906,14 @@ __global__ void __launch_bounds__(32 * C::kWarps, 1) window_kernel(const __grid_
             if constexpr (C::kFp4) {
                 constexpr int kS = C::kScaleRow;
                 const uint32_t ks = k + 2 * kTile * kRow, vs = ks + kTile * kS;
-                if constexpr (kTile == 32) {
-                    cp_async_small<kS>(ks + lane * kS, p.ks + (size_t)row * kS, policy);
-                    cp_async_small<kS>(vs + lane * kS, p.vs + (size_t)row * kS, policy);
+                if constexpr (kTile >= 32) {
+#pragma unroll
+                    for (int m = 0; m < kMine; ++m) {
+                        cp_async_small<kS>(ks + (32 * m + lane) * kS, p.ks + (size_t)row[m] * kS, policy);
+                        cp_async_small<kS>(vs + (32 * m + lane) * kS, p.vs + (size_t)row[m] * kS, policy);
+                    }
                 } else   // rows of K for half the lanes, of V for the others
-                    cp_async_small<kS>((lane < 16 ? ks : vs - 16 * kS) + lane * kS, (lane < 16 ? p.ks : p.vs) + (size_t)row * kS, policy);
+                    cp_async_small<kS>((lane < 16 ? ks : vs - 16 * kS) + lane * kS, (lane < 16 ? p.ks : p.vs) + (size_t)row[0] * kS, policy);
             }
         };
 
