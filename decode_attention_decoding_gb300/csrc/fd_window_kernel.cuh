@@ -786,6 +786,7 @@ __global__ void __launch_bounds__(32 * C::kWarps, 1) window_kernel(const __grid_
     int *nonempty = prefix + p.batch + 1, *tmp = nonempty + p.batch + 1;
     int *s_seg = tmp + 2 * kWindowMaxWarps, *s_size = s_seg + 2 * kWindowMaxWarps;
     WindowParts *s_parts = reinterpret_cast<WindowParts *>(s_size + 2 * kWindowMaxWarps);
+    int *s_merges = tmp;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
 
     pdl_launch_dependents();
@@ -1078,26 +1079,27 @@ __global__ void __launch_bounds__(32 * C::kWarps, 1) window_kernel(const __grid_
     }
 
     // The CTA that writes the last partial of a segment adds them up, in the order of the workers.
-    __threadfence();
     __syncthreads();
-    if (threadIdx.x < 2 * C::kWarps) {
-        const int a = threadIdx.x;
+    if (warp == 0) {
         bool merge = false;
-        if (s_size[a] > 0 && s_parts[a].n > 1) {
-            unsigned int *count = p.ws_counts + s_parts[a].w0 * p.team + lead_of;
-            merge = atomicAdd(count, 1u) == (unsigned)s_parts[a].n - 1;
+        if (lane < 2 * C::kWarps && s_size[lane] > 0 && s_parts[lane].n > 1) {
+            unsigned int *count = p.ws_counts + s_parts[lane].w0 * p.team + lead_of;
+            __threadfence();   // the CTA's partials before the count, and the others' after it
+            merge = atomicAdd(count, 1u) == (unsigned)s_parts[lane].n - 1;
+            __threadfence();
             if (merge)
                 *count = 0;
         }
-        s_size[a] = merge ? 1 : 0;
+        const uint32_t all = __ballot_sync(0xffffffffu, merge);
+        if (merge)
+            s_size[__popc(all & ((1u << lane) - 1))] = lane;   // the list of them; the sizes are used up
+        if (lane == 0)
+            *s_merges = __popc(all);
     }
     __syncthreads();
-    int merges = 0;
-    for (int a = 0; a < 2 * C::kWarps; ++a)
-        merges += s_size[a];
+    const int merges = *s_merges;
     if (merges == 0)
         return;
-    __threadfence();
     // Threads share the (segment, 4 dims) pairs, or several share the partials of one.
     const int total = merges * items, per = min(total, (int)blockDim.x), split = blockDim.x / per, mine = threadIdx.x / per;
     WindowSum *shared = reinterpret_cast<WindowSum *>(smem);
@@ -1107,9 +1109,7 @@ __global__ void __launch_bounds__(32 * C::kWarps, 1) window_kernel(const __grid_
         int a = 0, b = 0, head = 0, col = 0, d = 0;
         WindowSum x;
         if (active) {
-            int which = i / items;
-            while (which > 0 || s_size[a] == 0)
-                which -= s_size[a++];
+            a = s_size[i / items];
             const WindowParts parts = s_parts[a];
             const int seg = s_seg[a], of = a % C::kWarps % p.team;
             b = seg / heads;
