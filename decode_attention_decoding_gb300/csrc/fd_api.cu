@@ -268,7 +268,7 @@ namespace {
 
 using namespace fd;
 
-constexpr int kVersion = 10500;   // 1.5.0
+constexpr int kVersion = 10600;   // 1.6.0
 constexpr unsigned long long kDefaultTimeoutNs = 2000000000ull;
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }

@@ -43,14 +43,25 @@ struct WindowCfg {
     static constexpr int kRow = kFp4 ? D / 2 : kFp8 ? D : 2 * D;   // bytes of a row
     static constexpr int kGran = kRow / 16;                  // 16-byte pieces of a row
     static constexpr int kScaleRow = kFp4 ? D / 16 : 0;      // bytes of a row's block scales
-    static constexpr int kTile = kFp4 && D == 128 && NT == 1 ? 64 : kRow <= 64 || (kRow <= 128 && !kFp4) ? 32 : 16;   // rows of a tile
+    // Rows of a tile, and warps of a CTA (12 and 16 leave 168 and 128 registers a thread, fewer 255).  Every warp has two
+    // tiles, one on its way: some 64 KB in flight on an SM, more of it was slower wherever memory is the bound (a window
+    // of 4096 over 64 GQA-4 requests, 8 warps: 166 us with one tile ahead, 186 with two).  Measured over 400 MB in 8
+    // requests of 8 heads (us, 1 / 8 / 16 columns), rows x warps: 4 bits, 64 dims: 32 x 12 114 / 117 / 161, 64 x 8
+    // 107 / 114 / 149, 64 x 12 98 / 105 / 147, 64 x 16 92 / 101 / 162; 128 dims: 32 x 12 88 / 99 / 144, 64 x 8 85 / 93 /
+    // 134; 256 dims: 16 x 8 99 / 114 / 163, 32 x 8 85 / 102 / 151 (no room with 16 columns); FP8, 64 dims: 32 x 12
+    // 73 / 78 / 95, 64 x 8 71 / 75 / 96; 128 dims: 16 x 8 86 / 91 / 106, 32 x 8 67 / 74 / 93, 64 x 4 69 / 82 / 126; 256
+    // dims: 16 x 8 67 / 78 / 101, 32 x 4 69 / 85 / 123; 16 bits, 64 dims: 16 x 8 86 / 87 / 93, 32 x 8 69 / 70 / 76, 64 x 4
+    // 71 / 74 / 85; 128 dims: 16 x 8 68 / 71 / 77, 32 x 4 69 / 72 / 85.  The floor is 59.
+    static constexpr int kTile = kFp4   ? (D < 256 ? 64 : NT == 1 ? 32 : 16)
+                                 : kFp8 ? (D == 64 ? (NT == 1 ? 64 : 32) : D == 128 ? 32 : 16)
+                                        : (D == 64 ? 32 : 16);
+    static constexpr int kWarps = kFp4 && D == 64 ? (NT == 1 ? 16 : 12) : kFp8 && D == 64 && NT == 2 ? 12 : !kFp4 && !kFp8 && D == 256 ? 4 : 8;
     static constexpr int kStage = 2 * kTile * (kRow + kScaleRow);
-    static constexpr int kWarps = kStage <= 4800 && D < 256 && NT == 1 ? 12 : kStage <= 9300 ? 8 : 4;
     // Two words a lane of each k step of the query: in registers where there are some left.
     static constexpr bool kQueryShared = NT == 2;
     static constexpr int kQuery = kQueryShared ? 16 * D * NT : 0;
     static constexpr int kSums = (int)sizeof(float) * NT * 8 * (D + 2);   // bytes of a warp's sums, left in its ring at the end
-    static constexpr int kStages = kSums <= 2 * kStage + kQuery ? 2 : (kSums - kQuery + kStage - 1) / kStage;
+    static constexpr int kStages = 2;
     static constexpr int kRing = (kStage + 16) * kStages + kQuery;   // bytes of a warp's tiles, of what each is, and of the query
 };
 
