@@ -28,6 +28,8 @@ constexpr int kWindowMaxColumns = 16;
 // flushes its outputs there.
 constexpr int kWindowSegCost = 1;
 
+constexpr int kWindowAbout = 32;   // bytes that say what a tile is
+
 // Shape of the split kernel for head dim D, a cache of type KV and MMAs of 8 NT
 // query columns.
 template <int D_, int KV_, int NT_>
@@ -62,7 +64,7 @@ struct WindowCfg {
     static constexpr int kQuery = kQueryShared ? 16 * D * NT : 0;
     static constexpr int kSums = (int)sizeof(float) * NT * 8 * (D + 2);   // bytes of a warp's sums, left in its ring at the end
     static constexpr int kStages = 2;
-    static constexpr int kRing = (kStage + 16) * kStages + kQuery;   // bytes of a warp's tiles, of what each is, and of the query
+    static constexpr int kRing = (kStage + kWindowAbout) * kStages + kQuery;   // bytes of a warp's tiles, of what each is, and of the query
 };
 
 struct WindowParams {
@@ -86,7 +88,7 @@ struct WindowParams {
 
 // What a request's new tokens see together.
 struct WindowReq {
-    int L, head, first, rows;
+    int L, head, first, rows;   // L = rows + first - head
 };
 __device__ __forceinline__ WindowReq window_req(const WindowParams &p, int b, unsigned int *err)
 {

@@ -87,16 +87,6 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b)
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-template <bool F16>
-__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b)
-{
-    uint32_t r;
-    if constexpr (F16)
-        asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    else
-        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
 // As mma_16816 with C = 0.
 template <bool F16>
 __device__ __forceinline__ void mma_16816_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
@@ -360,11 +350,11 @@ struct WindowWarp {
                             sc[kt][nt][2 * a + e] = -__builtin_huge_valf();
             }
     }
-    // Whether the token at position `own` sees row v of the request.
+    // Whether the token at position `own` sees row v of the request (v may pass 2^31 in a tile's last rows).
     __device__ __forceinline__ static bool visible(const WindowParams &p, const WindowReq &req, int v, int own)
     {
         const int pos = window_pos(req, v);
-        return v < req.rows && pos <= own && (!p.window || pos < p.sinks || own - pos < p.window);
+        return (unsigned)v < (unsigned)req.rows && pos <= own && (!p.window || pos < p.sinks || own - pos < p.window);
     }
 
     // Move the references up to the tile's scores if one passes its limit, which is rare after the first tiles.
@@ -410,9 +400,8 @@ struct WindowWarp {
     // The reference of a column, -inf if nothing was seen.
     __device__ __forceinline__ float reference(int nt, int e) const { return limit[nt][e] - kSlack; }
 
-    // The scores' softmax weights in parts, as the B operand of O^T: pf[kt][part][nt][2].  Where V may hold infinities,
-    // no part is less than `least`: an infinity times a part that is 0 would be NaN.
-    __device__ __forceinline__ void weights(const float (&sc)[KT][NT][4], uint32_t least, int c, uint32_t (&pf)[KT][kParts][NT][2])
+    // The scores' softmax weights in parts, as the B operand of O^T: pf[kt][part][nt][2].
+    __device__ __forceinline__ void weights(const float (&sc)[KT][NT][4], int c, uint32_t (&pf)[KT][kParts][NT][2])
     {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -430,8 +419,6 @@ struct WindowWarp {
                         const float2 top = f16x2_to_float2(w);
                         const uint32_t rest = pack_f16x2(x - top.x, y - top.y);
                         w = c & 2 ? rest : w;
-                        if constexpr (C::kInf)
-                            w = max2<true>(w, least);
                         pf[kt][0][nt][a] = movmatrix_trans(w);
                     } else {
 #pragma unroll
@@ -445,8 +432,6 @@ struct WindowWarp {
                                 x -= top.x;
                                 y -= top.y;
                             }
-                            if constexpr (C::kInf)
-                                w = max2<C::kF16>(w, least);
                             pf[kt][part][nt][a] = movmatrix_trans(w);
                         }
                     }
@@ -558,53 +543,98 @@ struct WindowWarp {
     {
         constexpr int kBytes = C::kFp4 ? kTile * C::kScaleRow : kTile * kRow;
         const uint32_t at = C::kFp4 ? vs : v;
-        bool bad = false;
-        for (int i = 4 * lane; i < kBytes; i += 128)
-            bad = bad || not_finite(lds32(at + i));
-        if (!__any_sync(0xffffffffu, bad))
+        uint32_t bad = 0;
+        for (int i = 16 * lane; i < kBytes; i += 512) {
+            const uint4 w = lds128(at + i);
+            bad |= not_finite(w.x) | not_finite(w.y) | not_finite(w.z) | not_finite(w.w);
+        }
+        if (!__any_sync(0xffffffffu, bad != 0))
             return;
         const int g = lane >> 2, c = lane & 3;
-        for (int r = 0; r < kTile; ++r) {
+        for (int r = 0; r < kTile; ++r)
 #pragma unroll
             for (int s = 0; s < kSteps; ++s)
 #pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    const float x = element(v, vs, r, block_dim(s, g) + y);
-                    if (fabsf(x) < __builtin_huge_valf())
-                        continue;
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int i = min(((nt * 8 + 2 * c + e) & kColMask) / p.group, p.q_len - 1);
-                            if (visible(p, req, row0 + r, req.L - p.q_len + i))
-                                acc[s][nt][2 * y + e] += x;
-                        }
-                }
-        }
+                for (int y = 0; y < 2; ++y)
+                    add_not_finite(p, req, row0 + r, s, y, c, element(v, vs, r, block_dim(s, g) + y));
         __syncwarp();
         for (int i = 4 * lane; i < kBytes; i += 128) {
             uint32_t w = lds32(at + i);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint32_t keep = C::kFp4 || C::kFp8 ? 0xFFu << 8 * e : 0xFFFFu << 16 * (e & 1);
-                if (not_finite(w & keep))
-                    w &= ~keep;
-            }
+            constexpr int kTop = C::kFp4 || C::kFp8 ? 7 : 15;
+            w &= ~((not_finite(w) >> kTop) * (kTop == 7 ? 0xFFu : 0xFFFFu));
             asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + i), "r"(w) : "memory");
         }
         __syncwarp();
     }
-    // Whether one of the elements (scales of a 4-bit cache) in w is an infinity or NaN.
-    __device__ __forceinline__ static bool not_finite(uint32_t w)
+    // The top bits of the elements (scales of a 4-bit cache) in w that are infinities or NaN.
+    __device__ __forceinline__ static uint32_t not_finite(uint32_t w)
     {
-        constexpr uint32_t kMask = C::kFp4 || KV == kKvE4m3 ? 0x7Fu : KV == kKvE5m2 ? 0x7Cu : KV == kKvF16 ? 0x7C00u : 0x7F80u;
-        bool bad = false;
-#pragma unroll
-        for (int e = 0; e < 32; e += C::kFp4 || C::kFp8 ? 8 : 16)
-            bad = bad || (w >> e & kMask) == kMask;
-        return bad;
+        constexpr uint32_t kExp = C::kFp4 || KV == kKvE4m3 ? 0x7F7F7F7Fu : KV == kKvE5m2 ? 0x7C7C7C7Cu : KV == kKvF16 ? 0x7C007C00u : 0x7F807F80u;
+        constexpr uint32_t kTop = C::kFp4 || C::kFp8 ? 0x80808080u : 0x80008000u;
+        constexpr uint32_t kStep = C::kFp4 || KV == kKvE4m3 ? 0x01010101u : KV == kKvE5m2 ? 0x04040404u : KV == kKvF16 ? 0x04000400u : 0x00800080u;
+        return ((w & kExp) + kStep) & kTop;
     }
+    // Add x, dim block_dim(s, g) + y of row v, to the sums of the columns that see the row, if it is not finite.
+    __device__ __forceinline__ void add_not_finite(const WindowParams &p, const WindowReq &req, int v, int s, int y, int c, float x)
+    {
+        if (fabsf(x) < __builtin_huge_valf())
+            return;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int i = min(((nt * 8 + 2 * c + e) & kColMask) / p.group, p.q_len - 1);
+                if (visible(p, req, v, req.L - p.q_len + i))
+                    acc[s][nt][2 * y + e] += x;
+            }
+    }
+    // An infinite V element times a weight's part that is 0 or less than 0 is NaN.  So where sums are NaN though the
+    // weights are not, they become what the elements that are not finite add up to, of the rows [from, to) that they have.
+    __device__ __forceinline__ void repair(const WindowParams &p, int b, int head, int from, int to, int g, int c)
+    {
+        bool broken = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    broken = broken || (acc[s][nt][e] != acc[s][nt][e] && l[nt][e & 1] == l[nt][e & 1]);
+        if (!__any_sync(0xffffffffu, broken))
+            return;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (acc[s][nt][e] != acc[s][nt][e] && l[nt][e & 1] == l[nt][e & 1])
+                        acc[s][nt][e] = 0.f;
+        const WindowReq req = window_req(p, b, nullptr);
+        for (int v = from; v < to; ++v) {
+            int slot = window_pos(req, v), page = b;
+            if (p.block_table) {
+                const int blk = slot / p.page_size;
+                slot -= blk * p.page_size;
+                page = p.block_table[(long long)b * p.max_blocks + blk];
+                page = (unsigned)page < (unsigned)p.num_pages ? page : 0;
+            }
+            const uint8_t *row = p.v + (size_t)((uint32_t)page * p.row_page + (uint32_t)slot * p.row_token + (uint32_t)head * p.row_head) * kRow;
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const int dim = block_dim(s, g) + y;
+                    float x;
+                    if constexpr (C::kFp8)
+                        x = fp8x2_to_float2<KV>((uint16_t)row[dim]).x;
+                    else
+                        x = x2_to_float2<C::kF16>(reinterpret_cast<const uint16_t *>(row)[dim]).x;
+                    add_not_finite(p, req, v, s, y, c, x);
+                }
+        }
+    }
+
     // V's element of row r and dim d of the tile.
     __device__ __forceinline__ static float element(uint32_t v, uint32_t vs, int r, int d)
     {
@@ -672,7 +702,7 @@ __device__ __forceinline__ void window_schedule(const WindowParams &p, int *pref
         const int b = b0 + threadIdx.x;
         int n = 0;
         if (b < p.batch)
-            n = (window_req(p, b, report ? p.ws_err : nullptr).rows + TILE - 1) / TILE;
+            n = (int)(((unsigned)window_req(p, b, report ? p.ws_err : nullptr).rows + TILE - 1) / TILE);   // rows may be close to 2^31
         int x = n * heads, y = n > 0 ? 1 : 0;
         const int mx = x, my = y;
 #pragma unroll
@@ -815,11 +845,12 @@ __global__ void __launch_bounds__(32 * C::kWarps, 1) window_kernel(const __grid_
     }
 
     Warp w;
-    w.q_at = smem_addr(smem) + warp * C::kRing + C::kStages * (C::kStage + 16) + 8 * lane;
+    w.q_at = smem_addr(smem) + warp * C::kRing + C::kStages * (C::kStage + kWindowAbout) + 8 * lane;
+    int from = 0, to = 0;        // the rows of a segment that the warp has summed
     int last = -1, begun = -1;   // the segment of the sums that the warp still holds; the one that it found begun and ended
     if (t0 < t1) {
         const uint32_t ring = smem_addr(smem) + warp * C::kRing;
-        const uint32_t meta = ring + kStages * C::kStage;   // of each tile: request, launch head, first row, kTile* and its rows
+        const uint32_t meta = ring + kStages * C::kStage;   // of each tile: request, launch head, first row, kTile* and its rows; the request's rows, head, skip
         const uint64_t policy = l2_policy_evict_first();
 
         WindowCursor ld;
@@ -857,7 +888,7 @@ __global__ void __launch_bounds__(32 * C::kWarps, 1) window_kernel(const __grid_
             const uint32_t head_row = (uint32_t)(ld.h * p.team + lead) * p.row_head;
 #pragma unroll
             for (int m = 0; m < kMine; ++m) {
-                int slot = position(min(ld.j * kTile + 32 * m + (lane & (kTile - 1)), ld.rows - 1));
+                int slot = position((int)min((unsigned)(ld.j * kTile + 32 * m + (lane & (kTile - 1))), (unsigned)(ld.rows - 1)));
                 page[m] = ld.b;
                 if (p.block_table) {
                     const int blk = p.page_shift >= 0 ? slot >> p.page_shift : (int)((unsigned)slot / (unsigned)p.page_size);
@@ -892,7 +923,9 @@ __global__ void __launch_bounds__(32 * C::kWarps, 1) window_kernel(const __grid_
                     plain = plain && (row0 + kTile <= ld.head || ld.rows + ld.skip - 1 - behind < p.window);
                 }
             }
-            sts128(meta + 16 * stage, ld.b, ld.h, row0, n << kTileN | (plain ? kTilePlain : 0) | (ld.j == 0 ? kTileFirst : 0) |
+            if (p.q_len > 1)
+                sts128(meta + kWindowAbout * stage + 16, ld.rows, ld.head, ld.skip, 0);
+            sts128(meta + kWindowAbout * stage, ld.b, ld.h, row0, n << kTileN | (plain ? kTilePlain : 0) | (ld.j == 0 ? kTileFirst : 0) |
                                                             (ld.j + 1 == ld.nb ? kTileLast : 0));
             const uint32_t k = ring + stage * C::kStage, even = k + to_even, odd = k + to_odd;
 #pragma unroll
@@ -931,12 +964,13 @@ __global__ void __launch_bounds__(32 * C::kWarps, 1) window_kernel(const __grid_
             cp_async_commit();
         };
         const bool first = ld.j == 0;
-        const int b0 = ld.b, h0 = ld.h;
+        const int b0 = ld.b, h0 = ld.h, from0 = ld.j * kTile;
 #pragma unroll
         for (int i = 0; i < kStages - 1; ++i)
             fetch(i);
         w.start(p, b0, h0 * p.team + lead, g, c);   // while the first tile is on its way
         last = b0 * heads + h0;
+        from = from0;
 
         const WindowPlaces<C> places(g, c);
         int stage = 0;
@@ -945,12 +979,14 @@ __global__ void __launch_bounds__(32 * C::kWarps, 1) window_kernel(const __grid_
             cp_async_wait<kStages - 2>();
             __syncwarp();
             fetch(stage == 0 ? kStages - 1 : stage - 1);
-            const uint4 tile = lds128(meta + 16 * stage);
+            const uint32_t about = meta + kWindowAbout * stage;
+            const uint4 tile = lds128(about);
             const int b = (int)tile.x, h = (int)tile.y, row0 = (int)tile.z, flags = (int)tile.w;
             const int seg = b * heads + h, head = h * p.team + lead;
             if (seg != last) {
                 w.start(p, b, head, g, c);
                 last = seg;
+                from = row0;
                 whole = flags & kTileFirst;
             }
             const uint32_t k = ring + stage * C::kStage, v = k + kTile * kRow, ks = v + kTile * kRow, vs = ks + kTile * C::kScaleRow;
@@ -958,23 +994,25 @@ __global__ void __launch_bounds__(32 * C::kWarps, 1) window_kernel(const __grid_
             float sc[Warp::KT][NT][4];
             uint32_t pf[Warp::KT][Warp::kParts][NT][2];
             w.scores(places, k, ks, sc);
-            uint32_t least = C::kF16 ? 0x00010001u : 0x00800080u;   // 2^-38 or 2^-126 of a reference's weight
             if (!(flags & kTilePlain)) {
                 if (p.q_len == 1)
                     w.cut(flags >> kTileN, g, sc);
                 else {
-                    const WindowReq req = window_req(p, b, nullptr);
+                    const uint4 what = lds128(about + 16);
+                    const WindowReq req = {(int)(what.x + what.z), (int)what.y, (int)(what.y + what.z), (int)what.x};
                     w.mask(p, req, row0, g, c, sc);
                     w.screen(p, req, row0, v, vs, lane);
-                    least = 0u;
                 }
             }
             w.rescale(sc);
-            w.weights(sc, least, c, pf);
+            w.weights(sc, c, pf);
             w.values(places, v, vs, pf);
+            to = row0 + (flags >> kTileN);
             if ((flags & kTileLast) && (whole || t + 1 < t1)) {
                 // the segment ends inside the run: its output, or a partial of a segment that others began
                 w.finish();
+                if constexpr (C::kInf)
+                    w.repair(p, b, head, from, to, g, c);
                 const long long slot_o = (long long)(2 * worker) * p.team + lead;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -1014,6 +1052,8 @@ __global__ void __launch_bounds__(32 * C::kWarps, 1) window_kernel(const __grid_
     // sums in its own ring.
     if (last >= 0) {
         w.finish();
+        if constexpr (C::kInf)
+            w.repair(p, last / heads, last % heads * p.team + lead, from, to, g, c);
         float *ml = reinterpret_cast<float *>(smem + warp * C::kRing), *sum = ml + kMl;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)

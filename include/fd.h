@@ -683,7 +683,8 @@ fd_status fd_cache_read4(const int64_t *slot_map, int num_tokens, int num_kv_hea
  * columns Hq/Hkv x q_len of head_dim 128); initialise it once with
  * fd_workspace_init.  A workspace of one shape serves every shape with no more
  * requests, no more columns and no larger head_dim.  Pure host function; 0 for
- * shapes that no call accepts. */
+ * shapes that no call accepts.  It holds counts that every call leaves at 0:
+ * memory that anything else has written to is initialised again first. */
 size_t fd_window_workspace_size(int batch, int num_q_heads, int num_kv_heads, int head_dim, int q_len);
 
 /*

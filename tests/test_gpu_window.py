@@ -165,6 +165,57 @@ def test_visible_infinities(fd, kv, hq, T):
         assert bool(o[..., [0, 1, 4, 6, 8, 10, 12, 21, 63]].isfinite().all())
 
 
+@pytest.mark.parametrize("kv", ["bf16", "f16", "e5m2"])
+@pytest.mark.parametrize("T", [1, 3])
+def test_large_values_without_weight(fd, kv, T):
+    """V of the type's largest numbers at positions whose weights are below 2^-60: they leave no trace beside weights of 1."""
+    L = 3000
+    c = u.make_case(23, 1, T, 4, 2, 128, [L], kv=kv)
+    big = float(torch.finfo(u.TYPES[kv]).max) if kv != "bf16" else 2.0 ** 20
+    q = torch.ones_like(c["q"]) * 4
+    c["q"], c["q64"] = q, q.double().numpy()
+    for name, i, far, near in (("k64", 0, -1.0, 0.0), ("v64", 1, big, 1.0)):
+        x = np.full((L, 2, 128), far)
+        x[100::977] = near
+        c[name][0] = x
+        c["pool"][i][0] = torch.from_numpy(x).to(c["pool"][i].dtype)
+    o, lse = u.run(fd, c, 0.125)          # scores of -64 nats, 2^-92, and 0: at most 3 rows of weight 1 a token
+    assert float((o - 1.0).abs().max()) <= 2.0 ** -20
+    check(o, lse, u.want(c, 0.125))
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e2m1"])
+@pytest.mark.parametrize("T", [1, 3])
+def test_lengths_next_to_2_31(fd, kv, T):
+    """A window at the end of a request of 2^31 - 2 tokens: pages of 49981, of which two are seen."""
+    page, blocks, W, S = 49981, 42966, 130, 3
+    L = page * blocks
+    assert L == 2 ** 31 - 2
+    c = u.make_case(24, 1, T, 4, 2, 64, [W + T - 1 + S], kv=kv)      # what is seen, one after another
+    n = W + T - 1 + S
+    pool = [torch.empty(3, *((2, page) if kv == "e2m1" else (page, 2)), t.shape[-1], dtype=t.dtype, device="cuda") for t in c["pool"]]
+    for t, x in zip(pool, c["pool"]):
+        x = x[0].cuda()
+        for row in range(n):
+            pos = row if row < S else L - n + row
+            pg, slot = (1 if pos < page else 2), pos % page
+            if kv == "e2m1":
+                t.view(torch.uint8)[pg, :, slot] = x.view(torch.uint8)[:, row]
+            else:
+                t[pg, slot] = x[row]
+    table = torch.full((1, blocks), -5, dtype=torch.int32, device="cuda")
+    table[0, 0], table[0, -1] = 1, 2
+    lens = torch.tensor([L], dtype=torch.int32, device="cuda")
+    q = c["q"].cuda()
+    ks, vs = scales(kv)
+    kw = dict(window=W, sinks=S, scale=0.1, k_scale=ks, v_scale=vs)
+    ws = fd.make_window_workspace(1, 4, 2, 64, q_len=T)
+    o, lse = (fd.fd_decode4_paged(q, fd.Cache4(*pool), table, lens, workspace=ws, **kw) if kv == "e2m1"
+              else fd.fd_window_decode_paged(q, *pool, table, lens, workspace=ws, **kw))
+    check(o, lse, u.attention(c["q64"], c["k64"], c["v64"], [n], W, S, 0.1 * ks, vs))
+    assert fd.fd_get_device_error(ws) == fd.FD_OK
+
+
 @pytest.mark.parametrize("kv", KINDS)
 def test_as_fd_decode(fd, kv):
     """A window over everything is fd_decode, whose cache is in 16 bits or FP8; a 4-bit one is compared with its values in fp16."""
