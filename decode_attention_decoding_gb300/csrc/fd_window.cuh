@@ -28,6 +28,9 @@ constexpr int kWindowMaxColumns = 16;
 // flushes its outputs there.
 constexpr int kWindowSegCost = 1;
 
+// Tiles a warp that a segment may have to be one CTA's (fd_window_kernel.cuh).
+constexpr int kWindowSegmentTiles = 2;
+
 constexpr int kWindowAbout = 32;   // bytes that say what a tile is
 
 // Shape of the split kernel for head dim D, a cache of type KV and MMAs of 8 NT

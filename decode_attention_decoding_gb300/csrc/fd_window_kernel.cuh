@@ -691,20 +691,21 @@ __device__ __forceinline__ float window_lse(float m, float l)
     return l == 0.f ? -__builtin_huge_valf() : ((m == -__builtin_huge_valf() ? 0.f : m) + log2f(l)) * 0.6931471805599453f;
 }
 
-// The CTA's copy of the schedule: prefix and non-empty requests in shared memory.
+// The CTA's copy of the schedule: prefix and non-empty requests in shared memory.  Returns the tiles of the longest
+// segment.
 template <int TILE>
-__device__ __forceinline__ void window_schedule(const WindowParams &p, int *prefix, int *nonempty, int *tmp, bool report)
+__device__ __forceinline__ int window_schedule(const WindowParams &p, int *prefix, int *nonempty, int *tmp, bool report)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int heads = p.hkv / p.team;
-    int run = 0, live = 0;
+    int run = 0, live = 0, most = 0;
     for (int b0 = 0; b0 < p.batch; b0 += blockDim.x) {
         const int b = b0 + threadIdx.x;
         int n = 0;
         if (b < p.batch)
             n = (int)(((unsigned)window_req(p, b, report ? p.ws_err : nullptr).rows + TILE - 1) / TILE);   // rows may be close to 2^31
         int x = n * heads, y = n > 0 ? 1 : 0;
-        const int mx = x, my = y;
+        const int mx = x, my = y, top = __reduce_max_sync(0xffffffffu, n);
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const int a = __shfl_up_sync(0xffffffffu, x, off), c = __shfl_up_sync(0xffffffffu, y, off);
@@ -714,8 +715,9 @@ __device__ __forceinline__ void window_schedule(const WindowParams &p, int *pref
             }
         }
         if (lane == 31) {
-            tmp[2 * warp] = x;
-            tmp[2 * warp + 1] = y;
+            tmp[3 * warp] = x;
+            tmp[3 * warp + 1] = y;
+            tmp[3 * warp + 2] = top;
         }
         __syncthreads();
         int bx = 0, by = 0, ax = 0, ay = 0;
@@ -724,8 +726,9 @@ __device__ __forceinline__ void window_schedule(const WindowParams &p, int *pref
                 bx = ax;
                 by = ay;
             }
-            ax += tmp[2 * w];
-            ay += tmp[2 * w + 1];
+            ax += tmp[3 * w];
+            ay += tmp[3 * w + 1];
+            most = max(most, tmp[3 * w + 2]);
         }
         if (b < p.batch) {
             prefix[b] = run + bx + x - mx;
@@ -733,13 +736,15 @@ __device__ __forceinline__ void window_schedule(const WindowParams &p, int *pref
         }
         run += ax;
         live += ay;
-        __syncthreads();
+        if (b0 + blockDim.x < p.batch)
+            __syncthreads();   // tmp is written again
     }
     if (threadIdx.x == 0) {
         prefix[p.batch] = run;
         nonempty[p.batch] = live;
     }
     __syncthreads();
+    return most;
 }
 
 // The partials of a segment that workers w0 .. w1 share: one of each CTA, and one more of w1 if it went on to another
@@ -768,7 +773,7 @@ struct WindowParts {
 
 // Shared memory: the warps' rings, then prefix and non-empty [batch + 1], then scratch: the scan's sums,
 // and what the warps hold at the end.
-constexpr int kWindowScratch = 2 * kWindowMaxWarps * (3 + (int)(sizeof(WindowParts) / sizeof(int)));
+constexpr int kWindowScratch = kWindowMaxWarps * (3 + 2 * (2 + (int)(sizeof(WindowParts) / sizeof(int))));
 template <class C>
 constexpr size_t window_smem(int batch)
 {
@@ -814,14 +819,14 @@ __global__ void __launch_bounds__(32 * C::kWarps, 1) window_kernel(const __grid_
     extern __shared__ __align__(128) uint8_t smem[];
     int *prefix = reinterpret_cast<int *>(smem + C::kWarps * C::kRing);
     int *nonempty = prefix + p.batch + 1, *tmp = nonempty + p.batch + 1;
-    int *s_seg = tmp + 2 * kWindowMaxWarps, *s_size = s_seg + 2 * kWindowMaxWarps;
+    int *s_seg = tmp + 3 * kWindowMaxWarps, *s_size = s_seg + 2 * kWindowMaxWarps;
     WindowParts *s_parts = reinterpret_cast<WindowParts *>(s_size + 2 * kWindowMaxWarps);
     int *s_merges = tmp;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
 
     pdl_launch_dependents();
     pdl_wait_prior_grid();
-    window_schedule<kTile>(p, prefix, nonempty, tmp, blockIdx.x == 0);
+    const int most = window_schedule<kTile>(p, prefix, nonempty, tmp, blockIdx.x == 0);
     const int heads = p.hkv / p.team;
     for (int b = blockIdx.x; b < p.batch; b += gridDim.x)   // requests that see nothing
         if (prefix[b] == prefix[b + 1])
@@ -832,12 +837,23 @@ __global__ void __launch_bounds__(32 * C::kWarps, 1) window_kernel(const __grid_
                     p.lse[row] = -__builtin_huge_valf();
             }
     WindowSchedule sch = {{prefix, nonempty, p.batch, heads, kWindowSegCost, 0}};
-    const int teams = window_workers(sch.cost(), gridDim.x, C::kWarps / p.team);
-    sch.P = gridDim.x * teams;
     const int team = warp / p.team, lead = warp - team * p.team;   // the warp's kv head of the team's
+    // A few short segments: one for a CTA, whose warps share its tiles, and nothing is left to join.
+    const int segments = nonempty[p.batch] * heads;
+    const bool by_segment = segments <= (int)gridDim.x && most <= kWindowSegmentTiles * (C::kWarps / p.team);
+    const int teams = by_segment ? C::kWarps / p.team : window_workers(sch.cost(), gridDim.x, C::kWarps / p.team);
+    sch.P = gridDim.x * teams;
     const int worker = blockIdx.x * teams + team;
     int t0 = 0, t1 = 0;
-    if (team < teams && worker < sch.ctas()) {
+    if (by_segment) {
+        if ((int)blockIdx.x < segments) {
+            const int b = request_of_tile(nonempty, p.batch, blockIdx.x / heads);
+            const int nb = (prefix[b + 1] - prefix[b]) / heads, share = (nb + teams - 1) / teams;
+            const int begin = prefix[b] + (int)(blockIdx.x % heads) * nb;
+            t0 = begin + min(nb, team * share);
+            t1 = begin + min(nb, (team + 1) * share);
+        }
+    } else if (team < teams && worker < sch.ctas()) {
         // odd lanes find the run's end
         const int t = sch.tile_at(sch.begin(worker + (lane & 1)));
         t0 = __shfl_sync(0xffffffffu, t, 0);
@@ -1089,7 +1105,10 @@ __global__ void __launch_bounds__(32 * C::kWarps, 1) window_kernel(const __grid_
                 while (a + n * p.team < 2 * C::kWarps && s_seg[a + n * p.team] == seg)
                     ++n;
             s_size[a] = n;
-            s_parts[a] = WindowParts(sch, teams, seg);
+            if (by_segment)
+                s_parts[a].n = 1;
+            else
+                s_parts[a] = WindowParts(sch, teams, seg);
         }
     }
     __syncthreads();
