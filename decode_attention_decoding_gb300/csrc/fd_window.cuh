@@ -111,29 +111,55 @@ __device__ __forceinline__ WindowReq window_req(const WindowParams &p, int b, un
 }
 __device__ __forceinline__ int window_pos(const WindowReq &r, int row) { return row < r.head ? row : row - r.head + r.first; }
 
+// fd_sched.h's Schedule with divisions of 32 bits where they do: a short call
+// waits for them (a 64-bit division costs some 100 instructions).
+static __device__ __noinline__ long long window_divide(long long x, long long y) { return x / y; }
+__device__ __forceinline__ long long window_quotient(long long x, long long y)
+{
+    return ((unsigned long long)x | (unsigned long long)y) >> 32 == 0 ? (long long)((uint32_t)x / (uint32_t)y) : window_divide(x, y);
+}
+struct WindowSchedule : Schedule {
+    long long total;   // cost()
+    int busy;          // ctas()
+    __device__ __forceinline__ int cta_at(long long pos) const { return (int)window_quotient(pos * busy, total); }
+    // the first tile of CTA c (as Schedule::tile_at of its first cost position)
+    __device__ __forceinline__ int first_tile(int c) const
+    {
+        const long long x = window_quotient(total * c + busy - 1, busy);
+        if (x >= total)
+            return tiles();
+        int lo = 0, hi = batch - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if ((long long)prefix[mid + 1] + (long long)w * hkv * nonempty[mid + 1] > x)
+                hi = mid;
+            else
+                lo = mid + 1;
+        }
+        const int nb = (prefix[lo + 1] - prefix[lo]) / hkv;
+        const long long q = x - ((long long)prefix[lo] + (long long)w * hkv * nonempty[lo]) - w;
+        if (q <= 0)
+            return prefix[lo];
+        long long h = window_quotient(q, nb + w), j = q - h * (nb + w);
+        if (j >= nb) {   // in the gap before head h + 1
+            ++h;
+            j = 0;
+        }
+        return prefix[lo] + (int)(h * nb + j);
+    }
+};
+
 // Workers (teams of p.team warps) of a CTA of a call of this cost: no more
 // than there is work for, so that a short call spreads over all SMs.
 __device__ __forceinline__ int window_workers(long long cost, int grid, int most)
 {
-    const long long want = (cost + grid - 1) / grid;
+    const long long want = window_quotient(cost + grid - 1, grid);
     return want < 1 ? 1 : want < most ? (int)want : most;
 }
 
 // A scale of 0 becomes this one, so that a hidden score (-inf) keeps its
 // weight of 0; scores below 1e30 are still 0.
 constexpr float kWindowLeastScale = 1e-37f;
-
-// fd_sched.h's Schedule with divisions of 32 bits where they do: a short call
-// waits for them (a 64-bit division costs some 100 instructions).
-struct WindowSchedule : Schedule {
-    __device__ __forceinline__ static long long quotient(long long x, long long y)
-    {
-        return (unsigned long long)x >> 32 == 0 && (unsigned long long)y >> 32 == 0 ? (long long)((uint32_t)x / (uint32_t)y) : x / y;
-    }
-    __device__ __forceinline__ int cta_at(long long pos) const { return (int)quotient(pos * ctas(), cost()); }
-    // cost position at which CTA c's tiles begin
-    __device__ __forceinline__ long long begin(int c) const { return quotient(cost() * c + ctas() - 1, ctas()); }
-};
 
 // Host side.
 struct WindowLaunch {

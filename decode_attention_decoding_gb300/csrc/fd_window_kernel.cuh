@@ -155,6 +155,22 @@ __device__ __forceinline__ void sts128(uint32_t addr, int x, int y, int z, int w
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
+// The rows that new token i of a request sees: [0, below) and [from, to).
+struct WindowSight {
+    int below, from, to;
+    __device__ __forceinline__ WindowSight(const WindowParams &p, const WindowReq &req, int i)
+    {
+        const int own = req.L - p.q_len + i, skip = req.first - req.head;
+        below = min(req.head, own + 1);
+        from = req.head;
+        if (p.window)
+            from = (int)max((long long)req.head, (long long)own - p.window - skip + 1);
+        to = own - skip + 1;
+    }
+    // v may pass 2^31 in a tile's last rows
+    __device__ __forceinline__ bool sees(int v) const { return v >= 0 && (v < below || (v >= from && v < to)); }
+};
+
 // One warp's place in the schedule.
 struct WindowCursor {
     int b, h, j, nb;        // request, launch head, tile of the segment, tiles of a segment
@@ -340,21 +356,14 @@ struct WindowWarp {
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int i = ((nt * 8 + 2 * c + e) & kColMask) / p.group;
-                const int own = req.L - p.q_len + min(i, p.q_len - 1);
+                const WindowSight sight(p, req, min(((nt * 8 + 2 * c + e) & kColMask) / p.group, p.q_len - 1));
 #pragma unroll
                 for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
                     for (int a = 0; a < 2; ++a)
-                        if (!visible(p, req, row0 + kt * 16 + r + 8 * a, own))
+                        if (!sight.sees(row0 + kt * 16 + r + 8 * a))
                             sc[kt][nt][2 * a + e] = -__builtin_huge_valf();
             }
-    }
-    // Whether the token at position `own` sees row v of the request (v may pass 2^31 in a tile's last rows).
-    __device__ __forceinline__ static bool visible(const WindowParams &p, const WindowReq &req, int v, int own)
-    {
-        const int pos = window_pos(req, v);
-        return (unsigned)v < (unsigned)req.rows && pos <= own && (!p.window || pos < p.sinks || own - pos < p.window);
     }
 
     // Move the references up to the tile's scores if one passes its limit, which is rare after the first tiles.
@@ -537,27 +546,21 @@ struct WindowWarp {
         }
     }
 
-    // Of a tile that some columns see in part: what V holds that is not finite goes to the sums of the columns that see
-    // it (whose other terms do not matter) and becomes 0 in the tile, so that weights of 0 do not make it NaN.
-    __device__ __forceinline__ void screen(const WindowParams &p, const WindowReq &req, int row0, uint32_t v, uint32_t vs, int lane)
+    // Of a tile that some columns see in part: what V holds that is not finite becomes 0 in the tile, so that weights of 0
+    // do not make it NaN.  True if there was some; window_repair has to account for it.
+    __device__ __forceinline__ static bool screen(uint32_t v, uint32_t vs, int lane)
     {
         constexpr int kBytes = C::kFp4 ? kTile * C::kScaleRow : kTile * kRow;
         const uint32_t at = C::kFp4 ? vs : v;
-        uint32_t bad = 0;
+        bool bad = false;
+#pragma unroll 2
         for (int i = 16 * lane; i < kBytes; i += 512) {
             const uint4 w = lds128(at + i);
-            bad |= not_finite(w.x) | not_finite(w.y) | not_finite(w.z) | not_finite(w.w);
+            bad = bad || (not_finite(w.x) | not_finite(w.y) | not_finite(w.z) | not_finite(w.w));
         }
-        if (!__any_sync(0xffffffffu, bad != 0))
-            return;
-        const int g = lane >> 2, c = lane & 3;
-        for (int r = 0; r < kTile; ++r)
-#pragma unroll
-            for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-                for (int y = 0; y < 2; ++y)
-                    add_not_finite(p, req, row0 + r, s, y, c, element(v, vs, r, block_dim(s, g) + y));
-        __syncwarp();
+        if (!__any_sync(0xffffffffu, bad))
+            return false;
+#pragma unroll 1
         for (int i = 4 * lane; i < kBytes; i += 128) {
             uint32_t w = lds32(at + i);
             constexpr int kTop = C::kFp4 || C::kFp8 ? 7 : 15;
@@ -565,6 +568,7 @@ struct WindowWarp {
             asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + i), "r"(w) : "memory");
         }
         __syncwarp();
+        return true;
     }
     // The top bits of the elements (scales of a 4-bit cache) in w that are infinities or NaN.
     __device__ __forceinline__ static uint32_t not_finite(uint32_t w)
@@ -574,81 +578,20 @@ struct WindowWarp {
         constexpr uint32_t kStep = C::kFp4 || KV == kKvE4m3 ? 0x01010101u : KV == kKvE5m2 ? 0x04040404u : KV == kKvF16 ? 0x04000400u : 0x00800080u;
         return ((w & kExp) + kStep) & kTop;
     }
-    // Add x, dim block_dim(s, g) + y of row v, to the sums of the columns that see the row, if it is not finite.
-    __device__ __forceinline__ void add_not_finite(const WindowParams &p, const WindowReq &req, int v, int s, int y, int c, float x)
+    // Whether some sum is NaN (a type without infinities has NaN only beside NaN).
+    __device__ __forceinline__ bool broken() const
     {
-        if (fabsf(x) < __builtin_huge_valf())
-            return;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int i = min(((nt * 8 + 2 * c + e) & kColMask) / p.group, p.q_len - 1);
-                if (visible(p, req, v, req.L - p.q_len + i))
-                    acc[s][nt][2 * y + e] += x;
-            }
-    }
-    // An infinite V element times a weight's part that is 0 or less than 0 is NaN.  So where sums are NaN though the
-    // weights are not, they become what the elements that are not finite add up to, of the rows [from, to) that they have.
-    __device__ __forceinline__ void repair(const WindowParams &p, int b, int head, int from, int to, int g, int c)
-    {
-        bool broken = false;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        bool any = false;
+        if constexpr (C::kInf) {
 #pragma unroll
             for (int s = 0; s < kSteps; ++s)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    broken = broken || (acc[s][nt][e] != acc[s][nt][e] && l[nt][e & 1] == l[nt][e & 1]);
-        if (!__any_sync(0xffffffffu, broken))
-            return;
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (acc[s][nt][e] != acc[s][nt][e] && l[nt][e & 1] == l[nt][e & 1])
-                        acc[s][nt][e] = 0.f;
-        const WindowReq req = window_req(p, b, nullptr);
-        for (int v = from; v < to; ++v) {
-            int slot = window_pos(req, v), page = b;
-            if (p.block_table) {
-                const int blk = slot / p.page_size;
-                slot -= blk * p.page_size;
-                page = p.block_table[(long long)b * p.max_blocks + blk];
-                page = (unsigned)page < (unsigned)p.num_pages ? page : 0;
-            }
-            const uint8_t *row = p.v + (size_t)((uint32_t)page * p.row_page + (uint32_t)slot * p.row_token + (uint32_t)head * p.row_head) * kRow;
-#pragma unroll
-            for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    const int dim = block_dim(s, g) + y;
-                    float x;
-                    if constexpr (C::kFp8)
-                        x = fp8x2_to_float2<KV>((uint16_t)row[dim]).x;
-                    else
-                        x = x2_to_float2<C::kF16>(reinterpret_cast<const uint16_t *>(row)[dim]).x;
-                    add_not_finite(p, req, v, s, y, c, x);
-                }
+                    for (int e = 0; e < 4; ++e)
+                        any = any || acc[s][nt][e] != acc[s][nt][e];
         }
-    }
-
-    // V's element of row r and dim d of the tile.
-    __device__ __forceinline__ static float element(uint32_t v, uint32_t vs, int r, int d)
-    {
-        const int byte = d * kRow / D;
-        const uint32_t w = lds8(v + r * kRow + (((byte >> 4) ^ window_swizzle<kGran>(r)) << 4) + (byte & 15));
-        if constexpr (C::kFp4) {
-            const float s = fp8x2_to_float2<kKvE4m3>((uint16_t)lds8(vs + r * C::kScaleRow + d / 16)).x;
-            return f16x2_to_float2(e2m1x2_to_f16x2<0>(d & 1 ? w >> 4 : w)).x * s;
-        } else if constexpr (C::kFp8) {
-            return fp8x2_to_float2<KV>((uint16_t)w).x;
-        } else {
-            const uint32_t hi = lds8(v + r * kRow + (((byte >> 4) ^ window_swizzle<kGran>(r)) << 4) + (byte & 15) + 1);
-            return x2_to_float2<C::kF16>(w | hi << 8).x;
-        }
+        return any;
     }
 
     // First of the two dims that the lane holds of output block blk (rows g and g + 8 of the MMA).
@@ -685,6 +628,64 @@ __device__ __forceinline__ long long window_out_row(const WindowParams &p, int b
     const int i = col / p.group;
     return (long long)(b * p.q_len + i) * p.hq + head * p.group + (col - i * p.group);
 }
+// V's element d of row v of a request.
+template <class C>
+__device__ __forceinline__ float window_element(const WindowParams &p, const WindowReq &req, int b, int head, int v, int d)
+{
+    int slot = window_pos(req, v), page = b;
+    if (p.block_table) {
+        const int blk = slot / p.page_size;
+        slot -= blk * p.page_size;
+        page = p.block_table[(long long)b * p.max_blocks + blk];
+        page = (unsigned)page < (unsigned)p.num_pages ? page : 0;
+    }
+    const size_t row = (uint32_t)page * p.row_page + (uint32_t)slot * p.row_token + (uint32_t)head * p.row_head;
+    if constexpr (C::kFp4) {
+        const uint32_t w = p.v[row * C::kRow + d / 2];
+        return f16x2_to_float2(e2m1x2_to_f16x2<0>(d & 1 ? w >> 4 : w)).x *
+               fp8x2_to_float2<kKvE4m3>((uint16_t)p.vs[row * C::kScaleRow + d / 16]).x;
+    } else if constexpr (C::kFp8)
+        return fp8x2_to_float2<C::KV>((uint16_t)p.v[row * C::kRow + d]).x;
+    else
+        return x2_to_float2<C::kF16>(reinterpret_cast<const uint16_t *>(p.v + row * C::kRow)[d]).x;
+}
+// An infinite V element times a weight's part that is 0 or less than 0 is NaN, and in tiles that are seen in part V's
+// elements that are not finite were left out.  Here a warp looks for them in rows [from, to) of a request, whose sums (or
+// output, base null) it has just written, and adds those that a token sees to its columns with a bit in `ok`: what else
+// was summed there does not matter.
+template <class C>
+__device__ __noinline__ void window_repair(const WindowParams &p, int b, int head, int from, int to, uint32_t ok, float *base)
+{
+    constexpr int D = C::D, kMine = D / 32;
+    const int lane = threadIdx.x & 31;
+    const WindowReq req = window_req(p, b, nullptr);
+    __syncwarp();
+#pragma unroll 1
+    for (int i = 0; i < p.q_len; ++i) {
+        const WindowSight sight(p, req, i);
+        float sum[kMine];
+#pragma unroll
+        for (int e = 0; e < kMine; ++e)
+            sum[e] = 0.f;
+#pragma unroll 4
+        for (int v = from; v < to; ++v)
+            if (sight.sees(v))
+#pragma unroll
+                for (int e = 0; e < kMine; ++e) {
+                    const float x = window_element<C>(p, req, b, head, v, lane + 32 * e);
+                    sum[e] += fabsf(x) < __builtin_huge_valf() ? 0.f : x;
+                }
+#pragma unroll 1
+        for (int col = i * p.group; col < (i + 1) * p.group; ++col)
+            if (ok >> col & 1)
+#pragma unroll
+                for (int e = 0; e < kMine; ++e) {
+                    float *at = (base ? base + col * D : p.o + window_out_row(p, b, head, col) * D) + lane + 32 * e;
+                    if (sum[e] != 0.f)
+                        *at = *at != *at ? sum[e] : *at + sum[e];
+                }
+    }
+}
 // LSE from the reference exponent (log2) and the sum of weights.
 __device__ __forceinline__ float window_lse(float m, float l)
 {
@@ -699,6 +700,27 @@ __device__ __forceinline__ int window_schedule(const WindowParams &p, int *prefi
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int heads = p.hkv / p.team;
     int run = 0, live = 0, most = 0;
+    if (p.batch <= 32) {   // every warp for itself
+        const int n = lane < p.batch ? (int)(((unsigned)window_req(p, lane, report && warp == 0 ? p.ws_err : nullptr).rows + TILE - 1) / TILE) : 0;
+        const uint32_t full = __ballot_sync(0xffffffffu, n > 0);
+        int x = n;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int a = __shfl_up_sync(0xffffffffu, x, off);
+            if (lane >= off)
+                x += a;
+        }
+        if (warp == 0) {
+            if (lane < p.batch) {
+                prefix[lane + 1] = x * heads;
+                nonempty[lane + 1] = __popc(full & (2u << lane) - 1);
+            }
+            if (lane == 0)
+                prefix[0] = nonempty[0] = 0;
+        }
+        __syncthreads();
+        return __reduce_max_sync(0xffffffffu, n);
+    }
     for (int b0 = 0; b0 < p.batch; b0 += blockDim.x) {
         const int b = b0 + threadIdx.x;
         int n = 0;
@@ -759,7 +781,7 @@ struct WindowParts {
         const long long pos = s.seg_pos(b, seg - b * s.hkv), end = pos + (s.prefix[b + 1] - s.prefix[b]) / s.hkv;
         w0 = s.cta_at(pos);
         w1 = s.cta_at(end - 1);
-        apart = w0 != w1 && end + s.w < s.cost() && s.cta_at(end + s.w) == w1;
+        apart = w0 != w1 && end + s.w < s.total && s.cta_at(end + s.w) == w1;
         c0 = w0 / teams;
         c1 = (apart ? w1 - 1 : w1) / teams;
         n = c1 - c0 + 1 + (apart ? 1 : 0);
@@ -771,6 +793,13 @@ struct WindowParts {
     }
 };
 
+// The segment of tile t.
+__device__ __forceinline__ int segment_of_tile(const int *prefix, int batch, int heads, int t)
+{
+    const int b = request_of_tile(prefix, batch, t);
+    return b * heads + (t - prefix[b]) / ((prefix[b + 1] - prefix[b]) / heads);
+}
+
 // Shared memory: the warps' rings, then prefix and non-empty [batch + 1], then scratch: the scan's sums,
 // and what the warps hold at the end.
 constexpr int kWindowScratch = kWindowMaxWarps * (3 + 2 * (2 + (int)(sizeof(WindowParts) / sizeof(int))));
@@ -780,23 +809,34 @@ constexpr size_t window_smem(int batch)
     return (size_t)C::kWarps * C::kRing + sizeof(int) * (2 * ((size_t)batch + 1) + kWindowScratch);
 }
 
-constexpr int kWindowTogether = 4;   // partials whose loads a thread has in flight
+constexpr int kWindowTogether = 8;   // partials that a thread reads and adds together
 
 // Sums of weights and of weighted V rows (4 dims) against the reference exponent `top`.
 struct WindowSum {
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
     float top = -__builtin_huge_valf(), l = 0.f;
-    __device__ __forceinline__ void add(float2 ml, float4 x)
+    // Add N sums x with their references and weights ml (reference -inf: nothing).
+    template <int N>
+    __device__ __forceinline__ void add(const float2 (&ml)[N], const float4 (&x)[N])
     {
-        const float higher = fmaxf(top, ml.x), ref = higher == -__builtin_huge_valf() ? 0.f : higher;
-        // at least fp32's least normal number: an infinite sum stays infinite
-        const float f = fmaxf(exp2_approx(top - ref), 1.1754944e-38f), w = fmaxf(exp2_approx(ml.x - ref), 1.1754944e-38f);
+        float higher = top;
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            higher = fmaxf(higher, ml[e].x);
+        // factors of at least fp32's least normal number: an infinite sum stays infinite
+        const float ref = higher == -__builtin_huge_valf() ? 0.f : higher, f = fmaxf(exp2_approx(top - ref), 1.1754944e-38f);
         top = higher;
-        l = fmaf(w, ml.y, l * f);
-        sum.x = fmaf(w, x.x, sum.x * f);
-        sum.y = fmaf(w, x.y, sum.y * f);
-        sum.z = fmaf(w, x.z, sum.z * f);
-        sum.w = fmaf(w, x.w, sum.w * f);
+        l *= f;
+        sum = make_float4(sum.x * f, sum.y * f, sum.z * f, sum.w * f);
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const float w = fmaxf(exp2_approx(ml[e].x - ref), 1.1754944e-38f);
+            l = fmaf(w, ml[e].y, l);
+            sum.x = fmaf(w, x[e].x, sum.x);
+            sum.y = fmaf(w, x[e].y, sum.y);
+            sum.z = fmaf(w, x[e].z, sum.z);
+            sum.w = fmaf(w, x[e].w, sum.w);
+        }
     }
     template <int D>
     __device__ __forceinline__ void store(const WindowParams &p, int b, int head, int col, int d, float shift) const
@@ -821,14 +861,14 @@ __global__ void __launch_bounds__(32 * C::kWarps, 1) window_kernel(const __grid_
     int *nonempty = prefix + p.batch + 1, *tmp = nonempty + p.batch + 1;
     int *s_seg = tmp + 3 * kWindowMaxWarps, *s_size = s_seg + 2 * kWindowMaxWarps;
     WindowParts *s_parts = reinterpret_cast<WindowParts *>(s_size + 2 * kWindowMaxWarps);
-    int *s_merges = tmp;
+    int *s_list = tmp, *s_count = tmp + 2 * kWindowMaxWarps;   // the scan's sums are used up
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
 
     pdl_launch_dependents();
     pdl_wait_prior_grid();
     const int most = window_schedule<kTile>(p, prefix, nonempty, tmp, blockIdx.x == 0);
     const int heads = p.hkv / p.team;
-    for (int b = blockIdx.x; b < p.batch; b += gridDim.x)   // requests that see nothing
+    for (int b = blockIdx.x; b < p.batch && nonempty[p.batch] < p.batch; b += gridDim.x)   // requests that see nothing
         if (prefix[b] == prefix[b + 1])
             for (int i = threadIdx.x; i < p.q_len * p.hq * (D / 4); i += blockDim.x) {
                 const long long row = (long long)b * p.q_len * p.hq + i / (D / 4);
@@ -836,13 +876,20 @@ __global__ void __launch_bounds__(32 * C::kWarps, 1) window_kernel(const __grid_
                 if (p.lse && i % (D / 4) == 0)
                     p.lse[row] = -__builtin_huge_valf();
             }
-    WindowSchedule sch = {{prefix, nonempty, p.batch, heads, kWindowSegCost, 0}};
+    WindowSchedule sch;
+    sch.prefix = prefix;
+    sch.nonempty = nonempty;
+    sch.batch = p.batch;
+    sch.hkv = heads;
+    sch.w = kWindowSegCost;
+    sch.total = sch.cost();
     const int team = warp / p.team, lead = warp - team * p.team;   // the warp's kv head of the team's
     // A few short segments: one for a CTA, whose warps share its tiles, and nothing is left to join.
     const int segments = nonempty[p.batch] * heads;
     const bool by_segment = segments <= (int)gridDim.x && most <= kWindowSegmentTiles * (C::kWarps / p.team);
-    const int teams = by_segment ? C::kWarps / p.team : window_workers(sch.cost(), gridDim.x, C::kWarps / p.team);
+    const int teams = by_segment ? C::kWarps / p.team : window_workers(sch.total, gridDim.x, C::kWarps / p.team);
     sch.P = gridDim.x * teams;
+    sch.busy = sch.total < sch.P ? (int)sch.total : sch.P;
     const int worker = blockIdx.x * teams + team;
     int t0 = 0, t1 = 0;
     if (by_segment) {
@@ -853,24 +900,23 @@ __global__ void __launch_bounds__(32 * C::kWarps, 1) window_kernel(const __grid_
             t0 = begin + min(nb, team * share);
             t1 = begin + min(nb, (team + 1) * share);
         }
-    } else if (team < teams && worker < sch.ctas()) {
+    } else if (team < teams && worker < sch.busy) {
         // odd lanes find the run's end
-        const int t = sch.tile_at(sch.begin(worker + (lane & 1)));
+        const int t = sch.first_tile(worker + (lane & 1));
         t0 = __shfl_sync(0xffffffffu, t, 0);
         t1 = __shfl_sync(0xffffffffu, t, 1);
     }
 
     Warp w;
     w.q_at = smem_addr(smem) + warp * C::kRing + C::kStages * (C::kStage + kWindowAbout) + 8 * lane;
-    int from = 0, to = 0;        // the rows of a segment that the warp has summed
-    int last = -1, begun = -1;   // the segment of the sums that the warp still holds; the one that it found begun and ended
+    int last = -1, begun = -1;   // the segments of the sums in the warp's ring, and of a partial that it ended
     if (t0 < t1) {
         const uint32_t ring = smem_addr(smem) + warp * C::kRing;
         const uint32_t meta = ring + kStages * C::kStage;   // of each tile: request, launch head, first row, kTile* and its rows; the request's rows, head, skip
         const uint64_t policy = l2_policy_evict_first();
 
         WindowCursor ld;
-        auto request = [&](int b) {
+        auto request = [&](int b) {   // the request's tiles and rows
             const WindowReq r = window_req(p, b, nullptr);
             ld.b = b;
             ld.nb = (prefix[b + 1] - prefix[b]) / heads;
@@ -979,34 +1025,33 @@ __global__ void __launch_bounds__(32 * C::kWarps, 1) window_kernel(const __grid_
             }
             cp_async_commit();
         };
-        const bool first = ld.j == 0;
-        const int b0 = ld.b, h0 = ld.h, from0 = ld.j * kTile;
 #pragma unroll
         for (int i = 0; i < kStages - 1; ++i)
             fetch(i);
-        w.start(p, b0, h0 * p.team + lead, g, c);   // while the first tile is on its way
-        last = b0 * heads + h0;
-        from = from0;
-
+        // Who else has parts of the run's first and last segment is worked out while the tiles are on their way.
+        if (lane < 2 && !by_segment)
+            s_parts[lane * C::kWarps + warp] = WindowParts(sch, teams, segment_of_tile(prefix, p.batch, heads, lane ? t1 - 1 : t0));
         const WindowPlaces<C> places(g, c);
-        int stage = 0;
-        bool whole = first;   // the segment's first tile was the warp's
+        int stage = 0, seg = -1;             // the tile's slot; the segment of the sums
+        bool whole = false, dirty = false;   // the segment's first tile was the warp's; V was not finite in a tile seen in part
+        int from = 0;                        // the first of the segment's rows that the warp has
         for (int t = t0; t < t1; ++t) {
+            const uint32_t about = meta + kWindowAbout * stage;
+            __syncwarp();
+            const uint4 tile = lds128(about);
+            if ((int)(tile.x * heads + tile.y) != seg) {   // the query is loaded while the tile is on its way
+                seg = tile.x * heads + tile.y;
+                w.start(p, tile.x, tile.y * p.team + lead, g, c);
+                whole = tile.w & kTileFirst;
+                dirty = false;
+                from = tile.z;
+            }
             cp_async_wait<kStages - 2>();
             __syncwarp();
-            fetch(stage == 0 ? kStages - 1 : stage - 1);
-            const uint32_t about = meta + kWindowAbout * stage;
-            const uint4 tile = lds128(about);
-            const int b = (int)tile.x, h = (int)tile.y, row0 = (int)tile.z, flags = (int)tile.w;
-            const int seg = b * heads + h, head = h * p.team + lead;
-            if (seg != last) {
-                w.start(p, b, head, g, c);
-                last = seg;
-                from = row0;
-                whole = flags & kTileFirst;
-            }
             const uint32_t k = ring + stage * C::kStage, v = k + kTile * kRow, ks = v + kTile * kRow, vs = ks + kTile * C::kScaleRow;
             stage = stage + 1 == kStages ? 0 : stage + 1;
+            fetch(stage);
+            const int row0 = (int)tile.z, flags = (int)tile.w;
             float sc[Warp::KT][NT][4];
             uint32_t pf[Warp::KT][Warp::kParts][NT][2];
             w.scores(places, k, ks, sc);
@@ -1017,123 +1062,111 @@ __global__ void __launch_bounds__(32 * C::kWarps, 1) window_kernel(const __grid_
                     const uint4 what = lds128(about + 16);
                     const WindowReq req = {(int)(what.x + what.z), (int)what.y, (int)(what.y + what.z), (int)what.x};
                     w.mask(p, req, row0, g, c, sc);
-                    w.screen(p, req, row0, v, vs, lane);
+                    dirty |= w.screen(v, vs, lane);
                 }
             }
             w.rescale(sc);
             w.weights(sc, c, pf);
             w.values(places, v, vs, pf);
-            to = row0 + (flags >> kTileN);
-            if ((flags & kTileLast) && (whole || t + 1 < t1)) {
-                // the segment ends inside the run: its output, or a partial of a segment that others began
-                w.finish();
-                if constexpr (C::kInf)
-                    w.repair(p, b, head, from, to, g, c);
-                const long long slot_o = (long long)(2 * worker) * p.team + lead;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int col = nt * 8 + 2 * c + e;
-                        if (col >= p.cols || (PACK && c >= 2))
-                            continue;
-                        float *dst;
-                        float f = 1.f;
-                        if (whole) {
-                            const long long row = window_out_row(p, b, head, col);
-                            dst = p.o + row * D;
-                            f = w.l[nt][e] == 0.f ? 0.f : p.v_scale / w.l[nt][e];
-                            if (g == 0 && p.lse)
-                                p.lse[row] = window_lse(w.reference(nt, e) - Warp::kShift, w.l[nt][e]);
-                        } else {
-                            dst = p.ws_o + (slot_o * p.cols + col) * D;
-                            if (g == 0)
-                                p.ws_ml[slot_o * p.cols + col] = make_float2(w.reference(nt, e), w.l[nt][e]);
-                        }
-#pragma unroll
-                        for (int s = 0; s < Warp::kSteps; s += 2)
-                            *reinterpret_cast<float4 *>(dst + Warp::block_dim(s, g)) =
-                                make_float4(w.acc[s][nt][e] * f, w.acc[s][nt][e + 2] * f, w.acc[s + 1][nt][e] * f, w.acc[s + 1][nt][e + 2] * f);
-                    }
-                if (!whole)
-                    begun = seg;
-                last = -1;
+            const bool ends = flags & kTileLast;
+            if (!ends && t + 1 < t1)
+                continue;
+            // The end of the segment, or of the run.  A segment that the warp has whole: its output.  One that it found
+            // begun and whose end is inside the run: a partial.  Else: sums, left in the warp's own ring.
+            const int b = (int)tile.x, head = (int)tile.y * p.team + lead;
+            float *sums = nullptr, *ml = nullptr;
+            if (!ends || (!whole && t + 1 == t1)) {
+                ml = reinterpret_cast<float *>(smem + warp * C::kRing);
+                sums = ml + kMl;
+                last = seg;
+                __syncwarp();   // the tile has been read
+            } else if (!whole) {
+                const long long slot = (long long)(2 * worker) * p.team + lead;
+                ml = reinterpret_cast<float *>(p.ws_ml + slot * p.cols);
+                sums = p.ws_o + slot * p.cols * D;
+                begun = seg;
             }
+            w.finish();
+            uint32_t ok = 0;   // columns whose sums of weights are numbers
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int col = nt * 8 + 2 * c + e;
+                    const float l = w.l[nt][e], ref = w.reference(nt, e);
+                    ok |= l == l ? 1u << col : 0u;
+                    if (col >= p.cols || (PACK && c >= 2))
+                        continue;
+                    float *dst = sums + col * D;
+                    float f = 1.f;
+                    if (!sums) {
+                        const long long row = window_out_row(p, b, head, col);
+                        dst = p.o + row * D;
+                        f = l == 0.f ? 0.f : p.v_scale / l;
+                        if (g == 0 && p.lse)
+                            p.lse[row] = window_lse(ref - Warp::kShift, l);
+                    } else if (g == 0)
+                        *reinterpret_cast<float2 *>(ml + 2 * col) = make_float2(ref, l);
+#pragma unroll
+                    for (int s = 0; s < Warp::kSteps; s += 2)
+                        *reinterpret_cast<float4 *>(dst + Warp::block_dim(s, g)) =
+                            make_float4(w.acc[s][nt][e] * f, w.acc[s][nt][e + 2] * f, w.acc[s + 1][nt][e] * f, w.acc[s + 1][nt][e + 2] * f);
+                }
+            if (__any_sync(0xffffffffu, dirty || w.broken()))
+                window_repair<C>(p, b, head, from, row0 + (flags >> kTileN), __reduce_or_sync(0xffffffffu, ok), sums);
+            seg = -1;
         }
-        cp_async_wait<0>();
-        __syncwarp();
     }
 
-    // Sums that warps still hold: those of the same segment are added up over the CTA.  A warp leaves (m, l) and its
-    // sums in its own ring.
-    if (last >= 0) {
-        w.finish();
-        if constexpr (C::kInf)
-            w.repair(p, last / heads, last % heads * p.team + lead, from, to, g, c);
-        float *ml = reinterpret_cast<float *>(smem + warp * C::kRing), *sum = ml + kMl;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int col = nt * 8 + 2 * c + e;
-                if (col >= p.cols || (PACK && c >= 2))
-                    continue;
-                if (g == 0) {
-                    ml[2 * col] = w.reference(nt, e);
-                    ml[2 * col + 1] = w.l[nt][e];
-                }
-#pragma unroll
-                for (int s = 0; s < Warp::kSteps; s += 2)
-                    *reinterpret_cast<float4 *>(sum + col * D + Warp::block_dim(s, g)) =
-                        make_float4(w.acc[s][nt][e], w.acc[s][nt][e + 2], w.acc[s + 1][nt][e], w.acc[s + 1][nt][e + 2]);
-            }
-    }
+    // What the CTA has of segments that others share: the partials of segments that its warps found begun (entries 0 ..
+    // kWarps - 1), and its groups of warps that left sums of one segment (kWarps .. 2 kWarps - 1, at the group's first).
     if (lane == 0) {
         s_seg[warp] = begun;
         s_seg[C::kWarps + warp] = last;
+        if (by_segment)
+            s_parts[C::kWarps + warp].n = 1;
     }
     __syncthreads();
-    // What the CTA has of segments that others share: the partials of segments that its warps found begun (entries 0 ..
-    // kWarps - 1), and its groups of warps that hold sums of one segment (kWarps .. 2 kWarps - 1, at the group's first).
-    const int lead_of = threadIdx.x % C::kWarps % p.team;
-    if (threadIdx.x < 2 * C::kWarps) {
-        const int a = threadIdx.x, seg = s_seg[a];
-        s_size[a] = 0;
-        if (seg >= 0 && (a < C::kWarps || a < C::kWarps + p.team || s_seg[a - p.team] != seg)) {
-            int n = 1;
-            if (a >= C::kWarps)
-                while (a + n * p.team < 2 * C::kWarps && s_seg[a + n * p.team] == seg)
-                    ++n;
+    if (warp == 0) {
+        const int a = lane, seg = a < 2 * C::kWarps ? s_seg[a] : -1;
+        int n = seg >= 0 && (a < C::kWarps || a < C::kWarps + p.team || s_seg[a - p.team] != seg) ? 1 : 0;
+        const bool group = n && a >= C::kWarps;
+        if (group)
+            while (a + n * p.team < 2 * C::kWarps && s_seg[a + n * p.team] == seg)
+                ++n;
+        if (a < 2 * C::kWarps)
             s_size[a] = n;
-            if (by_segment)
-                s_parts[a].n = 1;
-            else
-                s_parts[a] = WindowParts(sch, teams, seg);
-        }
+        const uint32_t all = __ballot_sync(0xffffffffu, group);
+        if (group)
+            s_list[__popc(all & ((1u << lane) - 1))] = a;
+        if (lane == 0)
+            *s_count = __popc(all);
     }
     __syncthreads();
     const int items = p.cols * (D / 4);   // 4 dims of a column
-    for (int a = C::kWarps + warp; a < 2 * C::kWarps; a += C::kWarps) {   // a warp adds up its group
-        const int n = s_size[a];
-        if (n == 0)
-            continue;
-        const int seg = s_seg[a], b = seg / heads, head = (seg - b * heads) * p.team + lead;
-        const bool all = s_parts[a].n == 1;
-        const long long slot = (long long)(2 * worker + 1) * p.team + lead;
-        for (int i = lane; i < items; i += 32) {
-            const int col = i / (D / 4), d = 4 * (i - col * (D / 4));
-            WindowSum x;
-            for (int k = 0; k < n; ++k) {
-                const float *ml = reinterpret_cast<const float *>(smem + (warp + k * p.team) * C::kRing);
-                x.add(make_float2(ml[2 * col], ml[2 * col + 1]), *reinterpret_cast<const float4 *>(ml + kMl + col * D + d));
+    for (int i = threadIdx.x, end = *s_count * items; i < end; i += blockDim.x) {   // the groups' sums
+        const int a = s_list[i / items], n = s_size[a], first = a - C::kWarps, of = first % p.team, seg = s_seg[a], b = seg / heads;
+        const int col = i % items / (D / 4), d = 4 * (i % (D / 4));
+        WindowSum x;
+#pragma unroll 1
+        for (int k0 = 0; k0 < n; k0 += 4) {
+            float2 ml[4];
+            float4 y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float *at = reinterpret_cast<const float *>(smem + (first + min(k0 + e, n - 1) * p.team) * C::kRing);
+                ml[e] = k0 + e < n ? *reinterpret_cast<const float2 *>(at + 2 * col) : make_float2(-__builtin_huge_valf(), 0.f);
+                y[e] = k0 + e < n ? *reinterpret_cast<const float4 *>(at + kMl + col * D + d) : make_float4(0.f, 0.f, 0.f, 0.f);
             }
-            if (all)
-                x.store<D>(p, b, head, col, d, Warp::kShift);
-            else {
-                *reinterpret_cast<float4 *>(p.ws_o + (slot * p.cols + col) * D + d) = x.sum;
-                if (d == 0)
-                    p.ws_ml[slot * p.cols + col] = make_float2(x.top, x.l);
-            }
+            x.add(ml, y);
+        }
+        if (s_parts[a].n == 1)
+            x.store<D>(p, b, (seg - b * heads) * p.team + of, col, d, Warp::kShift);
+        else {
+            const long long slot = (long long)(2 * (blockIdx.x * teams + first / p.team) + 1) * p.team + of;
+            *reinterpret_cast<float4 *>(p.ws_o + (slot * p.cols + col) * D + d) = x.sum;
+            if (d == 0)
+                p.ws_ml[slot * p.cols + col] = make_float2(x.top, x.l);
         }
     }
 
@@ -1142,7 +1175,7 @@ __global__ void __launch_bounds__(32 * C::kWarps, 1) window_kernel(const __grid_
     if (warp == 0) {
         bool merge = false;
         if (lane < 2 * C::kWarps && s_size[lane] > 0 && s_parts[lane].n > 1) {
-            unsigned int *count = p.ws_counts + s_parts[lane].w0 * p.team + lead_of;
+            unsigned int *count = p.ws_counts + s_parts[lane].w0 * p.team + lane % C::kWarps % p.team;
             __threadfence();   // the CTA's partials before the count, and the others' after it
             merge = atomicAdd(count, 1u) == (unsigned)s_parts[lane].n - 1;
             __threadfence();
@@ -1151,12 +1184,12 @@ __global__ void __launch_bounds__(32 * C::kWarps, 1) window_kernel(const __grid_
         }
         const uint32_t all = __ballot_sync(0xffffffffu, merge);
         if (merge)
-            s_size[__popc(all & ((1u << lane) - 1))] = lane;   // the list of them; the sizes are used up
+            s_list[__popc(all & ((1u << lane) - 1))] = lane;
         if (lane == 0)
-            *s_merges = __popc(all);
+            *s_count = __popc(all);
     }
     __syncthreads();
-    const int merges = *s_merges;
+    const int merges = *s_count;
     if (merges == 0)
         return;
     // Threads share the (segment, 4 dims) pairs, or several share the partials of one.
@@ -1168,27 +1201,28 @@ __global__ void __launch_bounds__(32 * C::kWarps, 1) window_kernel(const __grid_
         int a = 0, b = 0, head = 0, col = 0, d = 0;
         WindowSum x;
         if (active) {
-            a = s_size[i / items];
+            a = s_list[i / items];
             const WindowParts parts = s_parts[a];
             const int seg = s_seg[a], of = a % C::kWarps % p.team;
             b = seg / heads;
             head = (seg - b * heads) * p.team + of;
             col = i % items / (D / 4);
             d = 4 * (i % (D / 4));
+#pragma unroll 1
             for (int k0 = mine; k0 < parts.n; k0 += split * kWindowTogether) {
                 float2 ml[kWindowTogether];
                 float4 y[kWindowTogether];
 #pragma unroll
                 for (int e = 0; e < kWindowTogether; ++e) {
-                    const int k = min(k0 + e * split, parts.n - 1);
-                    const long long slot = (long long)parts.slot(teams, k) * p.team + of;
-                    ml[e] = __ldcg(p.ws_ml + slot * p.cols + col);
-                    y[e] = __ldcg(reinterpret_cast<const float4 *>(p.ws_o + (slot * p.cols + col) * D + d));
+                    ml[e] = make_float2(-__builtin_huge_valf(), 0.f);
+                    y[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (k0 + e * split < parts.n) {
+                        const long long slot = (long long)parts.slot(teams, k0 + e * split) * p.team + of;
+                        ml[e] = __ldcg(p.ws_ml + slot * p.cols + col);
+                        y[e] = __ldcg(reinterpret_cast<const float4 *>(p.ws_o + (slot * p.cols + col) * D + d));
+                    }
                 }
-#pragma unroll
-                for (int e = 0; e < kWindowTogether; ++e)
-                    if (k0 + e * split < parts.n)
-                        x.add(ml[e], y[e]);
+                x.add(ml, y);
             }
         }
         if (split > 1) {   // then total < blockDim: one pass
@@ -1199,7 +1233,9 @@ __global__ void __launch_bounds__(32 * C::kWarps, 1) window_kernel(const __grid_
             if (active && mine == 0)
                 for (int k = 1; k < split; ++k) {
                     const WindowSum &y = shared[k * per + i];
-                    x.add(make_float2(y.top, y.l), y.sum);
+                    const float2 ml[1] = {make_float2(y.top, y.l)};
+                    const float4 of[1] = {y.sum};
+                    x.add(ml, of);
                 }
         }
         if (active && mine == 0)
