@@ -28,9 +28,6 @@ constexpr int kWindowMaxColumns = 16;
 // flushes its outputs there.
 constexpr int kWindowSegCost = 1;
 
-// Tiles a warp that a segment may have to be one CTA's (fd_window_kernel.cuh).
-constexpr int kWindowSegmentTiles = 2;
-
 constexpr int kWindowAbout = 32;   // bytes that say what a tile is
 
 // Shape of the split kernel for head dim D, a cache of type KV and MMAs of 8 NT
@@ -155,6 +152,21 @@ __device__ __forceinline__ int window_workers(long long cost, int grid, int most
 {
     const long long want = window_quotient(cost + grid - 1, grid);
     return want < 1 ? 1 : want < most ? (int)want : most;
+}
+
+// Short segments are not split over CTAs: joining a segment's parts (fence, count, partials through L2) takes as long as
+// this many tiles of a warp.  Measured on GB300, one request of 32 heads in 4 bits: 128 positions 10.1 us split and 6.4
+// whole, 512 10.5 and 7.3, 1024 10.6 and 9.6, 1536 10.8 and 11.7; 58 requests of 65 visible positions, 16 columns of 256
+// dims 41 and 29.
+__device__ __forceinline__ int window_join_tiles(int cols, int d) { return 2 + cols * d / 1024; }
+// CTAs that a call's segments are split over: n of them for a segment take the time of tiles / n and of n partials, which
+// one CTA reads; a warp's tile takes about as long as 60000 values of partials.  Measured on GB300 with 25000, 60000,
+// 150000, no limit (us): 65536 positions of one kv head in 4 bits, 16 columns 31.3, 30.4, 32.9, 39.0; 16384, 8 columns
+// 15.3, 14.9, 16.5, 21.4; two requests of 8 kv heads, 16 columns, 685 visible positions in E5M2 25.9, 19.0, 19.0, 19.0.
+__device__ __forceinline__ int window_ctas(int grid, int segments, int tiles, int cols, int d)
+{
+    const float n = sqrtf((float)segments * tiles * (60000.f / (cols * d)));
+    return n >= grid ? grid : max(1, (int)n);
 }
 
 // A scale of 0 becomes this one, so that a hidden score (-inf) keeps its

@@ -809,7 +809,7 @@ constexpr size_t window_smem(int batch)
     return (size_t)C::kWarps * C::kRing + sizeof(int) * (2 * ((size_t)batch + 1) + kWindowScratch);
 }
 
-constexpr int kWindowTogether = 8;   // partials that a thread reads and adds together
+constexpr int kWindowTogether = 16;   // partials that a thread reads and adds together
 
 // Sums of weights and of weighted V rows (4 dims) against the reference exponent `top`.
 struct WindowSum {
@@ -884,21 +884,24 @@ __global__ void __launch_bounds__(32 * C::kWarps, 1) window_kernel(const __grid_
     sch.w = kWindowSegCost;
     sch.total = sch.cost();
     const int team = warp / p.team, lead = warp - team * p.team;   // the warp's kv head of the team's
-    // A few short segments: one for a CTA, whose warps share its tiles, and nothing is left to join.
-    const int segments = nonempty[p.batch] * heads;
-    const bool by_segment = segments <= (int)gridDim.x && most <= kWindowSegmentTiles * (C::kWarps / p.team);
-    const int teams = by_segment ? C::kWarps / p.team : window_workers(sch.total, gridDim.x, C::kWarps / p.team);
-    sch.P = gridDim.x * teams;
+    // Short segments: a CTA has some whole, each shared by some of its warps, and nothing is left to join.
+    const int segments = nonempty[p.batch] * heads, all_teams = C::kWarps / p.team;
+    const int together = (segments + gridDim.x - 1) / gridDim.x, each = together > 0 && together <= all_teams ? all_teams / together : 0;
+    const bool by_segment = each > 0 && (most + each - 1) / each <= prefix[p.batch] / (int)(gridDim.x * all_teams) + window_join_tiles(p.cols, D);
+    const int grid = window_ctas(gridDim.x, segments, prefix[p.batch] / all_teams, p.cols, D);
+    const int teams = by_segment ? all_teams : window_workers(sch.total, grid, all_teams);
+    sch.P = grid * teams;
     sch.busy = sch.total < sch.P ? (int)sch.total : sch.P;
     const int worker = blockIdx.x * teams + team;
     int t0 = 0, t1 = 0;
     if (by_segment) {
-        if ((int)blockIdx.x < segments) {
-            const int b = request_of_tile(nonempty, p.batch, blockIdx.x / heads);
-            const int nb = (prefix[b + 1] - prefix[b]) / heads, share = (nb + teams - 1) / teams;
-            const int begin = prefix[b] + (int)(blockIdx.x % heads) * nb;
-            t0 = begin + min(nb, team * share);
-            t1 = begin + min(nb, (team + 1) * share);
+        const int mine = blockIdx.x * together + team / each;
+        if (team < each * together && mine < segments) {
+            const int b = request_of_tile(nonempty, p.batch, mine / heads);
+            const int nb = (prefix[b + 1] - prefix[b]) / heads, share = (nb + each - 1) / each, of = team % each;
+            const int begin = prefix[b] + mine % heads * nb;
+            t0 = begin + min(nb, of * share);
+            t1 = begin + min(nb, (of + 1) * share);
         }
     } else if (team < teams && worker < sch.busy) {
         // odd lanes find the run's end
