@@ -25,7 +25,9 @@ constexpr int kWindowMaxWarps = 16;  // warps of a split CTA
 constexpr int kWindowMaxColumns = 16;
 
 // Cost of a segment start, in tiles (fd_sched.h): a warp loads the query and
-// flushes its outputs there.
+// flushes its outputs there.  Measured on GB300 with 0, 1, 2, 4 (us): 64
+// requests of up to 16384 positions in 4 bits 129.7, 126.5, 127.0, 128.5, 8 of
+// 16 columns 117.8, 116.7, 116.6, 115.7; others alike.
 constexpr int kWindowSegCost = 1;
 
 constexpr int kWindowAbout = 32;   // bytes that say what a tile is

@@ -702,7 +702,9 @@ size_t fd_window_workspace_size(int batch, int num_q_heads, int num_kv_heads, in
  * Positions that no new token of a request sees are not read: they may hold
  * anything.  What a position holds does not reach the tokens that do not see it,
  * not-a-numbers included.  A visible V element that is infinite makes its dim of
- * the rows that see it infinite (NaN beside one of the other sign, or a NaN).
+ * the rows that see it infinite (NaN beside one of the other sign, or a NaN);
+ * calls that meet many of them, or not-a-numbers, take some 10 times as long (64
+ * requests of GQA-4, window 4096, bf16: 162 -> 2000 us).
  * Head groups, q_len, head_dim and batch as for fd_decode: G * q_len <= 16, but
  * any of them with any cache.  Rows of the cache (positions x kv heads) are
  * limited to 2^32 - 2, and num_kv_heads * batch * (visible positions / 16 + 2)
