@@ -155,6 +155,8 @@ def make_window_workspace(batch, num_q_heads, num_kv_heads, head_dim=128, device
 def _attend(name, call, q, gpu, cache, pages, page, hkv, table, seq_lens, window, sinks, seq_lens_host, scale, out, lse,
             workspace, num_ctas, split_events, check, kv, k_scale, v_scale):
     """Any cache: checks, outputs, and the call `name`; `cache`: its arguments in that call."""
+    if window >> 31 > 0 or sinks >> 31 > 0:
+        raise ValueError(f"window and sinks must be below 2^31, got {window} and {sinks}")
     shape, dt = q.shape, q.dtype
     if len(shape) == 4:
         B, T, hq, d = shape

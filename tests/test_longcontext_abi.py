@@ -126,6 +126,19 @@ def test_a_stream_of_another_gpu_is_refused(fd, monkeypatch, name, args):
         getattr(fd, name)(*args, stream=stream)
 
 
+@pytest.mark.parametrize("window, sinks", [(2 ** 31, 0), (2 ** 32 + 5, 4), (64, 2 ** 31), (64, 2 ** 32 + 1)])
+def test_windows_that_an_int_does_not_hold_are_refused(fd, window, sinks):
+    """ctypes would pass their low 32 bits: another window."""
+    from decode_attention_decoding_gb300 import longcontext
+
+    def call(*a):
+        raise AssertionError("called")
+    q = torch.zeros(1, 8, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="2\\^31"):
+        longcontext._attend("f", call, q, 0, (0, 0), 1, 16, 8, None, None, window, sinks, None, None, None, None, None, 0, None,
+                            True, 0, 1.0, 1.0)
+
+
 def test_cpu_tensors_are_refused(fd):
     c = u.make_case(1, 2, 1, 4, 2, 64, [5, 9], kv="e2m1")
     cache = fd.Cache4(*c["pool"])
