@@ -69,8 +69,9 @@ def attention(q, k, v, lens, window, sinks, scale, v_scale=1.0):
     The bounds, as for spec_util.tree_attention: a score is an fp32 dot product of D exact products,
     off by at most es = D 2^-23 scale sum|q k|.  A weight is then off relatively by 2 es, by the
     rounding of its argument (|s - m| 2^-23 and 2^-22 of the function), and by its parts: fp16 2^-10
-    2^-11, bf16 2^-7 2^-7 2^-8; below 2^-20 together.  Parts of at least 2^-38 of the largest weight
-    add 2^-37 of every V.  Sums over n positions in fp32 steps that may truncate: n 2^-23."""
+    2^-11, bf16 2^-7 2^-7 2^-8; below 2^-20 together.  A weight in fp16 parts, 2^13 to 2^14 times itself
+    for the largest, ends at half of fp16's least step, 2^-25: below 2^-38 of the largest it may be lost
+    whole, of every V (allowed: 2^-37).  Sums over n positions in fp32 steps that may truncate: n 2^-23."""
     B, T, hq, D = q.shape
     G = hq // k[0].shape[1]
     o, lse = np.zeros((B, T, hq, D)), np.full((B, T, hq), -np.inf)

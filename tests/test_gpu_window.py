@@ -108,6 +108,22 @@ def test_many_requests(fd, B, kv):
     both(fd, u.make_case(B, B, 1, 2, 1, 64, lens, kv=kv, page=16), 0.125)
 
 
+@pytest.mark.parametrize("hq,hkv,T", [(1, 1, 1), (16, 1, 1), (2, 2, 8), (5, 1, 2)])
+@pytest.mark.parametrize("D,kv", [(64, "f16"), (128, "e2m1"), (256, "e2m1"), (128, "bf16"), (256, "e5m2")])
+def test_many_partials(fd, hq, hkv, T, D, kv):
+    """Few segments that many CTAs share: more partials than are added at once, by one thread or by several."""
+    both(fd, u.make_case(D + T, 2, T, hq, hkv, D, [9000, 2500], kv=kv, window=8000, sinks=3), D ** -0.5)
+
+
+@pytest.mark.parametrize("B,hq,hkv,T", [(40, 8, 8, 1), (75, 8, 4, 1), (150, 6, 6, 2), (40, 32, 16, 2), (152, 4, 1, 4)])
+@pytest.mark.parametrize("D,kv,page", [(64, "bf16", 16), (128, "e4m3", 0), (128, "e2m1", 16), (256, "e2m1", 0), (64, "e5m2", 0)])
+def test_short_segments(fd, B, hq, hkv, T, D, kv, page):
+    """Segments of few tiles, from one to many a CTA, empty requests among them."""
+    rng = np.random.default_rng(B + D)
+    lens = (rng.integers(0, 4, B).clip(0, 1) * rng.integers(1, 150, B)).tolist()
+    both(fd, u.make_case(B, B, T, hq, hkv, D, lens, kv=kv, page=page, window=100, sinks=2), D ** -0.5)
+
+
 def test_largest_batch(fd):
     rng = np.random.default_rng(4)
     lens = rng.integers(0, 4, 4096).tolist()
@@ -163,6 +179,23 @@ def test_visible_infinities(fd, kv, hq, T):
         assert bool((o[..., 5] == math.inf).all()) and bool((o[..., 9] == -math.inf).all())
         assert bool(o[..., 11].isnan().all()) and bool(o[..., 20].isnan().all())
         assert bool(o[..., [0, 1, 4, 6, 8, 10, 12, 21, 63]].isfinite().all())
+
+
+@pytest.mark.parametrize("kv", ["bf16", "f16", "e5m2"])
+@pytest.mark.parametrize("hq,T", [(1, 1), (8, 2)])
+@pytest.mark.parametrize("L,ctas", [(150, 0), (7000, 0), (7000, 3)])
+def test_infinities_reach_the_tokens_that_see_them(fd, kv, hq, T, L, ctas):
+    """Infinities and NaN anywhere in V of several segments, in ones that a warp has whole, that warps share and that CTAs
+    share: every element by the definition, where a weight that 64 bits hold above 0 times an infinity is one."""
+    rng = np.random.default_rng(L + T)
+    c = u.make_case(31, 3, T, hq, 1, 64, [L, 0, L // 2], kv=kv, window=L // 2, sinks=2)
+    for b, n in ((0, L), (2, L // 2)):
+        for d in range(0, 64, 5):
+            at = int(rng.integers(n - 40 if d % 2 else 0, n))
+            x = (math.inf, -math.inf, math.nan)[d % 3]
+            c["v64"][b][at, 0, d] = x
+            c["pool"][1][b, at, 0, d] = torch.tensor(x).to(c["pool"][1].dtype)
+    both(fd, c, 0.125, num_ctas=ctas)
 
 
 @pytest.mark.parametrize("kv", ["bf16", "f16", "e5m2"])
