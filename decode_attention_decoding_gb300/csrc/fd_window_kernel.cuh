@@ -412,8 +412,7 @@ struct WindowWarp {
                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
                 const float was = limit[nt][e] - kSlack, now = fmaxf(was, x);
                 const float ref = now == -__builtin_huge_valf() ? 0.f : now;
-                // at least fp32's least normal number: an infinite sum stays infinite
-                const float alpha = fmaxf(exp2_approx(was - ref), 1.1754944e-38f);
+                const float alpha = exp2_approx(was - ref);   // 0 times an infinite sum: NaN, and window_repair looks for what made it
                 limit[nt][e] = now + kSlack;
                 offset[nt][e] = kShift - ref;
                 l[nt][e] *= alpha;
@@ -832,6 +831,22 @@ constexpr size_t window_smem(int batch)
 // positions, 12 columns of 64 dims in fp16 28.7, 28.8, 29.9, 28.9.
 constexpr int kWindowTogether = 16;
 
+template <class At>
+__device__ __noinline__ float4 window_infinities(float4 sum, int n, At at)
+{
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int k = 0; k < n; ++k) {
+        const float4 x = at(k);
+        s.x += fabsf(x.x) < __builtin_huge_valf() ? 0.f : x.x;
+        s.y += fabsf(x.y) < __builtin_huge_valf() ? 0.f : x.y;
+        s.z += fabsf(x.z) < __builtin_huge_valf() ? 0.f : x.z;
+        s.w += fabsf(x.w) < __builtin_huge_valf() ? 0.f : x.w;
+    }
+    return make_float4(sum.x == sum.x || s.x == 0.f ? sum.x : s.x, sum.y == sum.y || s.y == 0.f ? sum.y : s.y,
+                       sum.z == sum.z || s.z == 0.f ? sum.z : s.z, sum.w == sum.w || s.w == 0.f ? sum.w : s.w);
+}
+
 // Sums of weights and of weighted V rows (4 dims) against the reference exponent `top`.
 struct WindowSum {
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -844,19 +859,31 @@ struct WindowSum {
 #pragma unroll
         for (int e = 0; e < N; ++e)
             higher = fmaxf(higher, ml[e].x);
-        // factors of at least fp32's least normal number: an infinite sum stays infinite
-        const float ref = higher == -__builtin_huge_valf() ? 0.f : higher, f = fmaxf(exp2_approx(top - ref), 1.1754944e-38f);
+        const float ref = higher == -__builtin_huge_valf() ? 0.f : higher, f = exp2_approx(top - ref);
         top = higher;
         l *= f;
         sum = make_float4(sum.x * f, sum.y * f, sum.z * f, sum.w * f);
 #pragma unroll
         for (int e = 0; e < N; ++e) {
-            const float w = fmaxf(exp2_approx(ml[e].x - ref), 1.1754944e-38f);
+            const float w = exp2_approx(ml[e].x - ref);
             l = fmaf(w, ml[e].y, l);
             sum.x = fmaf(w, x[e].x, sum.x);
             sum.y = fmaf(w, x[e].y, sum.y);
             sum.z = fmaf(w, x[e].z, sum.z);
             sum.w = fmaf(w, x[e].w, sum.w);
+        }
+    }
+    // After sums at(0) .. at(n - 1) were added: an infinite one whose factor fp32 does not hold has made the sum NaN; the
+    // sum is what the infinite ones (and NaN) come to.  (Factors of fp32's least normal number in place of 0 would keep
+    // infinities too, but also 2^-14 of finite bf16 sums of 2^112; looking for them in each addition took 0.5 us of a short
+    // call's 10.1 and 3.4 of the 26.3 of 5 requests of 16 columns, one kv head.)
+    template <bool INF, class At>
+    __device__ __forceinline__ void infinities(int n, At at)
+    {
+        if constexpr (INF) {
+            const float any = (sum.x + sum.y) + (sum.z + sum.w);   // NaN if one of them is, or needlessly
+            if (any != any)
+                sum = window_infinities(sum, n, at);
         }
     }
     template <int D>
@@ -1184,6 +1211,9 @@ __global__ void __launch_bounds__(32 * C::kWarps, 1) window_kernel(const __grid_
             }
             x.add(ml, y);
         }
+        const float *sums = reinterpret_cast<const float *>(smem + first * C::kRing) + kMl + col * D + d;
+        const int step = p.team * C::kRing / (int)sizeof(float);
+        x.infinities<C::kInf>(n, [=](int k) { return *reinterpret_cast<const float4 *>(sums + k * step); });
         if (s_parts[a].n == 1)
             x.store<D>(p, b, (seg - b * heads) * p.team + of, col, d, Warp::kShift);
         else {
@@ -1270,8 +1300,13 @@ __global__ void __launch_bounds__(32 * C::kWarps, 1) window_kernel(const __grid_
                     x.add(ml, of);
                 }
         }
-        if (active && mine == 0)
+        if (active && mine == 0) {
+            const WindowParts *parts = s_parts + a;
+            const long long step = (long long)p.team * p.cols * D;
+            const float *sums = p.ws_o + ((long long)(a % C::kWarps % p.team) * p.cols + col) * D + d;
+            x.infinities<C::kInf>(parts->n, [=](int k) { return __ldcg(reinterpret_cast<const float4 *>(sums + parts->slot(teams, k) * step)); });
             x.store<D>(p, b, head, col, d, Warp::kShift);
+        }
     }
 }
 
