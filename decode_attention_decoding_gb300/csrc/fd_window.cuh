@@ -41,9 +41,9 @@ struct WindowCfg {
     static constexpr bool kF16 = KV != kKvBf16;              // type of the MMAs
     static constexpr bool kInf = KV == kKvBf16 || KV == kKvF16 || KV == kKvE5m2;   // types with infinities
     static constexpr int kParts = kF16 ? 2 : 3;              // 16-bit parts of a softmax weight
-    // The reference of a column's weights is a score of the column; scores may pass it by kSlack (in log2) before it is
-    // moved, and it has the weight 2^kShift: fp16 remainders of small weights keep their bits, and 2^15 is not passed.
-    static constexpr float kShift = kF16 ? 14.f : 0.f, kSlack = 1.f;
+    // The reference of a column's weights is its largest score so far, of weight 2^kShift: fp16 remainders of small weights
+    // keep their bits.
+    static constexpr float kShift = kF16 ? 14.f : 0.f;
     static constexpr int kRow = kFp4 ? D / 2 : kFp8 ? D : 2 * D;   // bytes of a row
     static constexpr int kGran = kRow / 16;                  // 16-byte pieces of a row
     static constexpr int kScaleRow = kFp4 ? D / 16 : 0;      // bytes of a row's block scales

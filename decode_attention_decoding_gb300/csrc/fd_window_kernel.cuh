@@ -202,7 +202,7 @@ struct WindowWarp {
     static constexpr int KT = kTile / 16;          // k steps of a tile
     static constexpr int kSteps = D / 16;          // k steps of a row, and 16-dim blocks of the output
     static constexpr int kParts = PACK ? 1 : C::kParts;   // MMAs a block (PACK: both parts in one)
-    static constexpr float kShift = C::kShift, kSlack = C::kSlack;
+    static constexpr float kShift = C::kShift;
     static constexpr int kColMask = PACK ? 3 : 8 * NT - 1;
 
     // The query as the B operand of S^T, two words of each k step: in registers, or in shared memory (every lane its own).
@@ -211,8 +211,12 @@ struct WindowWarp {
     uint32_t q_at;
     float mult[NT][2];         // score of column 2c, 2c + 1 of an MMA's eight -> log2 units
     float acc[kSteps][NT][4];
-    // of columns 2c, 2c + 1: what a score (log2 units) may not pass, kShift - the reference, and the sum of weights
-    float limit[NT][2], offset[NT][2], l[NT][2];
+    // Of columns 2c, 2c + 1: the largest score so far (the reference) times -1, fp32's largest number if there is none, and
+    // the sum of weights.  A weight is worked out from the difference of two scores: score * mult less the reference's,
+    // in one step, leaves the rounding of the reference, and that passes fp16's range for references from 2^25 on and
+    // fp32's from 2^31 on (the difference takes an addition a weight: 131072 positions of 32 heads in 4 bits 120.3 -> 122.3
+    // us, 64 ragged requests 126.2 -> 128.1, 16-bit and FP8 caches alike).
+    float minus[NT][2], l[NT][2];
 
     // Load the query of segment (b, head) as the B operand of S^T.
     __device__ __forceinline__ void start(const WindowParams &p, int b, int head, int g, int c)
@@ -269,8 +273,7 @@ struct WindowWarp {
             }
             mult[nt][0] = __shfl_sync(0xffffffffu, f, 8 * c);
             mult[nt][1] = __shfl_sync(0xffffffffu, f, 8 * c + 4);
-            limit[nt][0] = limit[nt][1] = -__builtin_huge_valf();
-            offset[nt][0] = offset[nt][1] = kShift;
+            minus[nt][0] = minus[nt][1] = 3.4028235e38f;
             l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
             for (int s = 0; s < kSteps; ++s)
@@ -384,7 +387,7 @@ struct WindowWarp {
             }
     }
 
-    // Move the references up to the tile's scores if one passes its limit, which is rare after the first tiles.
+    // Move the references up to the tile's scores if one passes its own, which is rare after the first tiles.
     __device__ __forceinline__ void rescale(const float (&sc)[KT][NT][4])
     {
         float top[NT][2];
@@ -397,8 +400,8 @@ struct WindowWarp {
 #pragma unroll
                 for (int kt = 1; kt < KT; ++kt)
                     x = fmaxf(x, fmaxf(sc[kt][nt][e], sc[kt][nt][e + 2]));
-                top[nt][e] = x * mult[nt][e];
-                over = over || top[nt][e] > limit[nt][e];
+                top[nt][e] = x;
+                over = over || x > -minus[nt][e];
             }
         if (!__any_sync(0xffffffffu, over))
             return;
@@ -410,11 +413,9 @@ struct WindowWarp {
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1)
                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
-                const float was = limit[nt][e] - kSlack, now = fmaxf(was, x);
-                const float ref = now == -__builtin_huge_valf() ? 0.f : now;
-                const float alpha = exp2_approx(was - ref);   // 0 times an infinite sum: NaN, and window_repair looks for what made it
-                limit[nt][e] = now + kSlack;
-                offset[nt][e] = kShift - ref;
+                // 0 times an infinite sum: NaN, and window_repair looks for what made it
+                const float now = fminf(minus[nt][e], -x), alpha = exp2_approx((now - minus[nt][e]) * mult[nt][e]);
+                minus[nt][e] = now;
                 l[nt][e] *= alpha;
 #pragma unroll
                 for (int s = 0; s < kSteps; ++s) {
@@ -423,8 +424,8 @@ struct WindowWarp {
                 }
             }
     }
-    // The reference of a column, -inf if nothing was seen.
-    __device__ __forceinline__ float reference(int nt, int e) const { return limit[nt][e] - kSlack; }
+    // The reference of a column in log2 units.
+    __device__ __forceinline__ float reference(int nt, int e) const { return -minus[nt][e] * mult[nt][e]; }
 
     // The scores' softmax weights in parts, as the B operand of O^T: pf[kt][part][nt][2].
     __device__ __forceinline__ void weights(const float (&sc)[KT][NT][4], int c, uint32_t (&pf)[KT][kParts][NT][2])
@@ -435,8 +436,8 @@ struct WindowWarp {
             for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
                 for (int a = 0; a < 2; ++a) {
-                    float x = exp2_approx(fmaf(sc[kt][nt][2 * a], mult[nt][0], offset[nt][0]));
-                    float y = exp2_approx(fmaf(sc[kt][nt][2 * a + 1], mult[nt][1], offset[nt][1]));
+                    float x = exp2_approx(fmaf(sc[kt][nt][2 * a] + minus[nt][0], mult[nt][0], kShift));
+                    float y = exp2_approx(fmaf(sc[kt][nt][2 * a + 1] + minus[nt][1], mult[nt][1], kShift));
                     l[nt][0] += x;
                     l[nt][1] += y;
                     if constexpr (PACK) {

@@ -95,3 +95,29 @@ def test_large_finite_values_vanish_and_infinities_stay(fd, kv, hq, T, L, ctas, 
     fin = np.isfinite(ref)
     off = np.abs(o[fin] - ref[fin])
     assert (off <= mean_bound(c, top)[fin] + 2.0 ** -149).all(), off.max()
+
+
+@pytest.mark.parametrize("kv", KINDS)
+@pytest.mark.parametrize("hq,T", COLUMNS)
+@pytest.mark.parametrize("L,ctas", [(40, 0), (1500, 1), (6000, 0)])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_large_scores(fd, kv, hq, T, L, ctas, sign):
+    """Scores of 0.7 2^e (or its negative), 0 and a little above that, each the same in many rows: the rows of the highest
+    have equal weights, the others none from e = 8 on.  Of a product that fp32 rounds by more than 1, each weight has to
+    mean the same."""
+    rng = np.random.default_rng(L)
+    level = rng.integers(0, 4, L)
+    level[0] = level[L - T] = 3
+    c = case(kv, hq, T, L, 3.0, 72)
+    fill(c, 0, sign * np.array([-1.5, 0.0, 0.5, 1.5])[level][:, None, None] * np.ones((1, 2, 128)))
+    fill(c, 1, rng.standard_normal((L, 2, 128)))
+    top = c["k64"][0][:, 0, 0] * sign == (c["k64"][0][:, 0, 0] * sign).max()
+    assert (top == (level == 3)).all()
+    bound = mean_bound(c, top)
+    for e in (8, 22, 23, 25, 26, 28, 33, 100):
+        scale = sign * float(np.float32(0.7 * 2.0 ** e / 576))
+        o, lse = u.run(fd, c, scale, num_ctas=ctas, k_scale=1.0, v_scale=1.0)
+        ref, ref_lse, _, _ = u.attention(c["q64"], c["k64"], c["v64"], c["lens"], 0, 0, scale)
+        # 576 dims' products are exact; the scale in log2 units, the product, the reference and ln 2: 2^-24 each, twice over
+        assert (np.abs(lse.double().cpu().numpy() - ref_lse) <= 2.0 ** -20 + np.abs(ref_lse) * 2.0 ** -21).all(), e
+        assert (np.abs(o.double().cpu().numpy() - ref) <= bound).all(), e
