@@ -30,6 +30,7 @@ __all__ = ["Cache4", "make_cache4", "fd_cache_write4", "fd_cache_read4", "fd_dec
 
 _U8 = torch.uint8
 _SCALES = (torch.float8_e4m3fn, torch.uint8)
+_INT = 1 << 31
 
 
 class Cache4(NamedTuple):
@@ -155,8 +156,8 @@ def make_window_workspace(batch, num_q_heads, num_kv_heads, head_dim=128, device
 def _attend(name, call, q, gpu, cache, pages, page, hkv, table, seq_lens, window, sinks, seq_lens_host, scale, out, lse,
             workspace, num_ctas, split_events, check, kv, k_scale, v_scale):
     """Any cache: checks, outputs, and the call `name`; `cache`: its arguments in that call."""
-    if window >> 31 > 0 or sinks >> 31 > 0:
-        raise ValueError(f"window and sinks must be below 2^31, got {window} and {sinks}")
+    if not (-_INT <= window < _INT and -_INT <= sinks < _INT):   # ctypes would pass their low 32 bits
+        raise ValueError(f"window and sinks must be below 2^31 in magnitude, got {window} and {sinks}")
     shape, dt = q.shape, q.dtype
     if len(shape) == 4:
         B, T, hq, d = shape
