@@ -16,6 +16,7 @@ kept to a few attribute reads a tensor.
 """
 from __future__ import annotations
 
+import ctypes
 import functools
 import math
 from typing import NamedTuple
@@ -63,9 +64,20 @@ def _call(gpu, f, *args):
         return f(*args, _raw_stream(gpu))
 
 
+def _held(num_ctas, *scales):
+    """Refuses what the options' C types do not hold: ctypes would pass num_ctas's low 32 bits, and a scale below fp32's
+    least number as 0, which stands for 1."""
+    if not -_INT <= num_ctas < _INT:
+        raise ValueError(f"num_ctas must be below 2^31 in magnitude, got {num_ctas}")
+    for x in scales:
+        if x != 0 and ctypes.c_float(x).value == 0:
+            raise ValueError(f"a scale of {x} is 0 in fp32")
+
+
 @functools.lru_cache(maxsize=256)
 def _opts(num_ctas, dtype, kv, k_scale, v_scale, q_len):
     """The options of these values; the library only reads them."""
+    _held(num_ctas, k_scale, v_scale)
     return FdOptions(num_ctas, 0, 0, None, None, dtype, kv, k_scale, v_scale, q_len)
 
 
@@ -139,7 +151,10 @@ def fd_cache_read4(slot_map, cache, dtype=_BF16, k_out=None, v_out=None, k_scale
 
 
 def fd_window_workspace_size(batch, num_q_heads, num_kv_heads, head_dim=128, q_len=1) -> int:
-    return int(_lib.fd_window_workspace_size(batch, num_q_heads, num_kv_heads, head_dim, q_len))
+    shape = (batch, num_q_heads, num_kv_heads, head_dim, q_len)
+    if not all(0 <= x < _INT for x in shape):   # ctypes would pass their low 32 bits
+        return 0
+    return int(_lib.fd_window_workspace_size(*shape))
 
 
 def make_window_workspace(batch, num_q_heads, num_kv_heads, head_dim=128, device="cuda", q_len=1) -> torch.Tensor:
@@ -197,6 +212,7 @@ def _attend(name, call, q, gpu, cache, pages, page, hkv, table, seq_lens, window
     if split_events is None:
         opts = _opts(num_ctas, f16, kv, float(k_scale), float(v_scale), T)
     else:
+        _held(num_ctas, k_scale, v_scale)
         opts = _options(num_ctas, 0, 0, split_events, f16, kv, k_scale, v_scale, T)
     st = _call(gpu, call, q.data_ptr(), *cache, *layout, None if seq_lens is None else _ptr_of(seq_lens, "seq_lens", _I32, (B,), gpu),
                None if host is None else host.data_ptr(), B, hq, hkv, d, *cap, window, sinks,

@@ -38,3 +38,34 @@ def test_other_negative_windows_are_the_library_s_to_refuse(fd, monkeypatch, win
     assert (window, sinks) in zip(a, a[1:])
     a = attend(fd, monkeypatch, 2 ** 31 - 1, 2 ** 31 - 1)
     assert (2 ** 31 - 1,) * 2 in zip(a, a[1:])
+
+
+class Event:
+    cuda_event = 1
+
+
+@pytest.mark.parametrize("events", [None, (Event(), Event())])
+@pytest.mark.parametrize("bad", [dict(num_ctas=2 ** 32 + 7), dict(num_ctas=2 ** 32), dict(num_ctas=-2 ** 32 + 7), dict(k_scale=1e-46),
+                                 dict(v_scale=1e-46), dict(k_scale=-1e-46)])
+def test_options_that_the_library_would_read_as_others(fd, monkeypatch, events, bad):
+    """2^32 + 7 CTAs as 7, and a scale that fp32 does not hold as 0, which stands for 1."""
+    with pytest.raises(ValueError):
+        attend(fd, monkeypatch, split_events=events, **bad)
+    for good in (dict(k_scale=1e-45), dict(v_scale=0.0), dict(num_ctas=160)):   # 1e-45: fp32's least number
+        attend(fd, monkeypatch, split_events=events, **good)
+
+
+def test_row_scales_that_fp32_does_not_hold(fd, monkeypatch):
+    from decode_attention_decoding_gb300 import longcontext
+    with pytest.raises(ValueError):
+        longcontext._opts(0, 0, 0, 1e-50, 1.0, 1)
+    with pytest.raises(ValueError):
+        longcontext._opts(0, 0, 0, 1.0, 1e-50, 1)
+
+
+@pytest.mark.parametrize("shape", [(2 ** 32 + 1, 8, 8, 128, 1), (1, 2 ** 32 + 8, 8, 128, 1), (1, 8, 2 ** 32 + 8, 128, 1),
+                                   (1, 8, 8, 2 ** 32 + 128, 1), (1, 8, 8, 128, 2 ** 32 + 1), (-2 ** 32 + 1, 8, 8, 128, 1)])
+def test_workspaces_of_shapes_that_no_call_accepts(fd, shape):
+    assert fd.fd_window_workspace_size(*shape) == 0
+    with pytest.raises(fd.FdError):
+        fd.make_window_workspace(*shape[:4], q_len=shape[4])
