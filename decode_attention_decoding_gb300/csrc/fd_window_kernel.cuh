@@ -596,18 +596,21 @@ struct WindowWarp {
         constexpr uint32_t kStep = C::kFp4 || KV == kKvE4m3 ? 0x01010101u : KV == kKvE5m2 ? 0x04040404u : KV == kKvF16 ? 0x04000400u : 0x00800080u;
         return ((w & kExp) + kStep) & kTop;
     }
-    // Whether some sum is NaN (a type without infinities has NaN only beside NaN).
+    // Whether some sum is NaN (a type without infinities has NaN only beside NaN) of a column whose weights are numbers.
     __device__ __forceinline__ bool broken() const
     {
         bool any = false;
         if constexpr (C::kInf) {
 #pragma unroll
-            for (int s = 0; s < kSteps; ++s)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int e = 0; e < 2; ++e) {
+                    bool nan = false;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        any = any || acc[s][nt][e] != acc[s][nt][e];
+                    for (int s = 0; s < kSteps; ++s)
+                        nan = nan || acc[s][nt][e] != acc[s][nt][e] || acc[s][nt][e + 2] != acc[s][nt][e + 2];
+                    any = any || (nan && l[nt][e] == l[nt][e]);
+                }
         }
         return any;
     }
@@ -669,8 +672,8 @@ __device__ __forceinline__ float window_element(const WindowParams &p, const Win
 }
 // An infinite V element times a weight's part that is 0 or less than 0 is NaN, and in tiles that are seen in part V's
 // elements that are not finite were left out.  Here a warp looks for them in rows [from, to) of a request, whose sums (or
-// output, base null) it has just written, and adds those that a token sees to its columns with a bit in `ok`: what else
-// was summed there does not matter.
+// output, base null) it has just written, and adds those that a token sees to its columns with a bit in `ok` (columns whose
+// weights are numbers; 0: there is nothing to do): what else was summed there does not matter.
 template <class C>
 __device__ __noinline__ void window_repair(const WindowParams &p, int b, int head, int from, int to, uint32_t ok, float *base)
 {
@@ -678,30 +681,47 @@ __device__ __noinline__ void window_repair(const WindowParams &p, int b, int hea
     const int lane = threadIdx.x & 31;
     const WindowReq req = window_req(p, b, nullptr);
     __syncwarp();
-#pragma unroll 1
-    for (int i = 0; i < p.q_len; ++i) {
-        const WindowSight sight(p, req, i);
-        float sum[kMine];
+    uint32_t found[kMine];   // of the lane's dims: bit i, token i sees infinity or NaN; bit 16 + i, -infinity or NaN
 #pragma unroll
-        for (int e = 0; e < kMine; ++e)
-            sum[e] = 0.f;
+    for (int e = 0; e < kMine; ++e)
+        found[e] = 0;
 #pragma unroll 4
-        for (int v = from; v < to; ++v)
-            if (sight.sees(v))
+    for (int v = from; v < to; ++v) {
+        float x[kMine];
+        bool any = false;
 #pragma unroll
-                for (int e = 0; e < kMine; ++e) {
-                    const float x = window_element<C>(p, req, b, head, v, lane + 32 * e);
-                    sum[e] += fabsf(x) < __builtin_huge_valf() ? 0.f : x;
-                }
+        for (int e = 0; e < kMine; ++e) {
+            x[e] = window_element<C>(p, req, b, head, v, lane + 32 * e);
+            any = any || !(fabsf(x[e]) < __builtin_huge_valf());
+        }
+        if (any) {
+            uint32_t who = 0;
 #pragma unroll 1
-        for (int col = i * p.group; col < (i + 1) * p.group; ++col)
-            if (ok >> col & 1)
+            for (int i = 0; i < p.q_len; ++i)
+                who |= WindowSight(p, req, i).sees(v) ? 1u << i : 0u;
 #pragma unroll
-                for (int e = 0; e < kMine; ++e) {
-                    float *at = (base ? base + col * D : p.o + window_out_row(p, b, head, col) * D) + lane + 32 * e;
-                    if (sum[e] != 0.f)
-                        *at = *at != *at ? sum[e] : *at + sum[e];
-                }
+            for (int e = 0; e < kMine; ++e) {
+                if (fabsf(x[e]) < __builtin_huge_valf())
+                    continue;
+                found[e] |= x[e] < 0.f ? 0u : who;           // NaN: both
+                found[e] |= x[e] > 0.f ? 0u : who << 16;
+            }
+        }
+    }
+#pragma unroll 1
+    for (int col = 0; col < p.cols; ++col) {
+        if (!(ok >> col & 1))
+            continue;
+        const int i = col / p.group;
+#pragma unroll
+        for (int e = 0; e < kMine; ++e) {
+            float *at = (base ? base + col * D : p.o + window_out_row(p, b, head, col) * D) + lane + 32 * e;
+            const bool plus = found[e] >> i & 1, minus = found[e] >> (16 + i) & 1;
+            if (plus || minus) {
+                const float x = (plus ? __builtin_huge_valf() : 0.f) - (minus ? __builtin_huge_valf() : 0.f);
+                *at = *at != *at ? x : *at + x;
+            }
+        }
     }
 }
 // LSE from the reference exponent (log2) and the sum of weights.
@@ -1164,8 +1184,11 @@ __global__ void __launch_bounds__(32 * C::kWarps, 1) window_kernel(const __grid_
                         *reinterpret_cast<float4 *>(dst + Warp::block_dim(s, g)) =
                             make_float4(w.acc[s][nt][e] * f, w.acc[s][nt][e + 2] * f, w.acc[s + 1][nt][e] * f, w.acc[s + 1][nt][e + 2] * f);
                 }
-            if (__any_sync(0xffffffffu, dirty || w.broken()))
-                window_repair<C>(p, b, head, from, row0 + (flags >> kTileN), __reduce_or_sync(0xffffffffu, ok), sums);
+            if (__any_sync(0xffffffffu, dirty || w.broken())) {
+                ok = __reduce_or_sync(0xffffffffu, ok) & ((1u << p.cols) - 1);
+                if (ok)
+                    window_repair<C>(p, b, head, from, row0 + (flags >> kTileN), ok, sums);
+            }
             seg = -1;
         }
     }

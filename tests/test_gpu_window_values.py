@@ -121,3 +121,37 @@ def test_large_scores(fd, kv, hq, T, L, ctas, sign):
         # 576 dims' products are exact; the scale in log2 units, the product, the reference and ln 2: 2^-24 each, twice over
         assert (np.abs(lse.double().cpu().numpy() - ref_lse) <= 2.0 ** -20 + np.abs(ref_lse) * 2.0 ** -21).all(), e
         assert (np.abs(o.double().cpu().numpy() - ref) <= bound).all(), e
+
+
+def test_one_request_s_not_a_numbers_do_not_hold_up_the_others(fd):
+    """Columns whose weights are NaN are NaN whatever V holds, so nothing is looked for in their rows; and infinities are
+    looked for once, not for each new token.  Measured: 1.0 times a clean call and 10, before 10.5 and 147; the limits of 3
+    and 40 lie between."""
+    B, L = 64, 8192
+    k, v = (torch.randn(B, L, 1, 128, device="cuda").bfloat16() for _ in range(2))
+    ws = fd.make_window_workspace(B, 16, 1, 128)
+
+    def time(q):
+        out, lse = torch.empty(q.shape, device="cuda"), torch.empty(q.shape[:-1], device="cuda")
+        times = []
+        for _ in range(6):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            for _ in range(3):
+                fd.fd_window_decode(q, k, v, None, L, out=out, lse=lse, workspace=ws)
+            b.record()
+            b.synchronize()
+            times.append(a.elapsed_time(b))
+        return min(times), out
+
+    q = torch.randn(B, 16, 1, 128, device="cuda").bfloat16()
+    one = torch.randn(B, 8, 128, device="cuda").bfloat16()
+    clean, clean_one = time(q)[0], time(one)[0]
+    one[5, :, 3] = math.nan
+    t, o = time(one)
+    assert bool(o[5].isnan().all()) and bool(o[:5].isfinite().all()) and bool(o[6:].isfinite().all())
+    assert t <= 3 * clean_one
+    v[:, ::1000, 0, 7] = math.inf
+    t, o = time(q)
+    assert bool((o[..., 7] == math.inf).all()) and bool(o[..., 8:].isfinite().all())
+    assert t <= 40 * clean
