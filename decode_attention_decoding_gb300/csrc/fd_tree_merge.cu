@@ -15,6 +15,27 @@ constexpr int kMergeScanBatch = 32; // requests whose positions every warp finds
 __host__ __device__ constexpr int merge_cols(int d) { return d == 256 ? 4 : 2; }
 __host__ __device__ constexpr int merge_warps(int d) { return d / 4 / merge_cols(d); }
 
+// A sum of the outputs of CTAs c0 .. c1 that has become NaN where an infinite one has a weight that fp32 does not hold: it is
+// what the infinite ones (and NaN) come to.  (A least weight of 2^-126 in place of 0 would also keep 2^-14 of finite
+// outputs of 2^112.)
+static __device__ __noinline__ float4 tree_merge_infinities(float4 sum, const float *lse, const float *out, int slot_rows, int d, int c0, int c1)
+{
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int c = c0; c <= c1; ++c) {
+        const int slot = 2 * c + (c == c0 ? 1 : 0);
+        if (lse[slot * slot_rows] == -__builtin_huge_valf())
+            continue;   // wrote nothing
+        const float4 o = *reinterpret_cast<const float4 *>(out + (long long)slot * d * slot_rows);
+        s.x += fabsf(o.x) < __builtin_huge_valf() ? 0.f : o.x;
+        s.y += fabsf(o.y) < __builtin_huge_valf() ? 0.f : o.y;
+        s.z += fabsf(o.z) < __builtin_huge_valf() ? 0.f : o.z;
+        s.w += fabsf(o.w) < __builtin_huge_valf() ? 0.f : o.w;
+    }
+    return make_float4(sum.x == sum.x || s.x == 0.f ? sum.x : s.x, sum.y == sum.y || s.y == 0.f ? sum.y : s.y,
+                       sum.z == sum.z || s.z == 0.f ? sum.z : s.z, sum.w == sum.w || s.w == 0.f ? sum.w : s.w);
+}
+
 // grid: (kv head x row group x 32 rows, request).  Partials are laid out
 // [D / 4][row][4], so that a warp (32 rows of one 4-dim column) reads 512
 // consecutive bytes; the rows are turned round in shared memory for the write.
@@ -93,10 +114,7 @@ __global__ void __launch_bounds__(32 * merge_warps(D)) tree_merge_kernel(const _
 #pragma unroll
                 for (int n = 0; n < kTogether; ++n)
                     higher = fmaxf(higher, x[n]);
-                // at least fp32's least normal number: an infinite sum stays infinite however small
-                // its weight is, and 10^-38 of a finite one does not matter
-                auto weight = [](float y) { return y < -126.f ? 1.1754944e-38f : exp2_approx(y); };   // NaN: NaN
-                const float ref = higher == kNegInf ? 0.f : higher, down = weight(top - ref);
+                const float ref = higher == kNegInf ? 0.f : higher, down = exp2_approx(top - ref);
                 sum *= down;
 #pragma unroll
                 for (int k = 0; k < kCols; ++k)
@@ -106,7 +124,7 @@ __global__ void __launch_bounds__(32 * merge_warps(D)) tree_merge_kernel(const _
                 for (int n = 0; n < kTogether; ++n) {
                     if (x[n] == kNegInf)
                         continue;   // no partial, or one that saw nothing and wrote nothing
-                    const float w = weight(x[n] - ref);
+                    const float w = exp2_approx(x[n] - ref);
                     sum += w;
 #pragma unroll
                     for (int k = 0; k < kCols; ++k) {
@@ -117,6 +135,15 @@ __global__ void __launch_bounds__(32 * merge_warps(D)) tree_merge_kernel(const _
                     }
                 }
             }
+            float any = 0.f;   // NaN if a sum is, or needlessly
+#pragma unroll
+            for (int k = 0; k < kCols; ++k)
+                any += (acc[k].x + acc[k].y) + (acc[k].z + acc[k].w);
+            if (any != any)
+#pragma unroll
+                for (int k = 0; k < kCols; ++k)
+                    acc[k] = tree_merge_infinities(acc[k], p.ws_lse + srow, p.ws_o + (((long long)warp * kCols + k) * p.slot_rows + srow) * 4,
+                                                   p.slot_rows, D, c0, c1);
             if (sum != 0.f) {   // true for NaN
                 const float inv = 1.f / sum;
 #pragma unroll
