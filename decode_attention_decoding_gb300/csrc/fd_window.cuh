@@ -55,7 +55,9 @@ struct WindowCfg {
     // 134; 256 dims: 16 x 8 99 / 114 / 163, 32 x 8 85 / 102 / 151 (no room with 16 columns); FP8, 64 dims: 32 x 12
     // 73 / 78 / 95, 64 x 8 71 / 75 / 96; 128 dims: 16 x 8 86 / 91 / 106, 32 x 8 67 / 74 / 93, 64 x 4 69 / 82 / 126; 256
     // dims: 16 x 8 67 / 78 / 101, 32 x 4 69 / 85 / 123; 16 bits, 64 dims: 16 x 8 86 / 87 / 93, 32 x 8 69 / 70 / 76, 64 x 4
-    // 71 / 74 / 85; 128 dims: 16 x 8 68 / 71 / 77, 32 x 4 69 / 72 / 85.  The floor is 59.
+    // 71 / 74 / 85; 128 dims: 16 x 8 68 / 71 / 77, 32 x 4 69 / 72 / 85.  The floor is 59.  The shapes taken, since weights
+    // come from differences of scores: 4 bits 94 / 102 / 149, 86 / 92 / 132, 82 / 98 / 164, FP8 69 / 73 / 101, 68 / 72 / 93,
+    // 67 / 72 / 100, 16 bits 67 / 68 / 75, 66 / 68 / 74, 66 / 77 / 104 (64, 128, 256 dims).
     static constexpr int kTile = kFp4   ? (D < 256 ? 64 : NT == 1 ? 32 : 16)
                                  : kFp8 ? (D == 64 ? (NT == 1 ? 64 : 32) : D == 128 ? 32 : 16)
                                         : (D == 64 ? 32 : 16);

@@ -23,18 +23,25 @@
 // m that only rises, l = sum 2^(x_t - m), O = sum 2^(x_t - m) v_t / l, LSE =
 // (m + log2 l) ln 2; sums of two warps with references m, m' join after
 // factors of 2^(m - max), 2^(m' - max).  A weight is two fp16 or three bf16
-// parts, so that it is off by 2^-22 of itself at most; up to four fp16 columns
-// have both parts as columns of one MMA.
+// parts, so that it is off by 2^-22 of itself at most, of fp16 parts by 2^-39
+// of the reference's weight where that is more (a weight's remainder ends at
+// half of fp16's least step, 2^-25, and the reference's weight is 2^14); up to
+// four fp16 columns have both parts as columns of one MMA.
 //
 // What bounds it (GB300, contexts of hundreds of MB): 16-bit and FP8 caches
 // memory: 64 requests of GQA-4 and a window of 4096 in bf16 162 us = 6.5 TB/s,
-// 96% of a copy; E4M3 314 us = 96%.  4-bit caches the warps' arithmetic: 604
-// MB in 121 us = 5.0 TB/s, 74%, the same with the pages in L2, and 96 us for
-// the loads alone.  An MMA of 2048 products a scheduler takes 8 cycles, each
-// conversion or multiplication of a code pair 2, and HMUL2 shares the MMAs'
-// pipe: 14.3 cycles for the MMA with its four pairs.  Not tcgen05: its
-// operands come from shared memory, so each code would have to be written
-// there as 16 bits and read again, for 4 to 16 columns of its 128 rows.
+// 96% of a copy; E4M3 314 us = 96%.  9 to 16 columns over FP8 caches are not
+// there (400 MB, 128 dims: 93 us of 59): two MMAs for each converted operand.
+// 4-bit caches the warps' arithmetic: 604 MB in 122 us = 4.9 TB/s, 73%, the
+// same with the pages in L2, and 96 us for the loads alone.  An MMA of 2048
+// products a scheduler takes 8 cycles, each conversion or multiplication of a
+// code pair 2, and HMUL2 shares the MMAs' pipe: 14.3 cycles for the MMA with
+// its four pairs.  V does not go to tcgen05: the scales of its blocks run along
+// the output's dims, not along the sum, so each code would have to be written
+// to shared memory in 16 bits and read again, for 1 to 16 columns of 128 rows.
+// K's codes and scales as they lie are operands of tcgen05's block-scaled FP4
+// MMAs (16 elements a scale, along the sum), with the query in several 4-bit
+// parts; that has been neither built nor measured.
 #pragma once
 
 #include <atomic>

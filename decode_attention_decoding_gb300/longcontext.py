@@ -12,7 +12,9 @@ tensors live on one GPU, outputs are allocated unless they are given.  A call
 runs on that GPU's current stream, whatever device is current, or on the
 stream given as `stream=`, one of that GPU, which then owns what the call
 allocates.  Short calls take less time on the GPU than here, so the checks are
-kept to a few attribute reads a tensor.
+kept to a few attribute reads a tensor; a program keeps a workspace
+(make_window_workspace) and gives it to its calls, which otherwise allocate and
+zero one each.
 """
 from __future__ import annotations
 

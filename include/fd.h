@@ -622,6 +622,9 @@ fd_status fd_tree_decode_paged(const void *q, const void *k_pages, const void *v
  * counterpart to these calls; the arithmetic of the attention is fd_decode's.
  * They follow the conventions at the top of this file, and may be captured and
  * replayed.
+ * What they do not go with: fd_tree_decode, fd_cache_compact and fd_decode's
+ * partial forms (fd_decode_partial) do not take a 4-bit cache, and neither a
+ * window nor a 4-bit cache has a partial form for sequence sharding.
  */
 
 /*
@@ -707,9 +710,13 @@ size_t fd_window_workspace_size(int batch, int num_q_heads, int num_kv_heads, in
  * (64 requests, window 4096, bf16: GQA-4 with 1 and 4 new tokens 170 -> 1910 and
  * 195 -> 1950 us, 16 new tokens of one query head a kv head 200 -> 1960).
  * Head groups, q_len, head_dim and batch as for fd_decode: G * q_len <= 16, but
- * any of them with any cache.  Rows of the cache (positions x kv heads) are
- * limited to 2^32 - 2, and num_kv_heads * batch * (visible positions / 16 + 2)
- * to 2^31 (FD_ERR_UNSUPPORTED).  Results are bitwise the same from call to call
+ * any of them with any cache.  A call's limits go by its capacity (s_max, or
+ * max_blocks_per_seq * page_size), whatever the lengths: it is below 2^31;
+ * num_kv_heads * batch * (n / 16 + 2) is below 2^31, n the capacity or, where
+ * that is less, window + sinks + q_len; and the rows of the cache (positions x
+ * kv heads, those of all pages) are at most 2^32 - 2 (FD_ERR_UNSUPPORTED; a
+ * wide table of many requests may be cut to the blocks in use).  Results are
+ * bitwise the same from call to call
  * (with the same num_ctas).  The first call of a shape on a device sets a kernel
  * attribute: make it before a capture.
  */
