@@ -608,15 +608,16 @@ struct WindowWarp {
     {
         bool any = false;
         if constexpr (C::kInf) {
+            // a sum of them is NaN if one of them is (or needlessly)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    bool nan = false;
+                    float x = 0.f;
 #pragma unroll
                     for (int s = 0; s < kSteps; ++s)
-                        nan = nan || acc[s][nt][e] != acc[s][nt][e] || acc[s][nt][e + 2] != acc[s][nt][e + 2];
-                    any = any || (nan && l[nt][e] == l[nt][e]);
+                        x += acc[s][nt][e] + acc[s][nt][e + 2];
+                    any = any || (x != x && l[nt][e] == l[nt][e]);
                 }
         }
         return any;
